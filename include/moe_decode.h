@@ -300,6 +300,136 @@ int mtp_eh_front(const int32_t *input_ids, const void *embed, int vocab, const v
                  const void *enorm, const void *hnorm, float eps, const void *eh_proj_w, int M, int H,
                  void *out, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The attention sublayer of a decode step: FP8 block-scaled projections, an FP8
+ * paged key/value cache, and attention of the step's tokens over it.  No
+ * counterpart on the source pages, whose executors leave attention to the
+ * stock forward; the weight and activation formats are those of the expert
+ * layers above.
+ *
+ * Workspaces.  Each call takes a workspace of its *_workspace_size, zeroed once
+ * by moe_workspace_init.  It starts with the status word (moe_device_status)
+ * and the counters of split work; every call leaves the counters at zero, so
+ * one workspace of the largest size may serve all of these calls in stream
+ * order.  After a call returned an error, or moe_device_status reported
+ * MOE_ERR_DEVICE_TIMEOUT, it has to be zeroed again.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Activation quantisation: per row and per group of 128 columns (the last may
+ * be shorter), s = amax / 448 in fp32 (rounded up to a power of two when e8m0;
+ * 1 for an all-zero group) and codes = E4M3(x / s), the quotient in fp32,
+ * rounded to nearest even and saturating.
+ *   x       bf16 [M, K], rows x_stride elements apart (x_stride >= K, % 8 == 0)
+ *   codes   fp8 [M, K];  scales fp32 [M, ceil(K / 128)]
+ * K % 16 == 0, K <= 131072, M <= 2^20; x and codes 16-byte aligned.  M == 0 is
+ * a no-op.  One kernel.
+ */
+int fp8_quant_rows(const void *x, long long x_stride, int M, int K, int e8m0, uint8_t *codes, float *scales,
+                   void *stream);
+
+/*
+ * out[m, n] = sum_kb scales[m, kb] * w_s[n / 128, kb] *
+ *             sum_{k in block kb} codes[m, k] * w[n, k]      (fp32 sums)
+ *   codes, scales  as fp8_quant_rows writes them
+ *   w     fp8 [N, K];  w_s fp32 [ceil(N / 128), ceil(K / 128)]
+ *   out   bf16 [M, N], rounded once (out_fp32 == 0), or fp32 [M, N]
+ * K % 16 == 0, K <= 131072, any N <= 2^20, M <= 2^20; codes, w, out and the
+ * workspace 16-byte aligned.  M == 0 is a no-op.  One kernel; results do not
+ * depend on the order in which CTAs finish.
+ */
+int fp8_block_gemm_workspace_size(int M, int N, int K, size_t *bytes);
+int fp8_block_gemm(const uint8_t *codes, const float *scales, const uint8_t *w, const float *w_s, int M, int N, int K,
+                   void *out, int out_fp32, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The linear layer out = x . w^T: fp8_quant_rows into the workspace, then
+ * fp8_block_gemm, launched so that it streams its first weights while the
+ * quantisation still runs.  Arguments and limits as theirs.  Two kernels.
+ */
+int fp8_linear_workspace_size(int M, int N, int K, size_t *bytes);
+int fp8_linear(const void *x, long long x_stride, const uint8_t *w, const float *w_s, int M, int N, int K, int e8m0,
+               void *out, int out_fp32, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * A paged key/value cache in FP8.  A block is a page of one key/value head:
+ * page_size tokens whose codes share one fp32 scale (value = code * scale).
+ *   k, v              fp8 [num_pages, kv_heads, page_size, head_dim]
+ *   k_scale, v_scale  fp32 [num_pages, kv_heads]
+ * page_size 16, 32, 64 or 128; head_dim 64 or 128; kv_heads <= 1024; k and v
+ * 16-byte aligned.  Nothing needs to be initialised: what a block held before
+ * its first slot is written does not matter.
+ *
+ * The batch of a step, shared by the two calls below (device arrays):
+ *   page_table  int32 [B, width]: page of each page_size tokens of a sequence;
+ *               entries past a sequence's length are not read
+ *   q_start     int32 [B + 1]: rows [q_start[b], q_start[b + 1]) of the step's
+ *               `total` tokens are sequence b's newest ones (a sequence may
+ *               have none)
+ *   lens        int32 [B]: tokens of each sequence, the new ones included
+ *   max_new     host bound of the new tokens of any sequence
+ * Values that do not fit (a page outside [0, num_pages), rows outside
+ * [0, total], a length above width * page_size) set the status word to
+ * MOE_ERR_INVALID_ARG; nothing outside the arrays is read or written.
+ * width * page_size <= 2^30, B <= 2^20, total <= 2^24.
+ */
+typedef struct moe_kv_cache {
+  uint8_t *k;
+  uint8_t *v;
+  float *k_scale;
+  float *v_scale;
+  int num_pages;
+  int kv_heads;
+  int page_size;
+  int head_dim;
+} moe_kv_cache;
+
+/*
+ * Write the new tokens' keys and values (bf16 [total, kv_heads, head_dim],
+ * tokens k_stride / v_stride elements apart, multiples of 8, so slices of a
+ * fused projection do; 16-byte aligned) at their positions lens[b] - n_b + i.
+ * A block's scale is the power of two at or above amax / 448 over the tokens
+ * written to it, at least 2^-126, and never shrinks while the block fills:
+ * when it grows, the codes that the block holds are rewritten in the new scale
+ * (exact except where a code becomes subnormal: nearest even).  A call that
+ * writes a block's first slot starts its scale anew.  Infinities do not set
+ * a scale (they saturate), NaN stays NaN.  A sequence with bad values is left
+ * out; where only a page is out of range, that block is.  A page may belong to
+ * two sequences only where neither writes it.  One kernel.
+ */
+int kv_cache_workspace_size(size_t *bytes);
+int kv_cache_append(const moe_kv_cache *cache, const void *k, long long k_stride, const void *v, long long v_stride,
+                    const int32_t *page_table, int width, const int32_t *q_start, const int32_t *lens, int B, int total,
+                    int max_new, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of the step's tokens over the cache (their own keys and values
+ * written before): for token i of sequence b, at position
+ * pos = lens[b] - n_b + i, and query head h with kv head h / (heads / kv_heads):
+ *   s_j = sm_scale * q . k_j;  if softcap > 0: s_j = softcap * tanh(s_j / softcap);
+ *   if slopes: s_j += slopes[h] * (j - pos)
+ *   over j <= pos, j < lens[b] and, if window > 0, j > pos - window:
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j);  lse = log sum_j exp(s_j).
+ * A row that sees no token gives zeros and lse = -inf.  Tokens of a page
+ * outside [0, num_pages) are masked.
+ *   q      bf16 [total, heads, head_dim], tokens q_stride elements apart
+ *          (% 8 == 0), 16-byte aligned; heads % kv_heads == 0, heads <= 4096
+ *   out    bf16 [total, heads, head_dim];  lse fp32 [total, heads] or NULL
+ *   slopes fp32 [heads] or NULL
+ * Scores, statistics and sums are fp32; the weights are rounded to 11 bits for
+ * their product with V.  V scales of one sequence and head may differ by up to
+ * 2^29 before weights lose bits.  An infinity or a NaN in a row of q makes the
+ * row NaN; a NaN in a new token's v reaches every row of its sequence's step.
+ * One kernel; results do not depend on the order in which CTAs finish.
+ */
+int decode_attention_workspace_size(int heads, int kv_heads, int head_dim, int max_new, size_t *bytes);
+int decode_attention(const moe_kv_cache *cache, const void *q, long long q_stride, int heads,
+                     const int32_t *page_table, int width, const int32_t *q_start, const int32_t *lens, int B, int total,
+                     int max_new, float sm_scale, float softcap, int window, const float *slopes, void *out, float *lse,
+                     void *ws, size_t ws_bytes, void *stream);
+
 /* Expert kernels (moe_decode_layer_plan, moe_set_expert_path). */
 enum moe_expert_path {
   MOE_PATH_AUTO = 0,      /* the library's choice by layer kind and token count */
@@ -319,9 +449,9 @@ int moe_decode_layer_plan(const moe_layer_dims *dims, int M, int *path, int *lau
  * from other host threads. */
 int moe_set_expert_path(int path);
 
-/* Read and clear the device status word of a moe_decode_layer workspace:
- * MOE_OK, or MOE_ERR_DEVICE_TIMEOUT when a bounded wait inside the expert
- * kernel gave up.  Synchronises `stream`; meant for tests and diagnostics. */
+/* Read and clear the device status word of a workspace: MOE_OK,
+ * MOE_ERR_DEVICE_TIMEOUT when a bounded wait inside a kernel gave up, or
+ * MOE_ERR_INVALID_ARG when a kernel met a token id, page or length out of range.  Synchronises `stream`; meant for tests and diagnostics. */
 int moe_device_status(void *ws, void *stream);
 
 /* Test hook: nonzero `fault` makes the next moe_decode_layer calls on this

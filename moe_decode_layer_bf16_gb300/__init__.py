@@ -9,7 +9,10 @@ Entry points (same names as the C ABI):
   moe_decode_workspace_size, moe_workspace_init, moe_decode_layer,
   splitk_gemm_workspace_size, splitk_gemm_bf16, rmsnorm_residual,
   moe_device_status, moe_debug_set_fault, moe_status_str
-plus MoeDecodeLayer, a holder of one layer's weights and workspace.
+plus MoeDecodeLayer, a holder of one layer's weights and workspace, and, from
+the attention module,
+  fp8_quant_rows, fp8_block_gemm, fp8_linear, kv_cache_append, decode_attention
+(with their *_workspace_size).
 """
 
 from __future__ import annotations
@@ -95,6 +98,8 @@ def lib() -> ctypes.CDLL:
                   "moe_decode_layer_plan", "moe_set_expert_path", "moe_decode_layer_partial", "moe_tp_boundary",
                   "mtp_eh_front_workspace_size", "mtp_eh_front"):
             getattr(L, n).restype = ctypes.c_int
+        from . import attention
+        attention.bind(L)
         _lib = L
     return _lib
 
@@ -310,3 +315,8 @@ class MoeDecodeLayer:
 
     def status(self) -> int:
         return moe_device_status(self.workspace)
+
+
+from .attention import (decode_attention, decode_attention_workspace_size, fp8_block_gemm,  # noqa: E402
+                        fp8_block_gemm_workspace_size, fp8_linear, fp8_linear_workspace_size, fp8_quant_rows,
+                        kv_cache_append, kv_cache_workspace_size)

@@ -191,6 +191,83 @@ struct EhNormArgs {
 };
 cudaError_t launch_eh_norm(const EhNormArgs& a, cudaStream_t s);
 
+// FP8 block-scaled linear layer (fp8_linear.cu).
+struct QuantArgs {
+  const void* x;  // bf16 [M, K], row stride ldx elements
+  long long ldx;
+  int M, K, nkb, e8m0;
+  uint8_t* codes;  // [M, K]
+  float* scales;   // [M, nkb]
+};
+cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s);
+
+constexpr int kLinMaxCtas = 160;  // CTAs of the product at most (one per SM)
+constexpr int kLinMinRun = 2;     // k-blocks of a CTA's share of the split pairs at least
+struct LinPlan {
+  int M, N, K, nkb;
+  int nt;             // the kernel's token columns: 16, 32, 64, 128 or 256
+  int chunk;          // tokens of a chunk (<= nt)
+  int n_chunks, n_tiles;
+  int G;              // CTAs
+  int waves;          // whole (row tile, chunk) pairs of each CTA
+  int G_split;        // CTAs that share the cells of the remaining pairs
+  long long split_cells;
+};
+struct LinArgs {
+  const float* xs;   // [M, nkb]
+  const float* w_s;  // [ceil(N / 128), nkb]
+  void* out;
+  int out_fp32;
+  int M, N, nkb, chunk, n_tiles, G, waves, G_split;
+  long long split_cells;
+  int* status;
+  int* tickets;      // [G], zero between calls
+  float* partials;   // [G_split][2][nt][128]
+};
+void plan_linear(LinPlan& p, int M, int N, int K, int sms);
+size_t linear_partial_bytes(const LinPlan& p);
+// pdl: the codes and scales come from the kernel just enqueued, a
+// launch_quant_rows; w and w_s do not
+cudaError_t launch_linear(const LinPlan& p, const uint8_t* xq, const float* xs, const uint8_t* w, const float* w_s,
+                          void* out, int out_fp32, int* status, int* tickets, float* partials, bool pdl,
+                          cudaStream_t s);
+
+// The FP8 paged cache: writing new tokens (kv_append.cu) and attention over it
+// (attention.cu).  Caches [num_pages][kv_heads][page_size][head_dim] codes,
+// scales [num_pages][kv_heads], page_table [B][width], q_start [B + 1], lens [B].
+struct AppendArgs {
+  const void* k; const void* v;  // bf16 [total][kv_heads][head_dim], token strides in elements
+  long long k_stride, v_stride;
+  uint8_t* k_cache; uint8_t* v_cache;
+  float* k_scale; float* v_scale;
+  const int32_t* page_table; const int32_t* q_start; const int32_t* lens;
+  int num_pages, kv_heads, page_size, head_dim, width, B, total, max_new;
+  int blocks;  // blocks a sequence's new tokens can touch
+  int* status;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
+
+constexpr int kAttMaxCtas = 160;  // CTAs of the attention kernel at most (one per SM)
+struct AttArgs {
+  const void* q;  // bf16 [total][G * kv_heads][head_dim], token stride in elements
+  long long q_stride;
+  const uint8_t* k_cache; const uint8_t* v_cache;
+  const float* k_scale; const float* v_scale;
+  const int32_t* page_table; const int32_t* q_start; const int32_t* lens;
+  const float* slopes;  // [G * kv_heads] or null
+  void* out; float* lse;
+  int num_pages, kv_heads, page_size, head_dim, width, B, total, max_new;
+  int G;       // query heads per kv head
+  int window;  // tokens a row sees at most, 0 = all
+  float sm_scale, softcap;
+  int* status;
+  int* tickets;     // [kAttMaxCtas], zero between calls
+  float* partials;  // attention_partial_bytes
+};
+int attention_row_tiles(int G, int max_new);
+size_t attention_partial_bytes(int D, int G, int max_new);
+cudaError_t launch_attention(const AttArgs& a, int sms, cudaStream_t s);
+
 // Launch configuration that lets a kernel start while its predecessor in the
 // stream finishes (it waits with griddepcontrol.wait before using its results).
 struct PdlLaunch {
