@@ -11,16 +11,17 @@
 // the head, far below the tensor cores' balance, so the cache stream from HBM
 // is the floor.  One pass with the running maximum and sum of the softmax.
 //
-// Work split.  The unit is a tile of 64 tokens of one item (sequence, kv head,
-// group of up to 8 RT rows).  Every CTA (one per SM) adds up the sequences' tile
-// counts for itself and takes an equal share of all tiles, whatever the
-// lengths, so one long sequence fills the GPU like a batch of short ones.  An
-// item that spans CTAs is joined through the workspace by the last CTA to
-// arrive, in order of position.
-//
-// Inside a CTA a producer warp copies pages (TMA, 128- or 64-byte swizzle) into a
-// ring of tiles and seven consumer warps take tiles in turn, each with its own
-// maximum, sum and accumulator; they join at the end of an item.
+// Work split.  The unit is a tile of 8 KB of the cache (32 tokens of 128, 64 of
+// 64) of one item (sequence, kv head, group of up to 8 RT rows); an item counts
+// kItemCost tiles more for its start and end.  Every CTA (one per SM) adds up the
+// sequences' units for itself and takes an equal share of all of them, and each
+// of its eight warps an equal share of that, whatever the lengths: one long
+// sequence fills the GPU like a batch of short ones.  A warp works alone: it
+// looks up the pages, copies them (TMA, 128- or 64-byte swizzle) into its own ring
+// of tiles, and keeps its own maximum, sum and accumulator.  An item inside one
+// warp's share is finished by it; pieces are joined in order of position, once
+// at the CTA's end through shared memory, and across CTAs through the workspace
+// by the last CTA to arrive.
 //
 // Arithmetic of a tile.
 //   S = Q K^T on mma m16n8k32 (E4M3): K goes to the tensor core as it is
@@ -54,33 +55,37 @@ namespace moe {
 
 namespace {
 
-constexpr int kTile = 64;                 // tokens of a tile
-constexpr int kWarps = 7;                 // consumer warps (with the producer two a scheduler: up to 255 registers)
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 8;                 // (255 registers a thread)
+constexpr int kThreads = kWarps * 32;
+constexpr int kItemCost = 2;              // units of an item beside its tiles
+constexpr int kMinUnits = 2;              // units of a warp at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.f;        // weights are rounded to f16 in units of 2^-15
 
-// Per tile: the scales of its four 16-token groups and which of them were loaded.
-struct TileMeta {
-  float ks[4], vs[4];
-  int mask;
-  int pad[3];
+// A piece of an item that a warp (or, in the workspace, a CTA) could not finish.
+struct Piece {
+  long long item0;   // first unit of the item, -1: no piece
+  int units;         // of the item
+  int start, row0, rows, head;
 };
 
 template <int D, int RT>
 struct AttCfg {
+  static constexpr int kTile = 4096 / D;                   // tokens of a tile
+  static constexpr int kGroups = kTile / 16;
   static constexpr int kRowsC = 8 * RT;                    // rows of an item
   static constexpr int kHalfTile = kTile * D;              // bytes of the K (or V) part of a tile
   static constexpr int kStage = 2 * kHalfTile;
-  static constexpr int kRed = kWarps * kRowsC * D * 4;     // the warps' accumulators at the end of an item
-  static constexpr int kNST = std::min(24, (220 * 1024 - kRed) / kStage);
-  static constexpr size_t kRedAt = (size_t)kNST * kStage;
-  static constexpr size_t kStatAt = kRedAt + kRed;         // [warp][row] maximum and sum, [warp] largest V scale
-  static constexpr size_t kMetaAt = kStatAt + (size_t)kWarps * (2 * kRowsC + 4) * 4;
-  static constexpr size_t kBarsAt = kMetaAt + (size_t)kNST * sizeof(TileMeta);
-  static constexpr size_t kMiscAt = kBarsAt + (2 * kNST + 2) * 8;
-  static constexpr size_t kSmem = 1024 + kMiscAt + 64 + 40;
+  static constexpr int kNST = RT == 1 ? 3 : 2;             // ring stages of a warp
+  static constexpr int kPartF = kRowsC * (D + 2);          // floats of a piece: accumulators, then (maximum, sum) a row
+  // a warp's first piece has a place of its own, its last one lies over its ring
+  static constexpr size_t kPartAt = (size_t)kWarps * kNST * kStage;
+  static constexpr size_t kRecAt = kPartAt + (size_t)kWarps * kPartF * 4;
+  static constexpr size_t kBarsAt = kRecAt + 2 * kWarps * sizeof(Piece);
+  static constexpr size_t kMiscAt = kBarsAt + kWarps * kNST * 8;
+  static constexpr size_t kSmem = 1024 + kMiscAt + kWarps * 16 + 16;
+  static_assert(kPartF * 4 <= kNST * kStage && kPartF % 4 == 0 && kSmem <= 227 * 1024, "shared memory");
 };
 
 struct AttMaps {
@@ -126,8 +131,9 @@ MOE_DEV uint32_t chunk_at(uint32_t base, int t, int c) {
 struct Seq {
   int start, n, len, tile0, tiles, groups;  // groups: row groups
 };
-template <int RT>
+template <int D, int RT>
 MOE_DEV Seq load_seq(const AttArgs& a, int b, bool report) {
+  constexpr int kTile = AttCfg<D, RT>::kTile;
   Seq s;
   s.start = __ldg(a.q_start + b);
   s.n = __ldg(a.q_start + b + 1) - s.start;
@@ -140,100 +146,113 @@ MOE_DEV Seq load_seq(const AttArgs& a, int b, bool report) {
   // the first token any row sees (the first row's window), then whole tiles
   const int lo = a.window > 0 ? max(0, s.len - s.n + 1 - a.window) : 0;
   s.tile0 = lo / kTile;
-  s.tiles = max(1, (s.len + kTile - 1) / kTile - s.tile0);
+  s.tiles = max(0, (s.len + kTile - 1) / kTile - s.tile0);
   s.groups = (int)(((long long)s.n * a.G + 8 * RT - 1) / (8 * RT));
   return s;
 }
 
-// The pieces of a CTA: tiles [t0, t1) of an item (b, head, group).
+// The pieces of a warp: units [u0, u1) of an item (b, head, group), of which
+// the first kItemCost are no tiles.
 struct Walk {
-  long long left;      // tiles this CTA still has to hand out
+  long long left;      // units still to hand out, this piece included
   int b, head, grp;
-  int t0, t1;
-  long long item0;     // first tile of the item, counted over all items
+  int u0, u1;
+  long long item0;     // first unit of the item, counted over all items
   Seq s;
 };
-template <int RT>
+template <int D, int RT>
 MOE_DEV void walk_start(Walk& w, const AttArgs& a, int b, long long b_first, long long x, long long count) {
   w.left = count;
   w.b = b;
-  if (count <= 0) return;
-  w.s = load_seq<RT>(a, b, false);
-  const long long it = (x - b_first) / w.s.tiles;
+  w.s = load_seq<D, RT>(a, b, false);
+  const int units = w.s.tiles + kItemCost;
+  const long long it = (x - b_first) / units;
   w.head = (int)(it / w.s.groups);
   w.grp = (int)(it % w.s.groups);
-  w.item0 = b_first + it * w.s.tiles;
-  w.t0 = (int)(x - w.item0);
-  w.t1 = (int)min((long long)w.s.tiles, w.t0 + count);
+  w.item0 = b_first + it * units;
+  w.u0 = (int)(x - w.item0);
+  w.u1 = (int)min((long long)units, w.u0 + count);
 }
-template <int RT>
+template <int D, int RT>
 MOE_DEV bool walk_next(Walk& w, const AttArgs& a) {  // to the next piece
-  w.left -= w.t1 - w.t0;
+  w.left -= w.u1 - w.u0;
   if (w.left <= 0) return false;
-  w.item0 += w.s.tiles;
+  w.item0 += w.s.tiles + kItemCost;
   if (++w.grp == w.s.groups) {
     w.grp = 0;
     if (++w.head == a.kv_heads) {
       w.head = 0;
       do {
         ++w.b;
-        w.s = load_seq<RT>(a, w.b, false);
-      } while (w.s.groups == 0);  // (a sequence without rows has no tiles; left > 0: one with rows follows)
+        w.s = load_seq<D, RT>(a, w.b, false);
+      } while (w.s.groups == 0);  // (a sequence without rows has no units; left > 0: one with rows follows)
     }
   }
-  w.t0 = 0;
-  w.t1 = (int)min((long long)w.s.tiles, w.left);
+  w.u0 = 0;
+  w.u1 = (int)min((long long)w.s.tiles + kItemCost, w.left);
   return true;
 }
 
+// Where a row of an item goes.
+struct OutRow {
+  size_t at;
+  MOE_DEV OutRow(const AttArgs& a, int start, int row, int head) {
+    at = (size_t)(start + row / a.G) * (size_t)(a.G * a.kv_heads) + head * a.G + row % a.G;
+  }
+  MOE_DEV uint16_t* out(const AttArgs& a, int D) const { return reinterpret_cast<uint16_t*>(a.out) + at * D; }
+  MOE_DEV void lse(const AttArgs& a, float M, float L) const {
+    if (a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
+};
+
+// Adds a piece of a row, with its own (maximum, sum) `st`, relative to the maximum ms.
+MOE_DEV void add_piece(float4& acc, float& L, float2 st, float4 o, float ms) {
+  const float e = ex2(st.x - ms);
+  L += e * st.y;
+  acc.x += o.x * e; acc.y += o.y * e; acc.z += o.z * e; acc.w += o.w * e;
+}
+
 // Four columns of a finished row, and (first column) its log-sum-exp.
-MOE_DEV void att_store(const AttArgs& a, int start, int row, int head, int D, int d, float4 acc, float M, float L) {
-  const size_t tok = (size_t)(start + row / a.G);
-  const int hq = head * a.G + row % a.G;
+MOE_DEV void store4(const AttArgs& a, const Piece& p, int r, int D, int d, float4 acc, float M, float L) {
+  const OutRow at(a, p.start, p.row0 + r, p.head);
   const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
-  uint2 v;
-  v.x = pack_bf16(acc.x * inv, acc.y * inv);
-  v.y = pack_bf16(acc.z * inv, acc.w * inv);
-  const size_t hi = tok * (size_t)(a.G * a.kv_heads) + hq;
-  *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + hi * D + d) = v;
-  if (a.lse && d == 0) a.lse[hi] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  *reinterpret_cast<uint2*>(at.out(a, D) + d) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (d == 0) at.lse(a, M, L);
 }
 
 template <int D, int RT, bool MODS>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const __grid_constant__ AttMaps maps) {
   using C = AttCfg<D, RT>;
-  constexpr int kRowsC = C::kRowsC;
+  constexpr int kRowsC = C::kRowsC, kTile = C::kTile, kGroups = C::kGroups, kNST = C::kNST;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t* ring = smem;
-  float* red = reinterpret_cast<float*>(smem + C::kRedAt);       // [warp][row][D]
-  float* stat = reinterpret_cast<float*>(smem + C::kStatAt);     // [warp][2][row], then [warp] at kWarps * 2 * rows
-  TileMeta* meta = reinterpret_cast<TileMeta*>(smem + C::kMetaAt);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt);
-  uint64_t* empty = full + C::kNST;
-  uint64_t* join = empty + C::kNST;   // the consumer warps' meeting point
-  long long* s_ll = reinterpret_cast<long long*>(smem + C::kMiscAt);  // [0] total [1] first tile of b, then ints
-  volatile int* s_i = reinterpret_cast<volatile int*>(s_ll + 2);      // [0] b, [1] last to arrive
+  uint8_t* ring = smem + (size_t)warp * kNST * C::kStage;                      // this warp's
+  Piece* recs = reinterpret_cast<Piece*>(smem + C::kRecAt);                     // [warp][first, last]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt) + warp * kNST;
+  long long* s_first = reinterpret_cast<long long*>(smem + C::kMiscAt);         // [warp] first unit of sequence s_b
+  int* s_b = reinterpret_cast<int*>(s_first + kWarps);                           // [warp], then [1] last to arrive
   int* status = a.status;
+  auto part_of = [&](int w, int last) {  // where warp w leaves its first or last piece
+    return reinterpret_cast<float*>(last ? smem + (size_t)w * kNST * C::kStage
+                                         : smem + C::kPartAt + (size_t)w * C::kPartF * 4);
+  };
 
-  if (tid == 0) {
-    for (int i = 0; i < C::kNST; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
-    }
-    mbar_init(join, kWarps);
+  if (lane == 0) {
+    for (int i = 0; i < kNST; ++i) mbar_init(full + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    recs[2 * warp].item0 = recs[2 * warp + 1].item0 = -1;
   }
 
-  // ---- this CTA's share: every thread adds up a run of sequences, then a scan
-  __shared__ long long s_scan[kWarps + 1];
+  // ---- the shares: every thread adds up a run of sequences, then a scan
+  __shared__ long long s_scan[kWarps];
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    const Seq s = load_seq<RT>(a, b, blockIdx.x == 0);
-    mine += (long long)s.tiles * s.groups * a.kv_heads;
+    const Seq s = load_seq<D, RT>(a, b, blockIdx.x == 0);
+    mine += (long long)(s.tiles + kItemCost) * s.groups * a.kv_heads;
   }
   long long incl = mine;
 #pragma unroll
@@ -245,118 +264,105 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps + 1; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const int G = (int)min((long long)gridDim.x, total);  // CTAs that get work: a tile each at least
-  if ((int)blockIdx.x >= G) return;                       // (the whole CTA; nothing is in flight)
-  const long long x0 = total * blockIdx.x / G, x1 = total * (blockIdx.x + 1) / G;
-  if (x0 >= before && x0 < before + mine) {  // one thread
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq<RT>(a, b, false);
-      const long long nb = (long long)s.tiles * s.groups * a.kv_heads;
-      if (x0 < at + nb) {
-        s_ll[1] = at;
-        s_i[0] = b;
-        break;
+  // CTAs that get work
+  const int G = (int)min((long long)gridDim.x, (total + kWarps * kMinUnits - 1) / (kWarps * kMinUnits));
+  if ((int)blockIdx.x >= G) return;  // (the whole CTA; nothing is in flight)
+  const long long X0 = total * blockIdx.x / G, X1 = total * (blockIdx.x + 1) / G;
+  auto share = [&](int w) { return X0 + (X1 - X0) * w / kWarps; };
+  for (int w = 0; w < kWarps; ++w) {
+    const long long x = share(w);
+    if (x >= before && x < before + mine) {  // one thread for each w
+      long long at = before;
+      for (int b = b0; b < b1; ++b) {
+        const Seq s = load_seq<D, RT>(a, b, false);
+        const long long nb = (long long)(s.tiles + kItemCost) * s.groups * a.kv_heads;
+        if (x < at + nb) {
+          s_first[w] = at;
+          s_b[w] = b;
+          break;
+        }
+        at += nb;
       }
-      at += nb;
     }
   }
   __syncthreads();
-  Walk w;
-  walk_start<RT>(w, a, s_i[0], s_ll[1], x0, x1 - x0);
-  const int P = a.page_size;
-  const int box = min(P, kTile);          // token rows of one copy
-  const int nbox = kTile / box;
 
-  if (warp == kWarps) {
-    // ================================================================ producer
-    // Eight tiles' pages and scales at a time: lane 4 t + g looks up 16-token
-    // group g of tile t, so the two dependent reads are paid once for eight tiles.
-    uint32_t n = 0;
-    int si = 0;
-    uint32_t ph = 0;
-    bool alive = true;
-    do {
-      const int lo = a.window > 0 ? max(0, w.s.len - w.s.n + 1 - a.window) : 0;
-      for (int tb = w.t0; tb < w.t1 && alive; tb += 8) {
-        const int tl = tb + (lane >> 2);
-        const int pos = (w.s.tile0 + tl) * kTile + 16 * (lane & 3);
-        bool ok = tl < w.t1 && pos < w.s.len && pos + 16 > lo;
-        int page = 0;
-        float ks = 0.f, vs = 0.f;
-        if (ok) {
-          page = __ldg(a.page_table + (size_t)w.b * a.width + pos / P);
-          if (page < 0 || page >= a.num_pages) {  // its tokens are masked
-            atomicExch(status, MOE_ERR_INVALID_ARG);
-            ok = false;
-          } else {
-            ks = __ldg(a.k_scale + (size_t)page * a.kv_heads + w.head);
-            vs = __ldg(a.v_scale + (size_t)page * a.kv_heads + w.head);
-          }
-        }
-        const uint32_t okm = __ballot_sync(0xffffffffu, ok);
-        for (int t = 0; t < 8 && tb + t < w.t1; ++t) {
-          const int m4 = (okm >> (4 * t)) & 15;
-          // box i holds groups i * box / 16 ...; it is copied if any of them is wanted
-          const int gpb = box >> 4;
-          int boxes = 0;
-          for (int i = 0; i < nbox; ++i) boxes += ((m4 >> (i * gpb)) & ((1 << gpb) - 1)) != 0;
-          bool go = true;
-          if (n >= (uint32_t)C::kNST) {
-            if (lane == 0) go = mbar_wait_landed(empty + si, ph ^ 1u, status);
-            go = __shfl_sync(0xffffffffu, go, 0);
-          }
-          if (!go) { alive = false; break; }
-          if ((lane >> 2) == t) {
-            meta[si].ks[lane & 3] = ks;
-            meta[si].vs[lane & 3] = vs;
-            if ((lane & 3) == 0) meta[si].mask = m4;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_expect_tx(full + si, (uint32_t)(boxes * 2 * box * D));
-          __syncwarp();
-          // lanes 0 .. nbox - 1 copy K boxes, the next nbox V boxes
-          const int i = lane % nbox;
-          const int src = 4 * t + __ffs((m4 >> (i * gpb)) & ((1 << gpb) - 1)) - 1 + i * gpb;
-          const int pg = __shfl_sync(0xffffffffu, page, src & 31);
-          if (lane < 2 * nbox && ((m4 >> (i * gpb)) & ((1 << gpb) - 1)) != 0) {
-            const int at = (w.s.tile0 + tb + t) * kTile % P;  // first row inside the page (0 unless a page holds several tiles)
-            uint8_t* dst = ring + (size_t)si * C::kStage + (lane < nbox ? 0 : C::kHalfTile) + i * box * D;
-            tma_load_3d(dst, lane < nbox ? &maps.k : &maps.v, 0, at, pg * a.kv_heads + w.head, full + si);
-          }
-          __syncwarp();
-          ++n;
-          if (++si == C::kNST) { si = 0; ph ^= 1u; }
-        }
-      }
-    } while (alive && walk_next<RT>(w, a));
-    // every copy this CTA issued lands before it ends
-    if (lane == 0)
-      for (uint32_t j = (n > (uint32_t)C::kNST ? n - C::kNST : 0); j < n; ++j)
-        mbar_wait_landed(full + (j % C::kNST), (j / C::kNST) & 1u, status);
-    __syncwarp();
-    return;
-  }
-
-  // ================================================================ consumers
   const int g = lane >> 2, q = lane & 3;
   const int fg = D == 128 ? ((g & 1) << 2 | g >> 1) : g;   // this thread's chunk of a V row (16 or 8 values)
   constexpr int kMT = D / 16;                              // 16-row tiles of V^T
-  uint32_t jn = 0;                                         // meetings so far
-  auto meet = [&]() -> bool {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(join);
-    return mbar_wait_landed(join, jn++ & 1u, status);
-  };
-  uint32_t n0 = 0;  // tiles of the pieces before this one
+  const int P = a.page_size;
+  const int box = min(P, kTile);          // token rows of one copy
+  const int nbox = kTile / box, gpb = box >> 4;
+  uint32_t issued = 0, used = 0;          // tiles copied and consumed so far (ring position and phase)
   bool alive = true;
-  do {
+  Walk w;
+  bool more = share(warp) < share(warp + 1);
+  if (more) walk_start<D, RT>(w, a, s_b[warp], s_first[warp], share(warp), share(warp + 1) - share(warp));
+  while (more) {
     const int rows = min(kRowsC, w.s.n * a.G - w.grp * kRowsC);
     const int pos0 = w.s.len - w.s.n;  // position of the step's first token
+    // tokens every row sees lie in [lo_all, hi_all), those some row sees in [lo_any, len)
+    const int hi_all = pos0 + 1;
+    const int lo_all = a.window > 0 ? max(0, w.s.len - a.window) : 0;
+    const int lo_any = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
+    const int t0 = w.s.tile0 + max(0, w.u0 - kItemCost), t1 = w.s.tile0 + max(0, w.u1 - kItemCost);
+
+    // ---- pages: lane i looks up 16-token group i of a batch of 32 / kGroups
+    // tiles; the next batch is read while this one is used
+    constexpr int kBatch = 32 / kGroups;
+    struct Look { int page; float ks, vs; uint32_t ok; };
+    auto look = [&](int tb) {
+      Look k;
+      const int pos = tb * kTile + 16 * lane;
+      bool ok = tb + lane / kGroups < t1 && pos < w.s.len && pos + 16 > lo_any;
+      k.page = 0;
+      k.ks = k.vs = 0.f;
+      if (ok) {
+        k.page = __ldg(a.page_table + (size_t)w.b * a.width + pos / P);
+        if (k.page < 0 || k.page >= a.num_pages) {  // its tokens are masked
+          atomicExch(status, MOE_ERR_INVALID_ARG);
+          ok = false;
+          k.page = 0;
+        } else {
+          k.ks = __ldg(a.k_scale + (size_t)k.page * a.kv_heads + w.head);
+          k.vs = __ldg(a.v_scale + (size_t)k.page * a.kv_heads + w.head);
+        }
+      }
+      k.ok = __ballot_sync(0xffffffffu, ok);
+      return k;
+    };
+    Look cur = look(t0), nxt = look(t0 + kBatch);
+    int cur0 = t0;  // first tile of cur
+    int ti = t0;    // next tile to copy
+    auto issue = [&]() {
+      const Look& k = ti - cur0 < kBatch ? cur : nxt;
+      const int r = (ti - cur0) % kBatch * kGroups;           // lane of the tile's first group
+      const uint32_t m = (k.ok >> r) & ((1u << kGroups) - 1);
+      const uint32_t bm = (1u << gpb) - 1;
+      const int si = issued % kNST;
+      // lanes 0 .. nbox - 1 copy K boxes, the next nbox V boxes; a box is copied
+      // if any of its groups is wanted
+      const int i = lane % nbox;
+      const uint32_t mine = (m >> (i * gpb)) & bm;
+      const int pg = __shfl_sync(0xffffffffu, k.page, (r + i * gpb + __ffs(mine | 1u << 31) - 1) & 31);
+      const bool go = lane < 2 * nbox && mine != 0;
+      const int copies = __popc(__ballot_sync(0xffffffffu, go));
+      if (lane == 0) mbar_expect_tx(full + si, (uint32_t)(copies * box * D));
+      __syncwarp();
+      if (go) {
+        uint8_t* dst = ring + (size_t)si * C::kStage + (lane < nbox ? 0 : C::kHalfTile) + i * box * D;
+        // the first row inside the page is 0 unless a page holds several tiles
+        tma_load_3d(dst, lane < nbox ? &maps.k : &maps.v, 0, ti * kTile % P, pg * a.kv_heads + w.head, full + si);
+      }
+      ++issued;
+      ++ti;
+    };
+    for (int i = 0; i < kNST && ti < t1; ++i) issue();
+
     // ---- Q fragments: rows g of each row tile, upper part in a0 / a2, lower in a1 / a3
     uint32_t qf[RT][D / 32][4];
     float qs[RT];      // 1 / (row's scale), times the softmax scale
@@ -429,26 +435,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
         for (int i = 0; i < 4; ++i) o[rt][mt][i] = 0.f;
     }
     float R = 0.f;  // largest V scale so far: the accumulators' unit is R 2^-15
-    // tokens every row sees lie in [lo_all, hi_all); tiles inside need no mask
-    const int hi_all = pos0 + 1;
-    const int lo_all = a.window > 0 ? max(0, w.s.len - a.window) : 0;
-    const int lo_any = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
-
-    const int cnt = w.t1 - w.t0;
-    for (int t = (int)((warp + kWarps - n0 % kWarps) % kWarps); t < cnt; t += kWarps) {
-      const uint32_t sq = n0 + t;
-      const int si = (int)(sq % C::kNST);
-      if (!mbar_wait_landed(full + si, (sq / C::kNST) & 1u, status)) { alive = false; break; }
-      const TileMeta& md = meta[si];
-      const int mask = md.mask;
-      const int base = (w.s.tile0 + w.t0 + t) * kTile;
-      const bool part = mask != 15 || base + kTile > hi_all || base < lo_all;
+    for (int t = t0; t < t1; ++t) {
+      const int si = used % kNST;
+      if (t - cur0 == kBatch) {
+        cur = nxt;
+        cur0 = t;
+        nxt = look(t + kBatch);
+      }
+      const int r0 = (t - cur0) * kGroups;
+      const int mask = (int)((cur.ok >> r0) & ((1u << kGroups) - 1));
+      float ksg[kGroups], vsg[kGroups];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) {
+        ksg[i] = __shfl_sync(0xffffffffu, cur.ks, r0 + i);
+        vsg[i] = __shfl_sync(0xffffffffu, cur.vs, r0 + i);
+      }
+      const int base = t * kTile;
+      const bool part = mask != (1 << kGroups) - 1 || base + kTile > hi_all || base < lo_all;
       const uint32_t kt = su32(ring + (size_t)si * C::kStage), vt = kt + C::kHalfTile;
+      if (!mbar_wait_landed(full + si, (used / kNST) & 1u, status)) { alive = false; break; }
+      ++used;
 
       // ---- scores: s[rt][2 j + i] is row g, token 16 (j / 2) + 8 (j % 2) + 4 i + q
-      float s[RT][16];
+      float s[RT][2 * kTile / 8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kTile / 8; ++j) {
         const int row = 8 * j + 4 * (g & 1) + (g >> 1);
         float c[RT][4];
 #pragma unroll
@@ -464,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
             mma_e4m3(c[rt], f1[0], f1[1], f1[2], f1[3], kv.z, kv.w);
           }
         }
-        const float ks = md.ks[j >> 1];
+        const float ks = ksg[j >> 1];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           const float f = qs[rt] * ks * (MODS ? 1.f : kLog2e);
@@ -476,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int k = 0; k < kTile / 4; ++k) {
             float x = s[rt][k];
             if (a.softcap > 0.f) x = a.softcap * tanhf(__fdividef(x, a.softcap));
             const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
@@ -487,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
+          for (int k = 0; k < kTile / 4; ++k) {
             const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
             const bool see = pos <= pos_r[rt] && (a.window <= 0 || pos > pos_r[rt] - a.window) && ((mask >> (k >> 2)) & 1);
             if (!see) s[rt][k] = -INFINITY;
@@ -496,18 +507,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
       // ---- running maximum and sum
       float Rn = R;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((mask >> i) & 1) Rn = fmaxf(Rn, md.vs[i]);
+      for (int i = 0; i < kGroups; ++i) Rn = fmaxf(Rn, vsg[i]);  // (0 where a group was not read)
       const float Rq = Rn > 0.f ? __fdividef(kPScale, Rn) : 0.f;
       const float rr = Rn == R ? 1.f : __fdividef(R, Rn);
       float al[RT];
       bool turn = Rn != R;
-      uint32_t pb[RT][8];
+      uint32_t pb[RT][kTile / 8];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         float mx = s[rt][0];
 #pragma unroll
-        for (int k = 1; k < 16; ++k) mx = fmaxf(mx, s[rt][k]);
+        for (int k = 1; k < kTile / 4; ++k) mx = fmaxf(mx, s[rt][k]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float mn = fmaxf(m[rt], mx);
@@ -517,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
         m[rt] = mn;
         float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float F = md.vs[j >> 1] * Rq;
+        for (int j = 0; j < kTile / 8; ++j) {
+          const float F = vsg[j >> 1] * Rq;
           const float p0 = ex2(s[rt][2 * j] - ms), p1 = ex2(s[rt][2 * j + 1] - ms);
           sum += p0 + p1;
           // masked tokens of a group that was not loaded: vs is 0, p is 0
@@ -542,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
       }
       // ---- O^T += V^T P^T, 16 tokens at a time
 #pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
+      for (int gr = 0; gr < kGroups; ++gr) {
         uint32_t v4[4][D / 32];  // tokens q, 4 + q, 8 + q, 12 + q of the group, this thread's chunk
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -577,113 +587,148 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + si);
+      __syncwarp();  // the stage has been read
+      if (ti < t1) issue();
     }
     if (!alive) break;
-    n0 += cnt;
 
-    // ---- the warps join: accumulators and statistics through shared memory
-    if (jn > 0 && !meet()) break;  // the piece before has been read out
-    {
-      float* rw = red + (size_t)warp * kRowsC * D;
+    // ---- the end of a piece
+    const bool whole = w.u0 == 0 && w.u1 == w.s.tiles + kItemCost;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 1);
+      l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 2);
+    }
+    const float ru = R * (1.f / kPScale);
+    if (whole) {
+      // columns 2 q and 2 q + 1 of the accumulator are rows; this thread has
+      // D / 8 consecutive values of each from fg * D / 8
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = rt * 8 + 2 * q + c;
+          const float L = __shfl_sync(0xffffffffu, l[rt], 8 * q + 4 * c);
+          const float M = __shfl_sync(0xffffffffu, m[rt], 8 * q + 4 * c);
+          if (r < rows) {
+            const float inv = L == 0.f ? 0.f : __fdiv_rn(ru, L);
+            const OutRow o_at(a, w.s.start, w.grp * kRowsC + r, w.head);
+            uint32_t v[kMT];
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) v[mt] = pack_bf16(o[rt][mt][c] * inv, o[rt][mt][2 + c] * inv);
+            uint4* dst = reinterpret_cast<uint4*>(o_at.out(a, D) + fg * (D / 8));
+#pragma unroll
+            for (int k = 0; k < kMT / 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+            if (g == 0) o_at.lse(a, M, L);
+          }
+        }
+    } else {
+      const int last = w.u0 == 0 ? 1 : 0;  // (a warp's piece that starts an item and does not end it is its last)
+      float* p = part_of(warp, last);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float sum = l[rt];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (q == 0) {
-          stat[(warp * 2 + 0) * kRowsC + rt * 8 + g] = m[rt];
-          stat[(warp * 2 + 1) * kRowsC + rt * 8 + g] = sum;
-        }
-        // columns 2 q, 2 q + 1 are rows; this thread's d are D / 8 consecutive ones from fg * D / 8
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int mt = 0; mt < kMT; mt += 2)
-            *reinterpret_cast<float4*>(rw + (rt * 8 + 2 * q + c) * D + fg * (D / 8) + 2 * mt) =
-                make_float4(o[rt][mt][c], o[rt][mt][2 + c], o[rt][mt + 1][c], o[rt][mt + 1][2 + c]);
+            *reinterpret_cast<float4*>(p + (rt * 8 + 2 * q + c) * D + fg * (D / 8) + 2 * mt) =
+                make_float4(o[rt][mt][c] * ru, o[rt][mt][2 + c] * ru, o[rt][mt + 1][c] * ru, o[rt][mt + 1][2 + c] * ru);
+        if (q == 0) *reinterpret_cast<float2*>(p + kRowsC * D + 2 * (rt * 8 + g)) = make_float2(m[rt], l[rt]);
       }
-      if (lane == 0) stat[kWarps * 2 * kRowsC + warp] = R;
+      if (lane == 0) {
+        Piece& rec = recs[2 * warp + last];
+        rec.item0 = w.item0;
+        rec.units = w.s.tiles + kItemCost;
+        rec.start = w.s.start;
+        rec.row0 = w.grp * kRowsC;
+        rec.rows = rows;
+        rec.head = w.head;
+      }
     }
-    if (!meet()) break;
-    const bool whole = w.t0 == 0 && w.t1 == w.s.tiles;
-    constexpr int kVec = D / 4;  // float4 of a row
-    const float* sR = stat + kWarps * 2 * kRowsC;
-    for (int i = tid; i < kRowsC * kVec; i += kWarps * 32) {
+    more = walk_next<D, RT>(w, a);
+  }
+  // every copy this warp issued lands before the CTA ends
+  for (; used < issued; ++used) mbar_wait_landed(full + used % kNST, (used / kNST) & 1u, status);
+  __syncthreads();
+
+  // ---- the CTA's pieces: neighbours of one item are added in order
+  constexpr int kVec = D / 4;  // float4 of a row
+  for (int i0 = 0; i0 < 2 * kWarps;) {
+    const long long item = recs[i0].item0;
+    int i1 = i0 + 1;
+    if (item < 0) { i0 = i1; continue; }
+    while (i1 < 2 * kWarps && (recs[i1].item0 == item || recs[i1].item0 < 0)) ++i1;
+    const Piece rec = recs[i0];
+    const bool here = item >= X0 && item + rec.units <= X1;  // the whole item is this CTA's
+    for (int i = tid; i < kRowsC * kVec; i += kThreads) {
       const int r = i / kVec, d = (i % kVec) * 4;
-      if (r >= rows) continue;
+      if (r >= rec.rows) continue;
       float M = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) M = fmaxf(M, stat[(x * 2) * kRowsC + r]);
+      for (int x = i0; x < i1; ++x)
+        if (recs[x].item0 == item) M = fmaxf(M, part_of(x >> 1, x & 1)[kRowsC * D + 2 * r]);
       const float ms = M == -INFINITY ? 0.f : M;
       float L = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int x = 0; x < kWarps; ++x) {
-        const float e = ex2(stat[(x * 2) * kRowsC + r] - ms);
-        L += e * stat[(x * 2 + 1) * kRowsC + r];
-        const float f = e * sR[x] * (1.f / kPScale);
-        const float4 ov = *reinterpret_cast<const float4*>(red + ((size_t)x * kRowsC + r) * D + d);
-        acc.x += ov.x * f; acc.y += ov.y * f; acc.z += ov.z * f; acc.w += ov.w * f;
-      }
-      if (whole) {
-        att_store(a, w.s.start, w.grp * kRowsC + r, w.head, D, d, acc, M, L);
+      for (int x = i0; x < i1; ++x)
+        if (recs[x].item0 == item) {
+          const float* p = part_of(x >> 1, x & 1);
+          add_piece(acc, L, *reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r),
+                    *reinterpret_cast<const float4*>(p + r * D + d), ms);
+        }
+      if (here) {
+        store4(a, rec, r, D, d, acc, M, L);
       } else {
-        float* part = a.partials + ((size_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * kRowsC * (D + 4);
-        __stcg(reinterpret_cast<float4*>(part + (size_t)r * D + d), acc);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(part + (size_t)kRowsC * D + 2 * r), make_float2(M, L));
+        // slot 0 continues an item of the CTA before this one, slot 1 starts one
+        float* p = a.partials + ((size_t)blockIdx.x * 2 + (item >= X0 ? 1 : 0)) * C::kPartF;
+        __stcg(reinterpret_cast<float4*>(p + (size_t)r * D + d), acc);
+        if (d == 0) __stcg(reinterpret_cast<float2*>(p + kRowsC * D + 2 * r), make_float2(M, L));
       }
     }
-    if (!whole) {
+    if (!here) {
+      const long long e = item + rec.units - 1;
+      const int c_first = (int)(((item + 1) * G - 1) / total), c_last = (int)(((e + 1) * G - 1) / total);
       __threadfence();
-      if (!meet()) break;
-      // CTAs that hold a piece of this item
-      const long long i0 = w.item0, i1 = w.item0 + w.s.tiles - 1;
-      const int c_first = (int)(((i0 + 1) * G - 1) / total), c_last = (int)(((i1 + 1) * G - 1) / total);
+      __syncthreads();
       if (tid == 0) {
         __threadfence();
         const bool last = atom_add_acq_rel(a.tickets + c_first, 1) == c_last - c_first;
         if (last) a.tickets[c_first] = 0;  // ready for the next call
-        s_i[1] = last;
+        s_b[kWarps] = last;
       }
-      if (!meet()) break;
-      if (s_i[1]) {
+      __syncthreads();
+      if (s_b[kWarps]) {
         __threadfence();
-        constexpr size_t kPart = (size_t)kRowsC * (D + 4);
-        for (int i = tid; i < kRowsC * kVec; i += kWarps * 32) {
+        for (int i = tid; i < kRowsC * kVec; i += kThreads) {
           const int r = i / kVec, d = (i % kVec) * 4;
-          if (r >= rows) continue;
+          if (r >= rec.rows) continue;
           float M = -INFINITY;
-          for (int c = c_first; c <= c_last; ++c) {
-            const float* part = a.partials + ((size_t)c * 2 + (c == c_first ? 1 : 0)) * kPart;
-            M = fmaxf(M, __ldcg(part + (size_t)kRowsC * D + 2 * r));
-          }
+#pragma unroll 4
+          for (int c = c_first; c <= c_last; ++c)
+            M = fmaxf(M, __ldcg(a.partials + ((size_t)c * 2 + (c == c_first)) * C::kPartF + kRowsC * D + 2 * r));
           const float ms = M == -INFINITY ? 0.f : M;
           float L = 0.f;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int c = c_first; c <= c_last; ++c) {
-            const float* part = a.partials + ((size_t)c * 2 + (c == c_first ? 1 : 0)) * kPart;
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(part + (size_t)kRowsC * D + 2 * r));
-            const float4 ov = __ldcg(reinterpret_cast<const float4*>(part + (size_t)r * D + d));
-            const float e = ex2(st.x - ms);
-            L += e * st.y;
-            acc.x += ov.x * e; acc.y += ov.y * e; acc.z += ov.z * e; acc.w += ov.w * e;
+            const float* p = a.partials + ((size_t)c * 2 + (c == c_first)) * C::kPartF;
+            add_piece(acc, L, __ldcg(reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r)),
+                      __ldcg(reinterpret_cast<const float4*>(p + (size_t)r * D + d)), ms);
           }
-          att_store(a, w.s.start, w.grp * kRowsC + r, w.head, D, d, acc, M, L);
+          store4(a, rec, r, D, d, acc, M, L);
         }
       }
+      __syncthreads();  // (the flag is used again)
     }
-  } while (walk_next<RT>(w, a));
+    i0 = i1;
+  }
 }
 
-// K or V cache [num_pages * kv_heads][page_size][D] bytes; box = up to 64 rows of one page
+// K or V cache [num_pages * kv_heads][page_size][D] bytes; box = rows of one page, up to a tile
 bool map_cache(CUtensorMap* m, const uint8_t* base, int D, int P, long long tiles) {
   if (!encode_fn()) return false;
   const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)tiles};
   const cuuint64_t stride[2] = {(cuuint64_t)D, (cuuint64_t)P * D};
-  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)std::min(P, kTile), 1};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)std::min(P, 4096 / D), 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dim, stride, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -714,7 +759,7 @@ cudaError_t launch_d(const AttArgs& a, const AttMaps& maps, int ctas, cudaStream
 int attention_row_tiles(int G, int max_new) { return (long long)G * max_new <= 8 ? 1 : 2; }
 
 size_t attention_partial_bytes(int D, int G, int max_new) {
-  return (size_t)kAttMaxCtas * 2 * 8 * attention_row_tiles(G, max_new) * (D + 4) * sizeof(float);
+  return (size_t)kAttMaxCtas * 2 * 8 * attention_row_tiles(G, max_new) * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttArgs& a, int sms, cudaStream_t s) {
