@@ -323,20 +323,23 @@ int mtp_eh_front(const int32_t *input_ids, const void *embed, int vocab, const v
  * 1 for an all-zero group) and codes = E4M3(x / s), the quotient in fp32,
  * rounded to nearest even and saturating.
  *   x       bf16 [M, K], rows x_stride elements apart (x_stride >= K, % 8 == 0)
- *   codes   fp8 [M, K];  scales fp32 [M, ceil(K / 128)]
- * K % 16 == 0, K <= 131072, M <= 2^20; x and codes 16-byte aligned.  M == 0 is
+ *   codes   fp8 [M, K]
+ *   scales  fp32 [ceil(K / 128), M4], M4 = M rounded up to a multiple of 4
+ *           (k-blocks first: the product reads a block's scales as one run;
+ *           columns from M on are not written)
+ * K % 16 == 0, K <= 131072, M <= 2^20; x, codes and scales 16-byte aligned.  M == 0 is
  * a no-op.  One kernel.
  */
 int fp8_quant_rows(const void *x, long long x_stride, int M, int K, int e8m0, uint8_t *codes, float *scales,
                    void *stream);
 
 /*
- * out[m, n] = sum_kb scales[m, kb] * w_s[n / 128, kb] *
+ * out[m, n] = sum_kb scales[kb, m] * w_s[n / 128, kb] *
  *             sum_{k in block kb} codes[m, k] * w[n, k]      (fp32 sums)
  *   codes, scales  as fp8_quant_rows writes them
  *   w     fp8 [N, K];  w_s fp32 [ceil(N / 128), ceil(K / 128)]
  *   out   bf16 [M, N], rounded once (out_fp32 == 0), or fp32 [M, N]
- * K % 16 == 0, K <= 131072, any N <= 2^20, M <= 2^20; codes, w, out and the
+ * K % 16 == 0, K <= 131072, any N <= 2^20, M <= 2^20; codes, scales, w, out and the
  * workspace 16-byte aligned.  M == 0 is a no-op.  One kernel; results do not
  * depend on the order in which CTAs finish.
  */

@@ -81,11 +81,11 @@ def _rows_stride(x, name, shape):
 
 def fp8_quant_rows(x, codes, scales, e8m0: bool = False, stream=None):
     """x (bf16 [M, K], any row stride) to E4M3 codes (uint8 [M, K]) and float32
-    scales [M, ceil(K / 128)]."""
+    scales [ceil(K / 128), M rounded up to a multiple of 4]."""
     M, K = x.shape
     ldx = _rows_stride(x, "x", (M, K))
     _want(codes, "codes", torch.uint8, (M, K))
-    _want(scales, "scales", torch.float32, (M, -(-K // 128)))
+    _want(scales, "scales", torch.float32, (-(-K // 128), -(-M // 4) * 4))
     _same_device(x, codes, scales)
     _check(lib().fp8_quant_rows(x.data_ptr(), ldx, M, K, 1 if e8m0 else 0, codes.data_ptr(), scales.data_ptr(),
                                 _stream(stream)), "fp8_quant_rows")
@@ -130,7 +130,7 @@ def fp8_block_gemm(codes, scales, w, w_s, out, workspace, stream=None):
     M = codes.shape[0]
     N, K, f32 = _weight(w, w_s, out, M)
     _want(codes, "codes", torch.uint8, (M, K))
-    _want(scales, "scales", torch.float32, (M, -(-K // 128)))
+    _want(scales, "scales", torch.float32, (-(-K // 128), -(-M // 4) * 4))
     _same_device(codes, scales, w, w_s, out, workspace)
     _check(lib().fp8_block_gemm(codes.data_ptr(), scales.data_ptr(), w.data_ptr(), w_s.data_ptr(), M, N, K,
                                 out.data_ptr(), f32, workspace.data_ptr(), workspace.numel() * workspace.element_size(),

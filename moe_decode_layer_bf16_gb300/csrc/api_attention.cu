@@ -45,13 +45,13 @@ int check_linear(int M, int N, int K) {
 size_t linear_partial_bound(int M, int N, int K) {
   LinPlan p;
   plan_linear(p, std::max(M, 1), N, K, kLinMaxCtas);
-  const long long cells = (long long)p.n_chunks * p.n_tiles * p.nkb;
+  const long long cells = (long long)p.n_tt * p.n_wt * p.nkb;
   const long long ctas = std::min<long long>(kLinMaxCtas, cells);
   return (size_t)ctas * 2 * p.nt * kBlock * sizeof(float);
 }
 
 size_t codes_bytes(int M, int K) { return up256((size_t)M * K); }
-size_t scales_bytes(int M, int K) { return up256((size_t)M * ((K + kBlock - 1) / kBlock) * sizeof(float)); }
+size_t scales_bytes(int M, int K) { return up256((size_t)linear_scale_stride(M) * ((K + kBlock - 1) / kBlock) * sizeof(float)); }
 
 int gemm_launch(const uint8_t* codes, const float* scales, const uint8_t* w, const float* w_s, int M, int N, int K,
                 void* out, int out_fp32, const Ws& ws, uint8_t* partials, bool pdl, cudaStream_t s) {
@@ -79,7 +79,7 @@ int quant_launch(const void* x, long long x_stride, int M, int K, int e8m0, uint
   if (rc != MOE_OK) return rc;
   QuantArgs a;
   a.x = x; a.ldx = x_stride; a.M = M; a.K = K; a.nkb = (K + kBlock - 1) / kBlock; a.e8m0 = e8m0 ? 1 : 0;
-  a.codes = codes; a.scales = scales;
+  a.codes = codes; a.scales = scales; a.mp = linear_scale_stride(M);
   return launch_quant_rows(a, sms, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -126,7 +126,7 @@ int fp8_quant_rows(const void* x, long long x_stride, int M, int K, int e8m0, ui
   if (rc != MOE_OK) return rc;
   if (M == 0) return MOE_OK;
   if ((rc = check_x(x, x_stride, K)) != MOE_OK) return rc;
-  if (!codes || !scales || !al16(codes)) return MOE_ERR_INVALID_ARG;
+  if (!codes || !scales || !al16(codes) || !al16(scales)) return MOE_ERR_INVALID_ARG;
   return quant_launch(x, x_stride, M, K, e8m0, codes, scales, (cudaStream_t)stream);
 }
 
@@ -145,7 +145,7 @@ int fp8_block_gemm(const uint8_t* codes, const float* scales, const uint8_t* w, 
   if (rc != MOE_OK) return rc;
   if (M == 0) return MOE_OK;
   if (!codes || !scales || !w || !w_s || !out || !ws) return MOE_ERR_INVALID_ARG;
-  if (!al16(codes) || !al16(w) || !al16(out) || !al16(ws)) return MOE_ERR_INVALID_ARG;
+  if (!al16(codes) || !al16(scales) || !al16(w) || !al16(out) || !al16(ws)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const Ws l(ws);
   return gemm_launch(codes, scales, w, w_s, M, N, K, out, out_fp32, l, l.data, false, (cudaStream_t)stream);

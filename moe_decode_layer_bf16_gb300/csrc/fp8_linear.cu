@@ -8,26 +8,30 @@
 // Two kernels: the quantisation (a stream over x), and the product on
 // tcgen05.mma.kind::f8f6f4 (E4M3 x E4M3, fp32 accumulators in tensor memory).
 //
-// The product.  The weights are the MMA's 128 rows and the tokens its columns
-// (NT = 16 .. 256 of a chunk), so that one token still fills the MMA's rows
-// and the weights are streamed once per 256 tokens.  The unit of work is a
-// cell: (128 rows of w) x (a chunk of tokens) x (one 128-column k-block), i.e.
-// one 16 KB weight tile and one NT x 128 activation tile through TMA (128-byte
+// The product, in two arrangements of one kernel.  Up to 128 tokens the weights are
+// the MMA's 128 rows and the tokens its columns (NT = 16 .. 128), so that one
+// token still fills the MMA's rows and the weights are streamed once.  Above,
+// 128 tokens are the rows and 256 weight rows the columns: a thread of the
+// epilogue then owns one token and one weight block, and needs one scale for
+// its 128 columns.
+//
+// The unit of work is a cell: a pair of a row tile and a column tile in one
+// 128-column k-block, i.e. one tile of each operand through TMA (128-byte
 // swizzle), four MMAs of K = 32 into one of the accumulator buffers, and an
 // epilogue that adds the buffer, times ws * xs, to fp32 registers: the scales
 // are fp32 values of their own for each k-block, so they cannot ride in the
 // MMA.  Rows past N, tokens past M and columns past K are zeros of the TMA fill.
 //
-// Work split.  One CTA per SM.  Whole waves of (row tile, chunk) pairs are
-// dealt out as they are; the remaining pairs are cut along K into one equal
-// share of cells per CTA (stream-K), so that one token's 72 row tiles keep all
-// 152 SMs streaming.  A CTA that holds a piece of a pair writes its fp32 sums to
-// the workspace; the last to arrive adds the pieces in k order (the result does
-// not depend on who is last).
+// Work split.  One CTA per SM.  Whole waves of pairs are dealt out as they are;
+// the remaining pairs are cut along K into one equal share of cells per CTA
+// (stream-K), so that one token's 72 row tiles keep all 152 SMs streaming.  A
+// CTA that holds a piece of a pair writes its fp32 sums to the workspace; the
+// last to arrive adds the pieces in k order (the result does not depend on who
+// is last).
 //
-// Roles (12 warps): TMA producer, MMA issuer, two warps that prepare the
-// ws * xs products of each cell, eight epilogue warps (four lane quadrants x
-// two column halves).  Every wait is bounded.
+// Roles (12 warps): TMA producer, MMA issuer, a warp that copies each cell's
+// token scales, an idle one, eight epilogue warps (four lane quadrants x two
+// column halves).  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -47,7 +51,18 @@ namespace {
 // One 16-lane half-warp per (token, 128-column group), 8 columns a lane: one
 // 16-byte load, a shuffle maximum, one 8-byte store.  K % 16 == 0, so a lane's
 // 8 columns lie inside a row or outside of it as a whole.
+//
+// A code is E4M3(fl32(x / s)), and the quotient matters only beside a border
+// between two codes: x * (1 / s) is within 2 units in the last place of it, so
+// unless that product lies as near to a midpoint of codes (or among the
+// subnormal codes, whose spacing differs) the code is the same, and only then the
+// division is carried out.  A power-of-two scale needs none.
 constexpr int kQuantThreads = 256;
+
+// True where E4M3 of a number within 2 ulp of q may differ from E4M3 of q.
+MOE_DEV bool near_border(float q) {
+  return ((__float_as_uint(q) - 0x7fffeu) & 0xfffffu) <= 4u || fabsf(q) < 0.015625f;
+}
 
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) {
   grid_dep_launch();  // the product may start streaming its weights now
@@ -71,53 +86,76 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) 
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
     const float s = group_scale(amax, a.e8m0 != 0);
     if (col < a.K) {
+      const float inv = __frcp_rn(s);
+      float c[8];
+      bool near = !(s >= 1e-30f && s <= 1e30f);  // (1 / s is a normal number)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = f[i] * inv;
+        near |= near_border(c[i]) && f[i] != 0.f;
+      }
+      if (near && (!a.e8m0 || !(s >= 1e-30f && s <= 1e30f))) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = __fdiv_rn(f[i], s);
+      }
       uint2 q;
-      q.x = f32x4_to_e4m3x4(__fdiv_rn(f[0], s), __fdiv_rn(f[1], s), __fdiv_rn(f[2], s), __fdiv_rn(f[3], s));
-      q.y = f32x4_to_e4m3x4(__fdiv_rn(f[4], s), __fdiv_rn(f[5], s), __fdiv_rn(f[6], s), __fdiv_rn(f[7], s));
+      q.x = f32x4_to_e4m3x4(c[0], c[1], c[2], c[3]);
+      q.y = f32x4_to_e4m3x4(c[4], c[5], c[6], c[7]);
       *reinterpret_cast<uint2*>(a.codes + m * a.K + col) = q;
     }
-    if (lane16 == 0) a.scales[gi] = s;
+    if (lane16 == 0) a.scales[(size_t)kb * a.mp + m] = s;  // k-blocks first: the product reads a block's scales as one run
   }
 }
 
 // ------------------------------------------------------------- product
-constexpr int kRows = 128;              // weight rows of a tile: the MMA's M
-constexpr int kWTile = kRows * 128;     // 16 KB
+constexpr int kRows = 128;              // rows of a row tile: the MMA's M
+constexpr int kRTile = kRows * 128;     // 16 KB
 constexpr int kNEpi = 8;                // epilogue warps
 constexpr int kThreads = 12 * 32;
 constexpr int kPW = 0, kMW = 1, kSW = 2, kEW0 = 4;
 
-template <int NT>
+// NT columns; TR: the tokens are the rows
+template <int NT, bool TR>
 struct Cfg {
-  static constexpr int kXBox = NT < 32 ? NT : 32;             // token rows of one activation copy
-  static constexpr int kStage = kWTile + NT * 128;            // ring stage: a weight and an activation tile
-  static constexpr int kNST = std::min(12, 204 * 1024 / kStage);
+  static constexpr int kCBox = TR ? NT : std::min(NT, 32);    // column rows of one copy (tokens: no more than there are)
+  static constexpr int kStage = kRTile + NT * 128;            // ring stage: a row tile and a column tile
+  static constexpr int kNST = std::min(12, 212 * 1024 / kStage);
+  // weight tiles in flight before the codes are waited for: the copies complete
+  // in order, so more of them delay the first cell's codes (11 of 11: one
+  // token 23.1 us, first cell 4.7 us after the start)
+  static constexpr int kAhead = std::min(kNST, 4);
   static constexpr int kTST = NT <= 128 ? 4 : 2;              // accumulator buffers in tensor memory
   static constexpr int kTCols = NT * kTST;                    // 64 .. 512, a power of two
   static constexpr int kHalf = NT / 2;                        // columns of an epilogue warp
-  static constexpr int kSWarps = NT <= 32 ? 1 : 2;            // warps that prepare scale products
+  static constexpr int kToks = TR ? kRows : NT;               // tokens of a cell
+  static constexpr int kXST = 8;                              // cells whose token scales are in flight
   static constexpr size_t kBars = (size_t)kNST * kStage;
-  static constexpr int kNBars = 2 * kNST + 3 * kTST + 3;
-  static constexpr size_t kScale = (kBars + kNBars * 8 + 15) / 16 * 16;  // [kTST][NT] fp32
-  static constexpr size_t kMisc = kScale + (size_t)kTST * NT * 4;
+  static constexpr int kNBars = 2 * kNST + 2 * kTST + 2 * kXST + 3;
+  static constexpr size_t kScale = (kBars + kNBars * 8 + 15) / 16 * 16;  // [kXST][kToks] fp32
+  static constexpr size_t kMisc = kScale + (size_t)kXST * kToks * 4;
   static constexpr size_t kSmem = 1024 + kMisc + 16;
+  // registers: 12 warps start with 168 a thread; with 128 accumulators the
+  // epilogue takes 216 of them and the other four warps keep 72
+  // (256 x 216 + 128 x 72 = 384 x 168)
+  static constexpr bool kSplitRegs = TR;
 };
 
 struct LinMaps {
   CUtensorMap w, x;
 };
 
-// The pieces of work of CTA c: whole (tile, chunk) pairs c, c + G, ..., then
-// its share of the cells of the remaining pairs, one pair after the other.
+// The pieces of work of CTA c: whole pairs c, c + G, ..., then its share of the
+// cells of the remaining pairs, one pair after the other.
 struct Pieces {
   const LinArgs& p;
   int c;
-  int i;               // next whole pair of this CTA
-  long long at, end;   // remaining cells [at, end) of the split pairs
-  int pair, k0, k1;    // the current piece
+  int i;             // next whole pair of this CTA
+  int at, end;       // remaining cells [at, end) of the split pairs
+  int pair, k0, k1;  // the current piece
+  int row, col;      // its row and column tile
   MOE_DEV Pieces(const LinArgs& a, int cta) : p(a), c(cta), i(0) {
-    at = p.split_cells * c / p.G_split;
-    end = p.split_cells * (c + 1) / p.G_split;
+    at = (int)((long long)p.split_cells * c / p.G_split);
+    end = (int)((long long)p.split_cells * (c + 1) / p.G_split);
     if (c >= p.G_split) at = end = 0;
   }
   MOE_DEV bool next() {
@@ -125,19 +163,30 @@ struct Pieces {
       pair = i++ * p.G + c;
       k0 = 0;
       k1 = p.nkb;
-      return true;
+    } else {
+      if (at >= end) return false;
+      const int t = at / p.nkb;
+      pair = p.waves * p.G + t;
+      k0 = at - t * p.nkb;
+      k1 = min(p.nkb, end - t * p.nkb);
+      at = t * p.nkb + k1;
     }
-    if (at >= end) return false;
-    const long long t = at / p.nkb;
-    pair = p.waves * p.G + (int)t;
-    k0 = (int)(at - t * p.nkb);
-    k1 = (int)min((long long)p.nkb, end - t * p.nkb);
-    at = t * p.nkb + k1;
+    // weight tiles follow one another within a token tile
+    const int w = pair % p.n_wt, t = pair / p.n_wt;
+    row = p.tok_rows ? t : w;
+    col = p.tok_rows ? w : t;
     return true;
   }
   // CTA that holds cell x of the split pairs
-  MOE_DEV int owner(long long x) const { return (int)(((x + 1) * p.G_split - 1) / p.split_cells); }
+  MOE_DEV int owner(int x) const { return (int)(((long long)(x + 1) * p.G_split - 1) / p.split_cells); }
 };
+
+// (a0, a1) += (d0, d1) * (f0, f1), one packed instruction
+MOE_DEV void fma2(float& a0, float& a1, float d0, float d1, float f0, float f1) {
+  asm("{ .reg .b64 a, d, f;\n mov.b64 a, {%0, %1};\n mov.b64 d, {%2, %3};\n mov.b64 f, {%4, %5};\n"
+      " fma.rn.f32x2 a, d, f, a;\n mov.b64 {%0, %1}, a; }"
+      : "+f"(a0), "+f"(a1) : "f"(d0), "f"(d1), "f"(f0), "f"(f1));
+}
 
 MOE_DEV void store_out(const LinArgs& p, long long m, int n, float v) {
   if (p.out_fp32)
@@ -146,26 +195,30 @@ MOE_DEV void store_out(const LinArgs& p, long long m, int n, float v) {
     reinterpret_cast<__nv_bfloat16*>(p.out)[m * p.N + n] = __float2bfloat16_rn(v);
 }
 
-template <int NT>
+template <int NT, bool TR>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __grid_constant__ LinMaps maps) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, TR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same in a warp)
   uint8_t* ring = smem;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBars);
   uint64_t* empty = full + C::kNST;
   uint64_t* tfull = empty + C::kNST;
   uint64_t* tempty = tfull + C::kTST;
-  uint64_t* sready = tempty + C::kTST;
-  uint64_t* mma_done = sready + C::kTST;
+  uint64_t* sfull = tempty + C::kTST;
+  uint64_t* sempty = sfull + C::kXST;
+  uint64_t* mma_done = sempty + C::kXST;
   uint64_t* pdone = mma_done + 1;  // the eight epilogue warps wrote their part of a piece
   uint64_t* pdec = pdone + 1;      // whether this CTA is the last of the pair to arrive
-  float* cstage = reinterpret_cast<float*>(smem + C::kScale);
+  float* xring = reinterpret_cast<float*>(smem + C::kScale);
   volatile int* s_misc = reinterpret_cast<volatile int*>(smem + C::kMisc);  // [0] tensor memory, [1] last to arrive
   int* status = p.status;
 
   if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.w) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.x) : "memory");
     for (int i = 0; i < C::kNST; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
@@ -173,7 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
     for (int i = 0; i < C::kTST; ++i) {
       mbar_init(tfull + i, 1);
       mbar_init(tempty + i, kNEpi);
-      mbar_init(sready + i, C::kSWarps);
+    }
+    for (int i = 0; i < C::kXST; ++i) {
+      mbar_init(sfull + i, 1);
+      mbar_init(sempty + i, kNEpi);
     }
     mbar_init(mma_done, 1);
     mbar_init(pdone, kNEpi);
@@ -191,184 +247,205 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
   tc_fence_after();
   const uint32_t tmem = (uint32_t)s_misc[0];
   Pieces pc(p, blockIdx.x);
+  // tokens of a token tile, live columns of a column tile
+  auto toks = [&](int t) { return min(p.chunk, p.M - t * p.chunk); };
+  auto cols = [&](int c) { return TR ? min(NT, p.N - c * NT) : toks(c); };
 
-  if (warp == kPW) {
-    // ================================================================ producer
-    // Weights do not depend on the kernel before this one (the quantisation):
-    // the ring's first tiles of them are in flight before it is waited for.
-    uint32_t gs = 0;
-    if (lane == 0) {
-      {
-        Pieces ahead(p, blockIdx.x);
-        int n = 0;
-        while (n < C::kNST && ahead.next()) {
-          const int tile = ahead.pair % p.n_tiles;
-          for (int kb = ahead.k0; kb < ahead.k1 && n < C::kNST; ++kb, ++n) {
-            const int chunk = ahead.pair / p.n_tiles;
-            const int ntok = min(p.chunk, p.M - chunk * p.chunk);
-            const int nbox = (ntok + C::kXBox - 1) / C::kXBox;
-            mbar_expect_tx(full + n, (uint32_t)(kWTile + nbox * C::kXBox * 128));
-            tma_load_2d(ring + (size_t)n * C::kStage, &maps.w, kb * kBlock, tile * kRows, full + n);
-          }
-        }
-      }
-      grid_dep_wait();
-      asm volatile("fence.proxy.async.global;" ::: "memory");  // codes of the kernel before are read with TMA
-      int si = 0;
-      uint32_t ph = 0;
-      bool alive = true;
-      while (alive && pc.next()) {
-        const int tile = pc.pair % p.n_tiles, chunk = pc.pair / p.n_tiles;
-        const int t0 = chunk * p.chunk;
-        const int ntok = min(p.chunk, p.M - t0);
-        const int nbox = (ntok + C::kXBox - 1) / C::kXBox;
-        for (int kb = pc.k0; kb < pc.k1; ++kb) {
+  if (warp < kEW0) {
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kPW) {
+      // ================================================================ producer
+      // Weights do not depend on the kernel before this one (the quantisation):
+      // the first tiles of them are in flight before it is waited for.
+      if (elect_one()) {
+        uint32_t gs = 0, ahead = 0;
+        auto load_w = [&](const Pieces& q, int kb, int si) {
           uint8_t* st = ring + (size_t)si * C::kStage;
-          if (gs >= (uint32_t)C::kNST) {
-            if (!mbar_wait_landed(empty + si, ph ^ 1u, status)) { alive = false; break; }
-            mbar_expect_tx(full + si, (uint32_t)(kWTile + nbox * C::kXBox * 128));
-            tma_load_2d(st, &maps.w, kb * kBlock, tile * kRows, full + si);
+          const int nbox = (cols(q.col) + C::kCBox - 1) / C::kCBox;
+          mbar_expect_tx(full + si, (uint32_t)(kRTile + nbox * C::kCBox * 128));
+          if (TR)
+            tma_load_2d(st + kRTile, &maps.w, kb * kBlock, q.col * NT, full + si);
+          else
+            tma_load_2d(st, &maps.w, kb * kBlock, q.row * kRows, full + si);
+        };
+        {
+          Pieces q(p, blockIdx.x);
+          while (ahead < (uint32_t)C::kAhead && q.next())
+            for (int kb = q.k0; kb < q.k1 && ahead < (uint32_t)C::kAhead; ++kb) load_w(q, kb, (int)ahead++);
+        }
+        grid_dep_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // codes of the kernel before are read with TMA
+        int si = 0;
+        uint32_t ph = 0;
+        bool alive = true;
+        while (alive && pc.next()) {
+          const int t0 = (TR ? pc.row : pc.col) * p.chunk;
+          const int nbox = TR ? 1 : (toks(pc.col) + C::kCBox - 1) / C::kCBox;
+          for (int kb = pc.k0; kb < pc.k1; ++kb) {
+            if (gs >= ahead) {
+              if (gs >= (uint32_t)C::kNST && !mbar_wait_landed(empty + si, ph ^ 1u, status)) { alive = false; break; }
+              load_w(pc, kb, si);
+            }
+            uint8_t* xt = ring + (size_t)si * C::kStage + (TR ? 0 : kRTile);
+            for (int b = 0; b < nbox; ++b)
+              tma_load_2d(xt + b * C::kCBox * 128, &maps.x, kb * kBlock, t0 + b * C::kCBox, full + si);
+            ++gs;
+            if (++si == C::kNST) { si = 0; ph ^= 1u; }
           }
-          for (int b = 0; b < nbox; ++b)
-            tma_load_2d(st + kWTile + b * C::kXBox * 128, &maps.x, kb * kBlock, t0 + b * C::kXBox, full + si);
-          ++gs;
-          if (++si == C::kNST) { si = 0; ph ^= 1u; }
         }
+        // every copy this CTA issued lands before it ends
+        for (uint32_t j = (gs > (uint32_t)C::kNST ? gs - C::kNST : 0); j < gs; ++j)
+          mbar_wait_landed(full + (j % C::kNST), (j / C::kNST) & 1u, status);
       }
-      // every copy this CTA issued lands before it ends
-      for (uint32_t j = (gs > (uint32_t)C::kNST ? gs - C::kNST : 0); j < gs; ++j)
-        mbar_wait_landed(full + (j % C::kNST), (j / C::kNST) & 1u, status);
-    }
-    __syncwarp();
-  } else if (warp == kMW) {
-    // ================================================================ MMA issue
-    if (lane == 0) {
-      int si = 0, ti = 0;
-      uint32_t ph = 0, tp = 0;
-      bool alive = true;
-      while (alive && pc.next()) {
-        const int chunk = pc.pair / p.n_tiles;
-        const int ntok = min(p.chunk, p.M - chunk * p.chunk);
-        const uint32_t idesc = instr_desc(kRows, (ntok + 15) & ~15);
-        for (int kb = pc.k0; kb < pc.k1; ++kb) {
-          if (!mbar_wait_landed(tempty + ti, tp ^ 1u, status) || !mbar_wait_landed(full + si, ph, status)) {
-            alive = false;
-            break;
+      __syncwarp();
+    } else if (warp == kMW) {
+      // ================================================================ MMA issue
+      if (elect_one()) {
+        int si = 0, ti = 0;
+        uint32_t ph = 0, tp = 0;
+        bool alive = true;
+        while (alive && pc.next()) {
+          const uint32_t idesc = instr_desc(kRows, (cols(pc.col) + 15) & ~15);
+          for (int kb = pc.k0; kb < pc.k1; ++kb) {
+            if (!mbar_wait_landed(tempty + ti, tp ^ 1u, status) || !mbar_wait_landed(full + si, ph, status)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sb = su32(ring + (size_t)si * C::kStage);
+            const uint64_t da = smem_desc(sb), db = smem_desc(sb + kRTile);
+            const uint32_t dt = tmem + (uint32_t)(ti * NT);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tc_mma(dt, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1 : 0);
+            tc_commit(empty + si);
+            tc_commit(tfull + ti);
+            if (++si == C::kNST) { si = 0; ph ^= 1u; }
+            if (++ti == C::kTST) { ti = 0; tp ^= 1u; }
           }
-          tc_fence_after();
-          const uint32_t sb = su32(ring + (size_t)si * C::kStage);
-          const uint64_t da = smem_desc(sb), db = smem_desc(sb + kWTile);
-          const uint32_t dt = tmem + (uint32_t)(ti * NT);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) tc_mma(dt, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1 : 0);
-          tc_commit(empty + si);
-          tc_commit(tfull + ti);
-          if (++si == C::kNST) { si = 0; ph ^= 1u; }
-          if (++ti == C::kTST) { ti = 0; tp ^= 1u; }
         }
+        // every MMA this thread issued is complete before the memory is freed
+        tc_commit(mma_done);
+        mbar_wait_landed(mma_done, 0, status);
       }
-      // every MMA this thread issued is complete before the memory is freed
-      tc_commit(mma_done);
-      mbar_wait_landed(mma_done, 0, status);
-    }
-    __syncwarp();
-  } else if (warp >= kSW && warp < kSW + C::kSWarps) {
-    // ================================================================ scale products
-    grid_dep_wait();
-    constexpr int kCols = NT / C::kSWarps;           // columns of this warp
-    constexpr int kPer = (kCols + 31) / 32;
-    const int c0 = (warp - kSW) * kCols;
-    int ti = 0;
-    uint32_t tp = 0;
-    bool alive = true;
-    while (alive && pc.next()) {
-      const int tile = pc.pair % p.n_tiles, chunk = pc.pair / p.n_tiles;
-      const int t0 = chunk * p.chunk;
-      const int ntok = min(p.chunk, p.M - t0);
-      const float* wr = p.w_s + (size_t)tile * p.nkb;
-      for (int kb = pc.k0; kb < pc.k1; ++kb) {
-        const float ws = ld_ca(wr + kb);
-        float v[kPer];
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int col = c0 + 32 * j + lane;
-          v[j] = 32 * j + lane < kCols && col < ntok ? ws * ld_ca(p.xs + (size_t)(t0 + col) * p.nkb + kb) : 0.f;
+      __syncwarp();
+    } else if (warp == kSW) {
+      // ================================================================ token scales
+      // A cell's xs run, copied up to kXST cells ahead of its epilogue (its own
+      // ring: it is held until the epilogue is done with the cell).
+      if (elect_one()) {
+        grid_dep_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        uint32_t n = 0;
+        bool alive = true;
+        while (alive && pc.next()) {
+          const int t = TR ? pc.row : pc.col;
+          const uint32_t bytes = (uint32_t)((toks(t) + 3) & ~3) * 4u;
+          for (int kb = pc.k0; kb < pc.k1; ++kb, ++n) {
+            const uint32_t xi = n % C::kXST;
+            if (!mbar_wait_landed(sempty + xi, ((n / C::kXST) & 1u) ^ 1u, status)) { alive = false; break; }
+            mbar_expect_tx(sfull + xi, bytes);
+            bulk_load(xring + xi * C::kToks, p.xs + (size_t)kb * p.mp + t * p.chunk, bytes, sfull + xi);
+          }
         }
-        if (!mbar_wait_landed(tempty + ti, tp ^ 1u, status)) { alive = false; break; }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (32 * j + lane < kCols) cstage[ti * NT + c0 + 32 * j + lane] = v[j];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sready + ti);
-        if (++ti == C::kTST) { ti = 0; tp ^= 1u; }
+        for (uint32_t j = (n > (uint32_t)C::kXST ? n - C::kXST : 0); j < n; ++j)
+          mbar_wait_landed(sfull + j % C::kXST, (j / C::kXST) & 1u, status);
       }
+      __syncwarp();
     }
-  } else if (warp >= kEW0) {
+  } else {
     // ================================================================ epilogue
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int qd = warp & 3, hf = (warp - kEW0) >> 2;
-    const int r = 32 * qd + lane;                 // row of the 128-row tile
+    const int r = 32 * qd + lane;                 // row of the row tile
     const int col0 = hf * C::kHalf;
-    constexpr int kStep = C::kHalf < 16 ? C::kHalf : 16;
+    constexpr int kStep = TR ? 32 : C::kHalf < 16 ? C::kHalf : 16;   // columns of one read of the accumulator
     float acc[C::kHalf];
     int ti = 0;
     uint32_t tp = 0, np = 0;  // np: split pieces so far (phases of pdone and pdec)
+    uint32_t nc = 0;          // cells so far
     bool alive = true;
     while (alive && pc.next()) {
-      const int tile = pc.pair % p.n_tiles, chunk = pc.pair / p.n_tiles;
-      const int t0 = chunk * p.chunk;
-      const int ntok = min(p.chunk, p.M - t0);
+      const int ncol = cols(pc.col) - col0;       // live columns of this warp (may be none)
+      // weight scales: lane i holds k-block i of a run of 32, the next run is
+      // read ahead; this warp's columns (TR) or the rows are one weight block
+      const int wblk = min(TR ? pc.col * (NT / kBlock) + hf : pc.row, p.n_wblk - 1);
+      const float* wr = p.w_s + (size_t)wblk * p.nkb;
+      float ws = pc.k0 + lane < pc.k1 ? __ldg(wr + pc.k0 + lane) : 0.f, wn = 0.f;
+      const bool whole = pc.k0 == 0 && pc.k1 == p.nkb;
+      int c_first = 0, c_last = 0;
+      if (!whole) {
+        const int x0 = (pc.pair - p.waves * p.G) * p.nkb;
+        c_first = pc.owner(x0);
+        c_last = pc.owner(x0 + p.nkb - 1);
+      }
 #pragma unroll
       for (int j = 0; j < C::kHalf; ++j) acc[j] = 0.f;
-      for (int kb = pc.k0; kb < pc.k1; ++kb) {
-        if (!mbar_wait_landed(tfull + ti, tp, status) || !mbar_wait_landed(sready + ti, tp, status)) {
-          alive = false;
-          break;
+      for (int kb = pc.k0; kb < pc.k1; ++kb, ++nc) {
+        const int off = (kb - pc.k0) & 31;
+        if (off == 0) {
+          if (kb != pc.k0) ws = wn;
+          wn = kb + 32 + lane < pc.k1 ? __ldg(wr + kb + 32 + lane) : 0.f;
         }
+        const float w = __shfl_sync(0xffffffffu, ws, off);
+        const uint32_t xi = nc % C::kXST;
+        const float* xs = xring + xi * C::kToks;
+        if (!mbar_wait_landed(sfull + xi, (nc / C::kXST) & 1u, status)) { alive = false; break; }
+        const float s = TR ? w * xs[r] : 0.f;
+        if (!mbar_wait_landed(tfull + ti, tp, status)) { alive = false; break; }
         tc_fence_after();
         const uint32_t ta = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(ti * NT + col0);
-        const float* cs = cstage + ti * NT + col0;
+        if constexpr (TR) {
+          // two reads of 32 columns in flight
+          float d[2][32];
+          tc_ld32(ta, d[0]);
 #pragma unroll
-        for (int j0 = 0; j0 < C::kHalf; j0 += kStep) {
-          if (col0 + j0 < ntok) {
-            float d[kStep];
-            if constexpr (kStep == 16) tc_ld16(ta + j0, d); else tc_ld8(ta + j0, d);
+          for (int j0 = 0; j0 < C::kHalf; j0 += kStep) {
+            const int k = (j0 / kStep) & 1;
             tc_wait_ld();
+            if (j0 + kStep < C::kHalf) tc_ld32(ta + j0 + kStep, d[k ^ 1]);
 #pragma unroll
-            for (int j = 0; j < kStep; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(cs + j0 + j);
-              acc[j0 + j] += d[j] * f.x;
-              acc[j0 + j + 1] += d[j + 1] * f.y;
-              acc[j0 + j + 2] += d[j + 2] * f.z;
-              acc[j0 + j + 3] += d[j + 3] * f.w;
+            for (int j = 0; j < kStep; j += 2) fma2(acc[j0 + j], acc[j0 + j + 1], d[k][j], d[k][j + 1], s, s);
+          }
+        } else {
+#pragma unroll
+          for (int j0 = 0; j0 < C::kHalf; j0 += kStep) {
+            if (j0 < ncol) {
+              float d[kStep];
+              if constexpr (kStep == 16) tc_ld16(ta + j0, d); else tc_ld8(ta + j0, d);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < kStep; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(xs + col0 + j0 + j);
+                fma2(acc[j0 + j], acc[j0 + j + 1], d[j], d[j + 1], f.x * w, f.y * w);
+                fma2(acc[j0 + j + 2], acc[j0 + j + 3], d[j + 2], d[j + 3], f.z * w, f.w * w);
+              }
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty + ti);
+        if (lane == 0) {
+          mbar_arrive(tempty + ti);
+          mbar_arrive(sempty + xi);
+        }
         if (++ti == C::kTST) { ti = 0; tp ^= 1u; }
       }
       if (!alive) break;
-      const int n = tile * kRows + r;
-      const bool whole = pc.k0 == 0 && pc.k1 == p.nkb;
-      int c_first = 0, c_last = 0;
       if (!whole) {
         // this piece's sums go to the workspace; the last CTA of the pair to
-        // arrive adds all pieces in k order
-        const long long x0 = (long long)(pc.pair - p.waves * p.G) * p.nkb;
-        c_first = pc.owner(x0);
-        c_last = pc.owner(x0 + p.nkb - 1);
-        // a CTA's pieces: slot 0 continues a pair of the CTA before it, slot 1 starts one
+        // arrive adds all pieces in k order.  A CTA's pieces: slot 0 continues
+        // a pair of the CTA before it, slot 1 starts one.  The counter's
+        // release and acquire reach the other warps through the barriers.
         float* part = p.partials + ((size_t)blockIdx.x * 2 + (pc.k0 == 0 ? 1 : 0)) * NT * kRows;
 #pragma unroll
-        for (int j = 0; j < C::kHalf; ++j)
-          if (col0 + j < ntok) __stcg(part + (size_t)(col0 + j) * kRows + r, acc[j]);
-        __threadfence();
+        for (int j = 0; j < C::kHalf; j += 4)
+          if (j < ncol)
+            __stcg(reinterpret_cast<float4*>(part) + (size_t)(col0 + j) / 4 * kRows + r,
+                   make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(pdone);
         if (!mbar_wait_landed(pdone, np & 1u, status)) break;
         if (tid == kEW0 * 32) {
-          __threadfence();
           const int got = atom_add_acq_rel(p.tickets + c_first, 1);
           const bool last = got == c_last - c_first;
           if (last) p.tickets[c_first] = 0;  // ready for the next call
@@ -378,20 +455,59 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
         if (!mbar_wait_landed(pdec, np & 1u, status)) break;
         ++np;
         if (!s_misc[1]) continue;
-        __threadfence();
 #pragma unroll
         for (int j = 0; j < C::kHalf; ++j) acc[j] = 0.f;
-        for (int c = c_first; c <= c_last; ++c) {
-          const float* ps = p.partials + ((size_t)c * 2 + (c == c_first ? 1 : 0)) * NT * kRows;
+        // up to 16 reads of 16 bytes in flight
+        constexpr int kJ = C::kHalf < 64 ? C::kHalf : 64, kC = 64 / kJ;
+        for (int c0 = c_first; c0 <= c_last; c0 += kC) {
 #pragma unroll
-          for (int j = 0; j < C::kHalf; ++j)
-            if (col0 + j < ntok) acc[j] += __ldcg(ps + (size_t)(col0 + j) * kRows + r);
+          for (int j0 = 0; j0 < C::kHalf; j0 += kJ) {
+            float4 v[kC][kJ / 4];
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+              const int c = min(c0 + i, c_last);
+              const float4* ps = reinterpret_cast<const float4*>(
+                  p.partials + ((size_t)c * 2 + (c == c_first ? 1 : 0)) * NT * kRows);
+#pragma unroll
+              for (int j = 0; j < kJ; j += 4)
+                v[i][j / 4] = j0 + j < ncol ? __ldcg(ps + (size_t)(col0 + j0 + j) / 4 * kRows + r)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kC; ++i)
+              if (c0 + i <= c_last)
+#pragma unroll
+                for (int j = 0; j < kJ; j += 4) {
+                  acc[j0 + j] += v[i][j / 4].x;
+                  acc[j0 + j + 1] += v[i][j / 4].y;
+                  acc[j0 + j + 2] += v[i][j / 4].z;
+                  acc[j0 + j + 3] += v[i][j / 4].w;
+                }
+          }
         }
       }
-      if (n < p.N) {
+      if constexpr (TR) {
+        const int m = pc.row * kRows + r, n0 = pc.col * NT + col0;
+        if (m < p.M) {
+          if (ncol >= C::kHalf && !p.out_fp32 && p.N % 8 == 0) {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + (size_t)m * p.N + n0);
 #pragma unroll
-        for (int j = 0; j < C::kHalf; ++j)
-          if (col0 + j < ntok) store_out(p, t0 + col0 + j, n, acc[j]);
+            for (int j = 0; j < C::kHalf; j += 8)
+              dst[j / 8] = make_uint4(pack_bf16(acc[j], acc[j + 1]), pack_bf16(acc[j + 2], acc[j + 3]),
+                                      pack_bf16(acc[j + 4], acc[j + 5]), pack_bf16(acc[j + 6], acc[j + 7]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < C::kHalf; ++j)
+              if (j < ncol) store_out(p, m, n0 + j, acc[j]);
+          }
+        }
+      } else {
+        const int n = pc.row * kRows + r;
+        if (n < p.N) {
+#pragma unroll
+          for (int j = 0; j < C::kHalf; ++j)
+            if (j < ncol) store_out(p, pc.col * p.chunk + col0 + j, n, acc[j]);
+        }
       }
     }
     tc_fence_before();
@@ -403,41 +519,41 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
   }
 }
 
-template <int NT>
+template <int NT, bool TR>
 cudaError_t launch_nt(const LinPlan& p, const LinArgs& a, const LinMaps& maps, bool pdl, cudaStream_t s) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, TR>;
   // a process-wide attribute of the kernel, set once (an atomic static)
   static const cudaError_t rc =
-      cudaFuncSetAttribute(linear_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+      cudaFuncSetAttribute(linear_kernel<NT, TR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (rc != cudaSuccess) return rc;
   if (pdl) {
     PdlLaunch L(dim3(p.G), dim3(kThreads), C::kSmem, s);
-    return cudaLaunchKernelEx(&L.cfg, linear_kernel<NT>, a, maps);
+    return cudaLaunchKernelEx(&L.cfg, linear_kernel<NT, TR>, a, maps);
   }
-  linear_kernel<NT><<<p.G, kThreads, C::kSmem, s>>>(a, maps);
+  linear_kernel<NT, TR><<<p.G, kThreads, C::kSmem, s>>>(a, maps);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Token columns of a chunk: the smallest MMA width that holds all tokens, up
-// to 256; above, equal chunks of at most 256 (a multiple of 16).
+// Up to 128 tokens: the tokens are the columns, at the smallest width that holds
+// them.  Above: token tiles of 128 rows, weight tiles of 256 columns.
 void plan_linear(LinPlan& p, int M, int N, int K, int sms) {
   p.M = M; p.N = N; p.K = K;
   p.nkb = (K + kBlock - 1) / kBlock;
+  p.tok_rows = M > 128;
   p.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
-  p.n_chunks = (M + p.nt - 1) / p.nt;
-  p.chunk = ((M + p.n_chunks - 1) / p.n_chunks + 15) & ~15;
-  p.n_chunks = (M + p.chunk - 1) / p.chunk;
-  p.n_tiles = (N + kRows - 1) / kRows;
-  const long long pairs = (long long)p.n_chunks * p.n_tiles;
+  p.chunk = std::min(p.nt, kRows);
+  p.n_tt = (M + p.chunk - 1) / p.chunk;
+  p.n_wt = p.tok_rows ? (N + 255) / 256 : (N + kRows - 1) / kRows;
+  const long long pairs = (long long)p.n_tt * p.n_wt;
   const long long cells = pairs * p.nkb;
   p.G = (int)std::min<long long>({cells, (long long)sms, (long long)kLinMaxCtas});
   p.waves = (int)(pairs / p.G);
-  p.split_cells = (pairs - (long long)p.waves * p.G) * p.nkb;
-  // at least kLinMinRun cells a CTA: shorter pieces cost more to add than they save
   const long long rest = pairs - (long long)p.waves * p.G;
-  p.G_split = (int)std::max<long long>(1, std::min<long long>(p.G, std::max(p.split_cells / kLinMinRun, rest)));
+  p.split_cells = (int)(rest * p.nkb);
+  // at least kLinMinRun cells a CTA: shorter pieces cost more to add than they save
+  p.G_split = (int)std::max<long long>(1, std::min<long long>(p.G, std::max(rest * p.nkb / kLinMinRun, rest)));
 }
 
 size_t linear_partial_bytes(const LinPlan& p) {
@@ -456,19 +572,20 @@ cudaError_t launch_linear(const LinPlan& p, const uint8_t* xq, const float* xs, 
                           void* out, int out_fp32, int* status, int* tickets, float* partials, bool pdl,
                           cudaStream_t s) {
   LinMaps maps;
-  if (!tmap_2d(&maps.w, w, p.K, p.N, 128, kRows) || !tmap_2d(&maps.x, xq, p.K, p.M, 128, p.nt < 32 ? p.nt : 32))
+  if (!tmap_2d(&maps.w, w, p.K, p.N, 128, p.tok_rows ? 256 : kRows) ||
+      !tmap_2d(&maps.x, xq, p.K, p.M, 128, p.tok_rows ? kRows : std::min(p.nt, 32)))
     return cudaErrorInvalidValue;
   LinArgs a;
-  a.xs = xs; a.w_s = w_s; a.out = out; a.out_fp32 = out_fp32;
-  a.M = p.M; a.N = p.N; a.nkb = p.nkb; a.chunk = p.chunk; a.n_tiles = p.n_tiles;
-  a.G = p.G; a.waves = p.waves; a.G_split = p.G_split; a.split_cells = p.split_cells;
+  a.xs = xs; a.mp = linear_scale_stride(p.M); a.w_s = w_s; a.out = out; a.out_fp32 = out_fp32;
+  a.M = p.M; a.N = p.N; a.nkb = p.nkb; a.chunk = p.chunk; a.n_wt = p.n_wt; a.n_wblk = (p.N + kBlock - 1) / kBlock;
+  a.tok_rows = p.tok_rows; a.G = p.G; a.waves = p.waves; a.G_split = p.G_split; a.split_cells = p.split_cells;
   a.status = status; a.tickets = tickets; a.partials = partials;
   switch (p.nt) {
-    case 16: return launch_nt<16>(p, a, maps, pdl, s);
-    case 32: return launch_nt<32>(p, a, maps, pdl, s);
-    case 64: return launch_nt<64>(p, a, maps, pdl, s);
-    case 128: return launch_nt<128>(p, a, maps, pdl, s);
-    default: return launch_nt<256>(p, a, maps, pdl, s);
+    case 16: return launch_nt<16, false>(p, a, maps, pdl, s);
+    case 32: return launch_nt<32, false>(p, a, maps, pdl, s);
+    case 64: return launch_nt<64, false>(p, a, maps, pdl, s);
+    case 128: return launch_nt<128, false>(p, a, maps, pdl, s);
+    default: return launch_nt<256, true>(p, a, maps, pdl, s);
   }
 }
 

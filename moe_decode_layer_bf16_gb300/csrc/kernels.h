@@ -197,29 +197,34 @@ struct QuantArgs {
   long long ldx;
   int M, K, nkb, e8m0;
   uint8_t* codes;  // [M, K]
-  float* scales;   // [M, nkb]
+  float* scales;   // [nkb][mp]
+  int mp;          // linear_scale_stride(M)
 };
+// tokens of a row of activation scales: M rounded up so that runs start on 16 bytes
+inline int linear_scale_stride(int M) { return (M + 3) & ~3; }
 cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s);
 
 constexpr int kLinMaxCtas = 160;  // CTAs of the product at most (one per SM)
-constexpr int kLinMinRun = 2;     // k-blocks of a CTA's share of the split pairs at least
+constexpr int kLinMinRun = 8;     // k-blocks of a CTA's share of the split pairs at least
 struct LinPlan {
   int M, N, K, nkb;
-  int nt;             // the kernel's token columns: 16, 32, 64, 128 or 256
-  int chunk;          // tokens of a chunk (<= nt)
-  int n_chunks, n_tiles;
+  bool tok_rows;      // the tokens are the MMA's rows (else its columns)
+  int nt;             // the kernel's columns: 16, 32, 64, 128 (tokens) or 256 (weight rows)
+  int chunk;          // tokens of a token tile
+  int n_tt, n_wt;     // token tiles, weight tiles
   int G;              // CTAs
-  int waves;          // whole (row tile, chunk) pairs of each CTA
+  int waves;          // whole (row tile, column tile) pairs of each CTA
   int G_split;        // CTAs that share the cells of the remaining pairs
-  long long split_cells;
+  int split_cells;
 };
 struct LinArgs {
-  const float* xs;   // [M, nkb]
-  const float* w_s;  // [ceil(N / 128), nkb]
+  const float* xs;   // [nkb][mp]
+  int mp;
+  const float* w_s;  // [n_wblk][nkb]
   void* out;
   int out_fp32;
-  int M, N, nkb, chunk, n_tiles, G, waves, G_split;
-  long long split_cells;
+  int M, N, nkb, chunk, n_wt, n_wblk, G, waves, G_split, split_cells;
+  bool tok_rows;
   int* status;
   int* tickets;      // [G], zero between calls
   float* partials;   // [G_split][2][nt][128]
