@@ -44,6 +44,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "async.cuh"
 #include "common.cuh"
@@ -65,7 +66,7 @@ constexpr float kPScale = 32768.f;        // weights are rounded to f16 in units
 
 // A piece of an item that a warp (or, in the workspace, a CTA) could not finish.
 struct Piece {
-  long long item0;   // first unit of the item, -1: no piece
+  int item0;         // first unit of the item, -1: no piece
   int units;         // of the item
   int start, row0, rows, head;
 };
@@ -84,7 +85,7 @@ struct AttCfg {
   static constexpr size_t kRecAt = kPartAt + (size_t)kWarps * kPartF * 4;
   static constexpr size_t kBarsAt = kRecAt + 2 * kWarps * sizeof(Piece);
   static constexpr size_t kMiscAt = kBarsAt + kWarps * kNST * 8;
-  static constexpr size_t kSmem = 1024 + kMiscAt + kWarps * 16 + 16;
+  static constexpr size_t kSmem = 1024 + kMiscAt + (2 * kWarps + 4) * 4;
   static_assert(kPartF * 4 <= kNST * kStage && kPartF % 4 == 0 && kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -154,24 +155,24 @@ MOE_DEV Seq load_seq(const AttArgs& a, int b, bool report) {
 // The pieces of a warp: units [u0, u1) of an item (b, head, group), of which
 // the first kItemCost are no tiles.
 struct Walk {
-  long long left;      // units still to hand out, this piece included
+  int left;            // units still to hand out, this piece included
   int b, head, grp;
   int u0, u1;
-  long long item0;     // first unit of the item, counted over all items
+  int item0;           // first unit of the item, counted over all items
   Seq s;
 };
 template <int D, int RT>
-MOE_DEV void walk_start(Walk& w, const AttArgs& a, int b, long long b_first, long long x, long long count) {
+MOE_DEV void walk_start(Walk& w, const AttArgs& a, int b, int b_first, int x, int count) {
   w.left = count;
   w.b = b;
   w.s = load_seq<D, RT>(a, b, false);
   const int units = w.s.tiles + kItemCost;
-  const long long it = (x - b_first) / units;
-  w.head = (int)(it / w.s.groups);
-  w.grp = (int)(it % w.s.groups);
+  const int it = (x - b_first) / units;
+  w.head = it / w.s.groups;
+  w.grp = it - w.head * w.s.groups;
   w.item0 = b_first + it * units;
-  w.u0 = (int)(x - w.item0);
-  w.u1 = (int)min((long long)units, w.u0 + count);
+  w.u0 = x - w.item0;
+  w.u1 = min(units, w.u0 + count);
 }
 template <int D, int RT>
 MOE_DEV bool walk_next(Walk& w, const AttArgs& a) {  // to the next piece
@@ -182,15 +183,23 @@ MOE_DEV bool walk_next(Walk& w, const AttArgs& a) {  // to the next piece
     w.grp = 0;
     if (++w.head == a.kv_heads) {
       w.head = 0;
-      do {
-        ++w.b;
+      do {  // (a sequence without rows has no units; one with rows follows, since units are left)
+        if (++w.b >= a.B) return false;
         w.s = load_seq<D, RT>(a, w.b, false);
-      } while (w.s.groups == 0);  // (a sequence without rows has no units; left > 0: one with rows follows)
+      } while (w.s.groups == 0);
     }
   }
   w.u0 = 0;
-  w.u1 = (int)min((long long)w.s.tiles + kItemCost, w.left);
+  w.u1 = min(w.s.tiles + kItemCost, w.left);
   return true;
+}
+// total * c / G without 64-bit divisions: c, G <= kAttMaxCtas
+MOE_DEV int cta_share(int q, int r, int G, int c) { return q * c + r * c / G; }
+// the CTA whose share holds unit x
+MOE_DEV int cta_of(int q, int r, int G, int x) {
+  int c = min(x / q, G - 1);
+  while (cta_share(q, r, G, c) > x) --c;
+  return c;
 }
 
 // Where a row of an item goes.
@@ -231,8 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   uint8_t* ring = smem + (size_t)warp * kNST * C::kStage;                      // this warp's
   Piece* recs = reinterpret_cast<Piece*>(smem + C::kRecAt);                     // [warp][first, last]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt) + warp * kNST;
-  long long* s_first = reinterpret_cast<long long*>(smem + C::kMiscAt);         // [warp] first unit of sequence s_b
-  int* s_b = reinterpret_cast<int*>(s_first + kWarps);                           // [warp], then [1] last to arrive
+  int* s_first = reinterpret_cast<int*>(smem + C::kMiscAt);                      // [warp] first unit of sequence s_b
+  int* s_b = s_first + kWarps;                                                   // [warp]
+  int* s_last = s_b + kWarps;                                                    // [2] last CTA to arrive, by piece
   int* status = a.status;
   auto part_of = [&](int w, int last) {  // where warp w leaves its first or last piece
     return reinterpret_cast<float*>(last ? smem + (size_t)w * kNST * C::kStage
@@ -268,18 +278,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
+  if (total > INT_MAX) {  // rows counted more than once: q_start does not ascend
+    if (tid == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
+    return;
+  }
   // CTAs that get work
   const int G = (int)min((long long)gridDim.x, (total + kWarps * kMinUnits - 1) / (kWarps * kMinUnits));
   if ((int)blockIdx.x >= G) return;  // (the whole CTA; nothing is in flight)
-  const long long X0 = total * blockIdx.x / G, X1 = total * (blockIdx.x + 1) / G;
-  auto share = [&](int w) { return X0 + (X1 - X0) * w / kWarps; };
-  for (int w = 0; w < kWarps; ++w) {
-    const long long x = share(w);
-    if (x >= before && x < before + mine) {  // one thread for each w
-      long long at = before;
+  const int Xq = (int)total / G, Xr = (int)total - Xq * G;
+  const int X0 = cta_share(Xq, Xr, G, blockIdx.x), X1 = cta_share(Xq, Xr, G, blockIdx.x + 1);
+  auto share = [&](int w) { return X0 + ((X1 - X0) >> 3) * w + (((X1 - X0) & 7) * w >> 3); };
+  static_assert(kWarps == 8, "share");
+  if (mine > 0 && before < X1 && before + mine > X0) {
+    for (int w = 0; w < kWarps; ++w) {
+      const int x = share(w);
+      if (x < before || x >= before + mine) continue;  // one thread for each w
+      int at = (int)before;
       for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq<D, RT>(a, b, false);
-        const long long nb = (long long)(s.tiles + kItemCost) * s.groups * a.kv_heads;
+        const int nb = (s.tiles + kItemCost) * s.groups * a.kv_heads;
         if (x < at + nb) {
           s_first[w] = at;
           s_b[w] = b;
@@ -311,31 +328,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
     const int lo_any = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
     const int t0 = w.s.tile0 + max(0, w.u0 - kItemCost), t1 = w.s.tile0 + max(0, w.u1 - kItemCost);
 
+    // ---- Q rows on their way before the cache's stream starts
+    uint4 qv[RT][D / 64][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = w.grp * kRowsC + rt * 8 + g;
+      const bool live = rt * 8 + g < rows;
+      const int i = live ? r / a.G : 0, hq = w.head * a.G + (live ? r - i * a.G : 0);
+      const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (long long)(w.s.start + i) * a.q_stride + hq * D;
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qv[rt][h][e] = live ? __ldg(reinterpret_cast<const uint4*>(qp + 64 * h + 16 * q + 8 * e)) : make_uint4(0, 0, 0, 0);
+    }
     // ---- pages: lane i looks up 16-token group i of a batch of 32 / kGroups
-    // tiles; the next batch is read while this one is used
+    // tiles.  The next batch's page numbers are read as this one begins, its
+    // scales half-way through, so that neither read is waited for.
     constexpr int kBatch = 32 / kGroups;
     struct Look { int page; float ks, vs; uint32_t ok; };
-    auto look = [&](int tb) {
-      Look k;
+    auto look_page = [&](Look& k, int tb) {
       const int pos = tb * kTile + 16 * lane;
-      bool ok = tb + lane / kGroups < t1 && pos < w.s.len && pos + 16 > lo_any;
-      k.page = 0;
+      k.page = -2;  // not wanted
+      if (tb + lane / kGroups < t1 && pos < w.s.len && pos + 16 > lo_any)
+        k.page = __ldg(a.page_table + (size_t)w.b * a.width + pos / P);
+    };
+    auto look_scale = [&](Look& k) {
+      bool ok = k.page >= 0 && k.page < a.num_pages;
+      if (!ok && k.page != -2) atomicExch(status, MOE_ERR_INVALID_ARG);  // its tokens are masked
       k.ks = k.vs = 0.f;
       if (ok) {
-        k.page = __ldg(a.page_table + (size_t)w.b * a.width + pos / P);
-        if (k.page < 0 || k.page >= a.num_pages) {  // its tokens are masked
-          atomicExch(status, MOE_ERR_INVALID_ARG);
-          ok = false;
-          k.page = 0;
-        } else {
-          k.ks = __ldg(a.k_scale + (size_t)k.page * a.kv_heads + w.head);
-          k.vs = __ldg(a.v_scale + (size_t)k.page * a.kv_heads + w.head);
-        }
+        k.ks = __ldg(a.k_scale + (size_t)k.page * a.kv_heads + w.head);
+        k.vs = __ldg(a.v_scale + (size_t)k.page * a.kv_heads + w.head);
       }
       k.ok = __ballot_sync(0xffffffffu, ok);
-      return k;
     };
-    Look cur = look(t0), nxt = look(t0 + kBatch);
+    Look cur, nxt;
+    look_page(cur, t0);
+    look_scale(cur);
     int cur0 = t0;  // first tile of cur
     int ti = t0;    // next tile to copy
     auto issue = [&]() {
@@ -361,7 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
       ++issued;
       ++ti;
     };
+    nxt = cur;
     for (int i = 0; i < kNST && ti < t1; ++i) issue();
+    look_page(nxt, t0 + kBatch);
 
     // ---- Q fragments: rows g of each row tile, upper part in a0 / a2, lower in a1 / a3
     uint32_t qf[RT][D / 32][4];
@@ -372,19 +404,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
     for (int rt = 0; rt < RT; ++rt) {
       const int r = w.grp * kRowsC + rt * 8 + g;
       const bool live = rt * 8 + g < rows;
-      const int i = live ? r / a.G : 0, hq = w.head * a.G + (live ? r % a.G : 0);
+      const int i = live ? r / a.G : 0, hq = w.head * a.G + (live ? r - i * a.G : 0);
       pos_r[rt] = live ? pos0 + i : -1;
       slope[rt] = 0.f;
       if (MODS && a.slopes && live) slope[rt] = __ldg(a.slopes + hq) * kLog2e;
-      const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (long long)(w.s.start + i) * a.q_stride + hq * D;
-      uint4 v[D / 64][2];
+      const uint4(&v)[D / 64][2] = qv[rt];
       float amax = 0.f;
       bool odd = false;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          v[h][e] = live ? __ldg(reinterpret_cast<const uint4*>(qp + 64 * h + 16 * q + 8 * e)) : make_uint4(0, 0, 0, 0);
           const uint32_t x[4] = {v[h][e].x, v[h][e].y, v[h][e].z, v[h][e].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -440,8 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
       if (t - cur0 == kBatch) {
         cur = nxt;
         cur0 = t;
-        nxt = look(t + kBatch);
+        look_page(nxt, t + kBatch);
       }
+      if (t - cur0 == kBatch / 2) look_scale(nxt);
       const int r0 = (t - cur0) * kGroups;
       const int mask = (int)((cur.ok >> r0) & ((1u << kGroups) - 1));
       float ksg[kGroups], vsg[kGroups];
@@ -651,75 +682,81 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   for (; used < issued; ++used) mbar_wait_landed(full + used % kNST, (used / kNST) & 1u, status);
   __syncthreads();
 
-  // ---- the CTA's pieces: neighbours of one item are added in order
-  constexpr int kVec = D / 4;  // float4 of a row
-  for (int i0 = 0; i0 < 2 * kWarps;) {
-    const long long item = recs[i0].item0;
-    int i1 = i0 + 1;
-    if (item < 0) { i0 = i1; continue; }
-    while (i1 < 2 * kWarps && (recs[i1].item0 == item || recs[i1].item0 < 0)) ++i1;
-    const Piece rec = recs[i0];
-    const bool here = item >= X0 && item + rec.units <= X1;  // the whole item is this CTA's
-    for (int i = tid; i < kRowsC * kVec; i += kThreads) {
-      const int r = i / kVec, d = (i % kVec) * 4;
-      if (r >= rec.rows) continue;
-      float M = -INFINITY;
-      for (int x = i0; x < i1; ++x)
-        if (recs[x].item0 == item) M = fmaxf(M, part_of(x >> 1, x & 1)[kRowsC * D + 2 * r]);
-      const float ms = M == -INFINITY ? 0.f : M;
-      float L = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = i0; x < i1; ++x)
-        if (recs[x].item0 == item) {
-          const float* p = part_of(x >> 1, x & 1);
-          add_piece(acc, L, *reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r),
-                    *reinterpret_cast<const float4*>(p + r * D + d), ms);
-        }
-      if (here) {
-        store4(a, rec, r, D, d, acc, M, L);
-      } else {
-        // slot 0 continues an item of the CTA before this one, slot 1 starts one
-        float* p = a.partials + ((size_t)blockIdx.x * 2 + (item >= X0 ? 1 : 0)) * C::kPartF;
-        __stcg(reinterpret_cast<float4*>(p + (size_t)r * D + d), acc);
-        if (d == 0) __stcg(reinterpret_cast<float2*>(p + kRowsC * D + 2 * r), make_float2(M, L));
-      }
+  // ---- the CTA's pieces: those of one item are added, in order.  Every warp
+  // finds the items for itself: lane x looks at piece x.
+  constexpr int kVec = D / 4, kRowVec = kRowsC * kVec;  // float4 of a row, of an item
+  static_assert(kRowVec % 32 == 0 && 2 * kWarps <= 32, "a warp works on one item at a time");
+  const int my_item = lane < 2 * kWarps ? recs[lane].item0 : -1;
+  const uint32_t same = __match_any_sync(0xffffffffu, my_item);
+  const bool lead = my_item >= 0 && __ffs(same) - 1 == lane;
+  const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+  // items that reach beyond this CTA: at most one from before it, one past it
+  const bool out = lead && (my_item < X0 || my_item + recs[lane & (2 * kWarps - 1)].units > X1);
+  const uint32_t outs = __ballot_sync(0xffffffffu, out);
+  const int n_items = __popc(leads);
+  for (int i = tid; i < n_items * kRowVec; i += kThreads) {
+    const int x0 = __fns(leads, 0, i / kRowVec + 1);  // first piece of the item
+    const Piece rec = recs[x0];
+    const uint32_t pieces = __shfl_sync(0xffffffffu, same, x0);
+    const int j = i % kRowVec, r = j / kVec, d = (j % kVec) * 4;
+    if (r >= rec.rows) continue;
+    float M = -INFINITY;
+    for (uint32_t k = pieces; k; k &= k - 1) {
+      const int x = __ffs(k) - 1;
+      M = fmaxf(M, part_of(x >> 1, x & 1)[kRowsC * D + 2 * r]);
     }
-    if (!here) {
-      const long long e = item + rec.units - 1;
-      const int c_first = (int)(((item + 1) * G - 1) / total), c_last = (int)(((e + 1) * G - 1) / total);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        const bool last = atom_add_acq_rel(a.tickets + c_first, 1) == c_last - c_first;
-        if (last) a.tickets[c_first] = 0;  // ready for the next call
-        s_b[kWarps] = last;
-      }
-      __syncthreads();
-      if (s_b[kWarps]) {
-        __threadfence();
-        for (int i = tid; i < kRowsC * kVec; i += kThreads) {
-          const int r = i / kVec, d = (i % kVec) * 4;
-          if (r >= rec.rows) continue;
-          float M = -INFINITY;
-#pragma unroll 4
-          for (int c = c_first; c <= c_last; ++c)
-            M = fmaxf(M, __ldcg(a.partials + ((size_t)c * 2 + (c == c_first)) * C::kPartF + kRowsC * D + 2 * r));
-          const float ms = M == -INFINITY ? 0.f : M;
-          float L = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int c = c_first; c <= c_last; ++c) {
-            const float* p = a.partials + ((size_t)c * 2 + (c == c_first)) * C::kPartF;
-            add_piece(acc, L, __ldcg(reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r)),
-                      __ldcg(reinterpret_cast<const float4*>(p + (size_t)r * D + d)), ms);
-          }
-          store4(a, rec, r, D, d, acc, M, L);
-        }
-      }
-      __syncthreads();  // (the flag is used again)
+    const float ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t k = pieces; k; k &= k - 1) {
+      const int x = __ffs(k) - 1;
+      const float* p = part_of(x >> 1, x & 1);
+      add_piece(acc, L, *reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r),
+                *reinterpret_cast<const float4*>(p + r * D + d), ms);
     }
-    i0 = i1;
+    if ((outs >> x0 & 1) == 0) {
+      store4(a, rec, r, D, d, acc, M, L);
+    } else {
+      // slot 0 continues an item of the CTA before this one, slot 1 starts one
+      float* p = a.partials + ((size_t)blockIdx.x * 2 + (rec.item0 >= X0 ? 1 : 0)) * C::kPartF;
+      __stcg(reinterpret_cast<float4*>(p + (size_t)r * D + d), acc);
+      if (d == 0) __stcg(reinterpret_cast<float2*>(p + kRowsC * D + 2 * r), make_float2(M, L));
+    }
+  }
+  if (outs == 0) return;
+  // ---- across CTAs: the last to arrive adds an item's pieces.  The counter's
+  // release and acquire reach the other threads through the barriers.
+  __syncthreads();
+  const int n_out = __popc(outs);
+  if (tid < 32 * n_out && lane == 0) {
+    const Piece rec = recs[__fns(outs, 0, warp + 1)];
+    const int c0 = cta_of(Xq, Xr, G, rec.item0), c1 = cta_of(Xq, Xr, G, rec.item0 + rec.units - 1);
+    const bool last = atom_add_acq_rel(a.tickets + c0, 1) == c1 - c0;
+    if (last) a.tickets[c0] = 0;  // ready for the next call
+    s_last[warp] = last ? c0 | c1 << 16 : -1;
+  }
+  __syncthreads();
+  for (int i = tid; i < n_out * kRowVec; i += kThreads) {
+    const int last = s_last[i / kRowVec];
+    if (last < 0) continue;
+    const Piece rec = recs[__fns(outs, 0, i / kRowVec + 1)];
+    const int c0 = last & 0xffff, c1 = last >> 16;
+    const int j = i % kRowVec, r = j / kVec, d = (j % kVec) * 4;
+    if (r >= rec.rows) continue;
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int c = c0; c <= c1; ++c)
+      M = fmaxf(M, __ldcg(a.partials + ((size_t)c * 2 + (c == c0)) * C::kPartF + kRowsC * D + 2 * r));
+    const float ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int c = c0; c <= c1; ++c) {
+      const float* p = a.partials + ((size_t)c * 2 + (c == c0)) * C::kPartF;
+      add_piece(acc, L, __ldcg(reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r)),
+                __ldcg(reinterpret_cast<const float4*>(p + (size_t)r * D + d)), ms);
+    }
+    store4(a, rec, r, D, d, acc, M, L);
   }
 }
 
