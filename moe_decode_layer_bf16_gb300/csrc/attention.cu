@@ -49,6 +49,7 @@
 #include "async.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 #include "tmap.h"
 #include "../../include/moe_decode.h"
 
@@ -59,7 +60,7 @@ namespace {
 constexpr int kWarps = 8;                 // (255 registers a thread)
 constexpr int kThreads = kWarps * 32;
 constexpr int kItemCost = 2;              // units of an item beside its tiles
-constexpr int kMinUnits = 2;              // units of a warp at least
+constexpr int kMinUnits = 1;              // units of a warp at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.f;        // weights are rounded to f16 in units of 2^-15
@@ -85,7 +86,7 @@ struct AttCfg {
   static constexpr size_t kRecAt = kPartAt + (size_t)kWarps * kPartF * 4;
   static constexpr size_t kBarsAt = kRecAt + 2 * kWarps * sizeof(Piece);
   static constexpr size_t kMiscAt = kBarsAt + kWarps * kNST * 8;
-  static constexpr size_t kSmem = 1024 + kMiscAt + (2 * kWarps + 4) * 4;
+  static constexpr size_t kSmem = 1024 + kMiscAt + 16;
   static_assert(kPartF * 4 <= kNST * kStage && kPartF % 4 == 0 && kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -104,6 +105,11 @@ MOE_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// tanh(y / (2 log2 e)) = 1 - 2 / (1 + 2^y): off by about 2^-23, absolutely
+MOE_DEV float tanh_of(float y) {
+  y = y > 80.f ? 80.f : y;  // (2^y stays finite, a NaN stays one)
+  return 1.f - __fdividef(2.f, 1.f + ex2(y));
 }
 // two E4M3 pairs (the lower and the upper half of w) to two f16 pairs
 MOE_DEV void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -214,20 +220,40 @@ struct OutRow {
   }
 };
 
-// Adds a piece of a row, with its own (maximum, sum) `st`, relative to the maximum ms.
-MOE_DEV void add_piece(float4& acc, float& L, float2 st, float4 o, float ms) {
-  const float e = ex2(st.x - ms);
-  L += e * st.y;
-  acc.x += o.x * e; acc.y += o.y * e; acc.z += o.z * e; acc.w += o.w * e;
-}
+// Four columns of a row over several pieces, each with its own maximum and sum.
+// Lane k of 16 holds piece k's (maximum, sum) of a row; with 32 lanes to a row the
+// upper 16 do the same again.
+struct Joined {
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  MOE_DEV float weight16(float2 st) {  // this lane's piece's weight; M, L and acc follow
+    float Mn = st.x;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+    Mn = fmaxf(Mn, M);
+    const float ms = Mn == -INFINITY ? 0.f : Mn, e0 = ex2(M - ms);
+    M = Mn;
+    const float e = ex2(st.x - ms);
+    float l = e * st.y;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    L = L * e0 + l;
+    acc.x *= e0; acc.y *= e0; acc.z *= e0; acc.w *= e0;
+    return e;
+  }
+  MOE_DEV void add(float e, int k, float4 o) {
+    const float f = __shfl_sync(0xffffffffu, e, (threadIdx.x & 16) | k);
+    acc.x += o.x * f; acc.y += o.y * f; acc.z += o.z * f; acc.w += o.w * f;
+  }
+};
 
 // Four columns of a finished row, and (first column) its log-sum-exp.
-MOE_DEV void store4(const AttArgs& a, const Piece& p, int r, int D, int d, float4 acc, float M, float L) {
+MOE_DEV void store4(const AttArgs& a, const Piece& p, int r, int D, int d, const Joined& J) {
   const OutRow at(a, p.start, p.row0 + r, p.head);
-  const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+  const float inv = J.L == 0.f ? 0.f : __fdiv_rn(1.f, J.L);
   *reinterpret_cast<uint2*>(at.out(a, D) + d) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (d == 0) at.lse(a, M, L);
+      make_uint2(pack_bf16(J.acc.x * inv, J.acc.y * inv), pack_bf16(J.acc.z * inv, J.acc.w * inv));
+  if (d == 0) at.lse(a, J.M, J.L);
 }
 
 template <int D, int RT, bool MODS>
@@ -240,9 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   uint8_t* ring = smem + (size_t)warp * kNST * C::kStage;                      // this warp's
   Piece* recs = reinterpret_cast<Piece*>(smem + C::kRecAt);                     // [warp][first, last]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt) + warp * kNST;
-  int* s_first = reinterpret_cast<int*>(smem + C::kMiscAt);                      // [warp] first unit of sequence s_b
-  int* s_b = s_first + kWarps;                                                   // [warp]
-  int* s_last = s_b + kWarps;                                                    // [2] last CTA to arrive, by piece
+  int* s_last = reinterpret_cast<int*>(smem + C::kMiscAt);                       // [2] last CTA to arrive, by piece
   int* status = a.status;
   auto part_of = [&](int w, int last) {  // where warp w leaves its first or last piece
     return reinterpret_cast<float*>(last ? smem + (size_t)w * kNST * C::kStage
@@ -257,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
 
   // ---- the shares: every thread adds up a run of sequences, then a scan
   __shared__ long long s_scan[kWarps];
+  int* s_before = reinterpret_cast<int*>(smem + C::kPartAt);  // [thread]: first unit of its sequences (the pieces come later)
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
@@ -278,6 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
+  s_before[tid] = mine > 0 && total <= INT_MAX ? (int)before : -1;
+  __syncthreads();
   if (total > INT_MAX) {  // rows counted more than once: q_start does not ascend
     if (tid == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
     return;
@@ -289,24 +316,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   const int X0 = cta_share(Xq, Xr, G, blockIdx.x), X1 = cta_share(Xq, Xr, G, blockIdx.x + 1);
   auto share = [&](int w) { return X0 + ((X1 - X0) >> 3) * w + (((X1 - X0) & 7) * w >> 3); };
   static_assert(kWarps == 8, "share");
-  if (mine > 0 && before < X1 && before + mine > X0) {
-    for (int w = 0; w < kWarps; ++w) {
-      const int x = share(w);
-      if (x < before || x >= before + mine) continue;  // one thread for each w
-      int at = (int)before;
-      for (int b = b0; b < b1; ++b) {
-        const Seq s = load_seq<D, RT>(a, b, false);
-        const int nb = (s.tiles + kItemCost) * s.groups * a.kv_heads;
-        if (x < at + nb) {
-          s_first[w] = at;
-          s_b[w] = b;
-          break;
-        }
-        at += nb;
-      }
+  // the sequence this warp's share starts in: the last thread whose run of
+  // sequences starts at or before it (and is not empty), then along that run
+  int wb = 0, wat = 0;
+  const int wx = share(warp);
+  {
+    int best = -1;  // lane l looks at threads 8 l ... 8 l + 7
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) {
+      const int at = s_before[lane * (kThreads / 32) + k];
+      if (at >= 0 && at <= wx) best = k;
+    }
+    const uint32_t have = __ballot_sync(0xffffffffu, best >= 0);
+    const int src = 31 - __clz(have);  // (unit 0 is somebody's, so there is one)
+    const int t = __shfl_sync(0xffffffffu, lane * (kThreads / 32) + best, src);
+    wat = s_before[t];
+    for (wb = min(a.B, t * per); per > 1; ++wb) {
+      const Seq s = load_seq<D, RT>(a, wb, false);
+      const int nb = (s.tiles + kItemCost) * s.groups * a.kv_heads;
+      if (wx < wat + nb || wb + 1 >= a.B) break;
+      wat += nb;
     }
   }
-  __syncthreads();
+  __syncthreads();  // s_before has been read
 
   const int g = lane >> 2, q = lane & 3;
   const int fg = D == 128 ? ((g & 1) << 2 | g >> 1) : g;   // this thread's chunk of a V row (16 or 8 values)
@@ -318,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   bool alive = true;
   Walk w;
   bool more = share(warp) < share(warp + 1);
-  if (more) walk_start<D, RT>(w, a, s_b[warp], s_first[warp], share(warp), share(warp + 1) - share(warp));
+  if (more) walk_start<D, RT>(w, a, wb, wat, wx, share(warp + 1) - wx);
   while (more) {
     const int rows = min(kRowsC, w.s.n * a.G - w.grp * kRowsC);
     const int pos0 = w.s.len - w.s.n;  // position of the step's first token
@@ -374,19 +406,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
       const uint32_t m = (k.ok >> r) & ((1u << kGroups) - 1);
       const uint32_t bm = (1u << gpb) - 1;
       const int si = issued % kNST;
-      // lanes 0 .. nbox - 1 copy K boxes, the next nbox V boxes; a box is copied
-      // if any of its groups is wanted
-      const int i = lane % nbox;
-      const uint32_t mine = (m >> (i * gpb)) & bm;
-      const int pg = __shfl_sync(0xffffffffu, k.page, (r + i * gpb + __ffs(mine | 1u << 31) - 1) & 31);
-      const bool go = lane < 2 * nbox && mine != 0;
-      const int copies = __popc(__ballot_sync(0xffffffffu, go));
-      if (lane == 0) mbar_expect_tx(full + si, (uint32_t)(copies * box * D));
-      __syncwarp();
-      if (go) {
-        uint8_t* dst = ring + (size_t)si * C::kStage + (lane < nbox ? 0 : C::kHalfTile) + i * box * D;
-        // the first row inside the page is 0 unless a page holds several tiles
-        tma_load_3d(dst, lane < nbox ? &maps.k : &maps.v, 0, ti * kTile % P, pg * a.kv_heads + w.head, full + si);
+      uint8_t* dst = ring + (size_t)si * C::kStage;
+      const int at = ti * kTile % P;  // first row inside the page: 0 unless a page holds several tiles
+      // a box is copied if any of its groups is wanted
+      int copies = 0;
+      for (int i = 0; i < nbox; ++i) copies += ((m >> (i * gpb)) & bm) != 0;
+      const bool one = elect_one();
+      if (one) mbar_expect_tx(full + si, (uint32_t)(2 * copies * box * D));
+      for (int i = 0; i < nbox; ++i) {
+        const uint32_t want = (m >> (i * gpb)) & bm;
+        if (!want) continue;
+        const int pg = __shfl_sync(0xffffffffu, k.page, r + i * gpb + __ffs(want) - 1) * a.kv_heads + w.head;
+        if (one) {
+          tma_load_3d(dst + i * box * D, &maps.k, 0, at, pg, full + si);
+          tma_load_3d(dst + C::kHalfTile + i * box * D, &maps.v, 0, at, pg, full + si);
+        }
       }
       ++issued;
       ++ti;
@@ -515,12 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
         }
       }
       if (MODS) {
+        const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
           for (int k = 0; k < kTile / 4; ++k) {
             float x = s[rt][k];
-            if (a.softcap > 0.f) x = a.softcap * tanhf(__fdividef(x, a.softcap));
+            if (a.softcap > 0.f) x = a.softcap * tanh_of(x * cap_in);
             const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
             s[rt][k] = fmaf(slope[rt], (float)(pos - pos_r[rt]), x * kLog2e);
           }
@@ -684,43 +719,94 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
 
   // ---- the CTA's pieces: those of one item are added, in order.  Every warp
   // finds the items for itself: lane x looks at piece x.
-  constexpr int kVec = D / 4, kRowVec = kRowsC * kVec;  // float4 of a row, of an item
-  static_assert(kRowVec % 32 == 0 && 2 * kWarps <= 32, "a warp works on one item at a time");
+  constexpr int kVec = D / 4;          // lanes of a row, four columns each
+  constexpr int kRPW = 32 / kVec;      // rows of a warp at a time
+  static_assert(2 * kWarps == 16, "a piece for each of 16 lanes");
+  const int d = lane % kVec * 4;
   const int my_item = lane < 2 * kWarps ? recs[lane].item0 : -1;
-  const uint32_t same = __match_any_sync(0xffffffffu, my_item);
-  const bool lead = my_item >= 0 && __ffs(same) - 1 == lane;
+  const uint32_t there = __ballot_sync(0xffffffffu, my_item >= 0);
+  const uint32_t below = there & ((1u << lane) - 1);
+  const int prev_item = __shfl_sync(0xffffffffu, my_item, 31 - __clz(below | 1));
+  const bool lead = my_item >= 0 && (below == 0 || prev_item != my_item);  // first piece of its item
   const uint32_t leads = __ballot_sync(0xffffffffu, lead);
   // items that reach beyond this CTA: at most one from before it, one past it
   const bool out = lead && (my_item < X0 || my_item + recs[lane & (2 * kWarps - 1)].units > X1);
   const uint32_t outs = __ballot_sync(0xffffffffu, out);
-  const int n_items = __popc(leads);
-  for (int i = tid; i < n_items * kRowVec; i += kThreads) {
-    const int x0 = __fns(leads, 0, i / kRowVec + 1);  // first piece of the item
+  auto item_pieces = [&](int x0) {  // from its first piece up to the next item's
+    const uint32_t later = leads & ~((2u << x0) - 1);
+    return there & ~((1u << x0) - 1) & ((later & (0u - later)) - 1);
+  };
+  auto nth = [](uint32_t m, int n) {  // bit of m number n
+    for (; n > 0; --n) m &= m - 1;
+    return __ffs(m) - 1;
+  };
+  // slot 0 continues an item of the CTA before this one, slot 1 starts one
+  auto cta_part = [&](const Piece& rec) {
+    return a.partials + ((size_t)blockIdx.x * 2 + (rec.item0 >= X0 ? 1 : 0)) * C::kPartF;
+  };
+  const int n_pairs = __popc(leads) * kRowsC;
+  // a thread for each (item, row): the pieces' weights take the place of their maxima
+  static_assert(2 * kWarps * kRowsC <= kThreads, "a thread for each row of each piece");
+  if (tid < n_pairs) {
+    const int x0 = nth(leads, tid / kRowsC), r = tid % kRowsC;
     const Piece rec = recs[x0];
-    const uint32_t pieces = __shfl_sync(0xffffffffu, same, x0);
-    const int j = i % kRowVec, r = j / kVec, d = (j % kVec) * 4;
-    if (r >= rec.rows) continue;
-    float M = -INFINITY;
-    for (uint32_t k = pieces; k; k &= k - 1) {
-      const int x = __ffs(k) - 1;
-      M = fmaxf(M, part_of(x >> 1, x & 1)[kRowsC * D + 2 * r]);
+    const uint32_t pieces = item_pieces(x0);
+    const bool final_ = (outs >> x0 & 1) == 0;
+    float M = -INFINITY, L = 0.f;
+    for (uint32_t m = pieces; m; m &= m - 1) {
+      const int k = __ffs(m) - 1;
+      M = fmaxf(M, part_of(k >> 1, k & 1)[kRowsC * D + 2 * r]);
     }
     const float ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (uint32_t k = pieces; k; k &= k - 1) {
-      const int x = __ffs(k) - 1;
-      const float* p = part_of(x >> 1, x & 1);
-      add_piece(acc, L, *reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r),
-                *reinterpret_cast<const float4*>(p + r * D + d), ms);
+    for (uint32_t m = pieces; m; m &= m - 1) {
+      const int k = __ffs(m) - 1;
+      float2* st = reinterpret_cast<float2*>(part_of(k >> 1, k & 1) + kRowsC * D + 2 * r);
+      st->x = ex2(st->x - ms);
+      L += st->x * st->y;
     }
-    if ((outs >> x0 & 1) == 0) {
-      store4(a, rec, r, D, d, acc, M, L);
-    } else {
-      // slot 0 continues an item of the CTA before this one, slot 1 starts one
-      float* p = a.partials + ((size_t)blockIdx.x * 2 + (rec.item0 >= X0 ? 1 : 0)) * C::kPartF;
-      __stcg(reinterpret_cast<float4*>(p + (size_t)r * D + d), acc);
-      if (d == 0) __stcg(reinterpret_cast<float2*>(p + kRowsC * D + 2 * r), make_float2(M, L));
+    if (final_) {
+      const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
+      for (uint32_t m = pieces; m; m &= m - 1) {
+        const int k = __ffs(m) - 1;
+        part_of(k >> 1, k & 1)[kRowsC * D + 2 * r] *= inv;
+      }
+      if (r < rec.rows) OutRow(a, rec.start, rec.row0 + r, rec.head).lse(a, M, L);
+    } else if (r < rec.rows) {
+      __stcg(reinterpret_cast<float2*>(cta_part(rec) + kRowsC * D + 2 * r), make_float2(M, L));
+    }
+  }
+  __syncthreads();
+  // a warp for each four rows (or pairs of rows, D = 64) of an item, side by side
+  constexpr int kChunk = 4 * kRPW, kChunks = kRowsC / kChunk;
+  const int n_chunks = __popc(leads) * kChunks;
+  for (int ch = warp; ch < n_chunks; ch += kWarps) {
+    const int x0 = nth(leads, ch / kChunks), r0 = ch % kChunks * kChunk + lane / kVec;
+    const Piece rec = recs[x0];
+    float4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t m = item_pieces(x0); m; m &= m - 1) {
+      const int k = __ffs(m) - 1;
+      const float* p = part_of(k >> 1, k & 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + i * kRPW;  // (rows past the item's last hold zeros)
+        const float e = p[kRowsC * D + 2 * r];
+        const float4 o = *reinterpret_cast<const float4*>(p + r * D + d);
+        acc[i].x += o.x * e; acc[i].y += o.y * e; acc[i].z += o.z * e; acc[i].w += o.w * e;
+      }
+    }
+    const bool final_ = (outs >> x0 & 1) == 0;
+    float* part = cta_part(rec);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + i * kRPW;
+      if (r >= rec.rows) continue;
+      if (final_)
+        *reinterpret_cast<uint2*>(OutRow(a, rec.start, rec.row0 + r, rec.head).out(a, D) + d) =
+            make_uint2(pack_bf16(acc[i].x, acc[i].y), pack_bf16(acc[i].z, acc[i].w));
+      else
+        __stcg(reinterpret_cast<float4*>(part + (size_t)r * D + d), acc[i]);
     }
   }
   if (outs == 0) return;
@@ -728,35 +814,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   // release and acquire reach the other threads through the barriers.
   __syncthreads();
   const int n_out = __popc(outs);
-  if (tid < 32 * n_out && lane == 0) {
-    const Piece rec = recs[__fns(outs, 0, warp + 1)];
+  if (warp < n_out && lane == 0) {
+    const Piece rec = recs[__ffs(warp == 0 ? outs : outs & (outs - 1)) - 1];
     const int c0 = cta_of(Xq, Xr, G, rec.item0), c1 = cta_of(Xq, Xr, G, rec.item0 + rec.units - 1);
     const bool last = atom_add_acq_rel(a.tickets + c0, 1) == c1 - c0;
     if (last) a.tickets[c0] = 0;  // ready for the next call
     s_last[warp] = last ? c0 | c1 << 16 : -1;
   }
   __syncthreads();
-  for (int i = tid; i < n_out * kRowVec; i += kThreads) {
-    const int last = s_last[i / kRowVec];
+  for (int i = 0; i < n_out; ++i) {
+    const int last = s_last[i];
     if (last < 0) continue;
-    const Piece rec = recs[__fns(outs, 0, i / kRowVec + 1)];
+    const Piece rec = recs[__ffs(i == 0 ? outs : outs & (outs - 1)) - 1];
     const int c0 = last & 0xffff, c1 = last >> 16;
-    const int j = i % kRowVec, r = j / kVec, d = (j % kVec) * 4;
-    if (r >= rec.rows) continue;
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c)
-      M = fmaxf(M, __ldcg(a.partials + ((size_t)c * 2 + (c == c0)) * C::kPartF + kRowsC * D + 2 * r));
-    const float ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-      const float* p = a.partials + ((size_t)c * 2 + (c == c0)) * C::kPartF;
-      add_piece(acc, L, __ldcg(reinterpret_cast<const float2*>(p + kRowsC * D + 2 * r)),
-                __ldcg(reinterpret_cast<const float4*>(p + (size_t)r * D + d)), ms);
+    for (int rb = warp * kRPW; rb < rec.rows; rb += kWarps * kRPW) {
+      const int r = rb + lane / kVec;
+      auto piece = [&](int c) { return a.partials + ((size_t)c * 2 + (c == c0)) * C::kPartF; };
+      Joined J;
+      for (int c = c0; c <= c1; c += 16) {
+        const int x = lane & 15, n = min(16, c1 + 1 - c);
+        float2 st = make_float2(-INFINITY, 0.f);
+        if (x < n && r < rec.rows) st = __ldcg(reinterpret_cast<const float2*>(piece(c + x) + kRowsC * D + 2 * r));
+        float4 v[16];  // all reads in flight
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          v[k] = k < n && r < rec.rows ? __ldcg(reinterpret_cast<const float4*>(piece(c + k) + (size_t)r * D + d))
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float e = J.weight16(st);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) J.add(e, k, v[k]);
+      }
+      if (r < rec.rows) store4(a, rec, r, D, d, J);
     }
-    store4(a, rec, r, D, d, acc, M, L);
   }
 }
 
