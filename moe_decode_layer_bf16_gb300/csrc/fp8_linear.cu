@@ -6,7 +6,8 @@
 // the expert layers, so the attention projections around them use it too.
 //
 // Two kernels: the quantisation (a stream over x), and the product on
-// tcgen05.mma.kind::f8f6f4 (E4M3 x E4M3, fp32 accumulators in tensor memory).
+// tcgen05.mma.kind::f8f6f4 (E4M3 x E4M3, fp32 accumulators in tensor memory);
+// up to 16 tokens one, the product quantising what it needs as it goes.
 //
 // The product, in two arrangements of one kernel.  Up to 128 tokens the weights are
 // the MMA's 128 rows and the tokens its columns (NT = 16 .. 128), so that one
@@ -30,7 +31,7 @@
 // is last).
 //
 // Roles (12 warps): TMA producer, MMA issuer, a warp that copies each cell's
-// token scales, an idle one, eight epilogue warps (four lane quadrants x two
+// token scales and an idle one (or two that quantise), eight epilogue warps (four lane quadrants x two
 // column halves).  Every wait is bounded.
 #include <cuda.h>
 
@@ -52,16 +53,44 @@ namespace {
 // 16-byte load, a shuffle maximum, one 8-byte store.  K % 16 == 0, so a lane's
 // 8 columns lie inside a row or outside of it as a whole.
 //
-// A code is E4M3(fl32(x / s)), and the quotient matters only beside a border
-// between two codes: x * (1 / s) is within 2 units in the last place of it, so
-// unless that product lies as near to a midpoint of codes (or among the
-// subnormal codes, whose spacing differs) the code is the same, and only then the
-// division is carried out.  A power-of-two scale needs none.
+// A code is E4M3(fl32(x / s)).  The quotient comes from one reciprocal a group and
+// Markstein's correction (IBM J. Res. Dev. 34, 1990): q = fl(x y) with
+// y = fl(1 / s), then fl(q + fl(x - q s) y) is fl(x / s).  x and amax are bf16, so
+// there are 128 x 128 pairs of significands, and the two agree for all of them.
 constexpr int kQuantThreads = 256;
 
-// True where E4M3 of a number within 2 ulp of q may differ from E4M3 of q.
-MOE_DEV bool near_border(float q) {
-  return ((__float_as_uint(q) - 0x7fffeu) & 0xfffffu) <= 4u || fabsf(q) < 0.015625f;
+struct Quotient {
+  float s, y;
+  bool far;  // 1 / s or the products may be no normal numbers
+  MOE_DEV explicit Quotient(float scale) {
+    s = scale;
+    y = __frcp_rn(scale);
+    far = !(scale >= 1e-30f && scale <= 1e30f);
+  }
+  MOE_DEV float operator()(float x) const {
+    const float q = x * y;
+    return fmaf(fmaf(-q, s, x), y, q);
+  }
+};
+// the same by division, for scales where the reciprocal will not do (kept out of line)
+__device__ __noinline__ uint32_t codes4_far(float s, uint32_t a, uint32_t b) {
+  return f32x4_to_e4m3x4(__fdiv_rn(bf16_lo(a), s), __fdiv_rn(bf16_hi(a), s), __fdiv_rn(bf16_lo(b), s),
+                         __fdiv_rn(bf16_hi(b), s));
+}
+MOE_DEV uint32_t codes4(const Quotient& q, uint32_t a, uint32_t b) {  // of four bf16 values
+  return f32x4_to_e4m3x4(q(bf16_lo(a)), q(bf16_hi(a)), q(bf16_lo(b)), q(bf16_hi(b)));
+}
+MOE_DEV uint2 codes8(const Quotient& q, const uint4& v) {
+  uint2 c = make_uint2(codes4(q, v.x, v.y), codes4(q, v.z, v.w));
+  if (q.far) c = make_uint2(codes4_far(q.s, v.x, v.y), codes4_far(q.s, v.z, v.w));
+  return c;
+}
+MOE_DEV float amax8(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+  return m;
 }
 
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) {
@@ -75,33 +104,15 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) 
     const int col = kb * kBlock + lane16 * 8;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (col < a.K) v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + m * a.ldx + col));
-    const float f[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
-                        bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w)};
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    // the half-warps of a warp may hold different numbers of groups
+    float amax = amax8(v);
+    // the half-warps of a warp may be at different groups
     const unsigned mask = 0xffffu << (threadIdx.x & 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
     const float s = group_scale(amax, a.e8m0 != 0);
     if (col < a.K) {
-      const float inv = __frcp_rn(s);
-      float c[8];
-      bool near = !(s >= 1e-30f && s <= 1e30f);  // (1 / s is a normal number)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = f[i] * inv;
-        near |= near_border(c[i]) && f[i] != 0.f;
-      }
-      if (near && (!a.e8m0 || !(s >= 1e-30f && s <= 1e30f))) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = __fdiv_rn(f[i], s);
-      }
-      uint2 q;
-      q.x = f32x4_to_e4m3x4(c[0], c[1], c[2], c[3]);
-      q.y = f32x4_to_e4m3x4(c[4], c[5], c[6], c[7]);
-      *reinterpret_cast<uint2*>(a.codes + m * a.K + col) = q;
+      const Quotient q(s);
+      *reinterpret_cast<uint2*>(a.codes + m * a.K + col) = codes8(q, v);
     }
     if (lane16 == 0) a.scales[(size_t)kb * a.mp + m] = s;  // k-blocks first: the product reads a block's scales as one run
   }
@@ -111,19 +122,27 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) 
 constexpr int kRows = 128;              // rows of a row tile: the MMA's M
 constexpr int kRTile = kRows * 128;     // 16 KB
 constexpr int kNEpi = 8;                // epilogue warps
-constexpr int kThreads = 12 * 32;
-constexpr int kPW = 0, kMW = 1, kSW = 2, kEW0 = 4;
+constexpr int kPW = 0, kMW = 1, kSW = 2, kEW0 = 4, kEW1 = kEW0 + kNEpi;
 
-// NT columns; TR: the tokens are the rows
-template <int NT, bool TR>
+// NT columns; TR: the tokens are the rows; XQ: the kernel quantises x itself
+template <int NT, bool TR, bool XQ>
 struct Cfg {
+  static_assert(!XQ || (!TR && NT <= 16), "a warp quantises a cell's tokens, eight at a time");
+  // warps that quantise: 2, 3 and four behind the epilogue (a cell takes one of
+  // them 1650 clocks, and a cell's weights arrive every 760: with two warps one
+  // token 20.0 us)
+  static constexpr int kQW = XQ ? 6 : 0;
+  static constexpr int kThreads = (kEW1 + (XQ ? kQW - 2 : 0)) * 32;
   static constexpr int kCBox = TR ? NT : std::min(NT, 32);    // column rows of one copy (tokens: no more than there are)
   static constexpr int kStage = kRTile + NT * 128;            // ring stage: a row tile and a column tile
-  static constexpr int kNST = std::min(12, 212 * 1024 / kStage);
+  static constexpr int kRaw = XQ ? 2 : 1;                     // cells of a quantising warp whose rows of x are on their way
+  static constexpr size_t kRawBytes = (size_t)kQW * kRaw * NT * 256;
+  static constexpr int kNST = std::min(12, (int)((212 * 1024 - kRawBytes) / kStage));
   // weight tiles in flight before the codes are waited for: the copies complete
   // in order, so more of them delay the first cell's codes (11 of 11: one
-  // token 23.1 us, first cell 4.7 us after the start)
-  static constexpr int kAhead = std::min(kNST, 4);
+  // token 23.1 us, first cell 4.7 us after the start).  XQ: all (holding the
+  // others back until the first rows of x are here: 18.4 -> 19.1 us)
+  static constexpr int kAhead = XQ ? kNST : std::min(kNST, 4);
   static constexpr int kTST = NT <= 128 ? 4 : 2;              // accumulator buffers in tensor memory
   static constexpr int kTCols = NT * kTST;                    // 64 .. 512, a power of two
   static constexpr int kHalf = NT / 2;                        // columns of an epilogue warp
@@ -133,7 +152,8 @@ struct Cfg {
   static constexpr int kNBars = 2 * kNST + 2 * kTST + 2 * kXST + 3;
   static constexpr size_t kScale = (kBars + kNBars * 8 + 15) / 16 * 16;  // [kXST][kToks] fp32
   static constexpr size_t kMisc = kScale + (size_t)kXST * kToks * 4;
-  static constexpr size_t kSmem = 1024 + kMisc + 16;
+  static constexpr size_t kRawAt = kMisc + 16;
+  static constexpr size_t kSmem = 1024 + kRawAt + kRawBytes;
   // registers: 12 warps start with 168 a thread; with 128 accumulators the
   // epilogue takes 216 of them and the other four warps keep 72
   // (256 x 216 + 128 x 72 = 384 x 168)
@@ -145,40 +165,51 @@ struct LinMaps {
 };
 
 // The pieces of work of CTA c: whole pairs c, c + G, ..., then its share of the
-// cells of the remaining pairs, one pair after the other.
+// cells of the remaining pairs, one pair after the other, from the host's
+// starts[c] up to starts[c + 1] (no division is left for the kernel's first steps).
 struct Pieces {
   const LinArgs& p;
-  int c;
   int i;             // next whole pair of this CTA
-  int at, end;       // remaining cells [at, end) of the split pairs
-  int pair, k0, k1;  // the current piece
+  int w, t, k;       // next cell of the split pairs: weight tile, token tile, k-block
+  int we, te, ke;    // where the CTA's share of them ends
+  int k0, k1;        // the current piece: k-blocks
   int row, col;      // its row and column tile
-  MOE_DEV Pieces(const LinArgs& a, int cta) : p(a), c(cta), i(0) {
-    at = (int)((long long)p.split_cells * c / p.G_split);
-    end = (int)((long long)p.split_cells * (c + 1) / p.G_split);
-    if (c >= p.G_split) at = end = 0;
+  MOE_DEV explicit Pieces(const LinArgs& a) : p(a), i(0) {
+    const int c = min((int)blockIdx.x, p.G_split), e = min((int)blockIdx.x + 1, p.G_split);
+    w = p.starts[c].w; t = p.starts[c].t; k = p.starts[c].k;
+    we = p.starts[e].w; te = p.starts[e].t; ke = p.starts[e].k;
   }
   MOE_DEV bool next() {
+    int cw, ct;
     if (i < p.waves) {
-      pair = i++ * p.G + c;
+      // weight tiles follow one another within a token tile
+      const int pair = i++ * p.G + blockIdx.x;
+      ct = pair / p.n_wt;
+      cw = pair - ct * p.n_wt;
       k0 = 0;
       k1 = p.nkb;
     } else {
-      if (at >= end) return false;
-      const int t = at / p.nkb;
-      pair = p.waves * p.G + t;
-      k0 = at - t * p.nkb;
-      k1 = min(p.nkb, end - t * p.nkb);
-      at = t * p.nkb + k1;
+      const bool last = w == we && t == te;
+      if (last && k >= ke) return false;
+      cw = w;
+      ct = t;
+      k0 = k;
+      k1 = last ? ke : p.nkb;
+      k = last ? ke : 0;
+      if (!last && ++w == p.n_wt) { w = 0; ++t; }
     }
-    // weight tiles follow one another within a token tile
-    const int w = pair % p.n_wt, t = pair / p.n_wt;
-    row = p.tok_rows ? t : w;
-    col = p.tok_rows ? w : t;
+    row = p.tok_rows ? ct : cw;
+    col = p.tok_rows ? cw : ct;
     return true;
   }
-  // CTA that holds cell x of the split pairs
-  MOE_DEV int owner(int x) const { return (int)(((long long)(x + 1) * p.G_split - 1) / p.split_cells); }
+  // CTA that holds k-block kb of the current (split) pair
+  MOE_DEV int owner(int kb) const {
+    const int cw = p.tok_rows ? col : row, ct = p.tok_rows ? row : col;
+    const int x = (ct * p.n_wt + cw - p.waves * p.G) * p.nkb + kb;  // of all split cells
+    int o = min(x / p.share_q, p.G_split - 1);
+    while (p.share_q * o + p.share_r * o / p.G_split > x) --o;
+    return o;
+  }
 };
 
 // (a0, a1) += (d0, d1) * (f0, f1), one packed instruction
@@ -195,9 +226,9 @@ MOE_DEV void store_out(const LinArgs& p, long long m, int n, float v) {
     reinterpret_cast<__nv_bfloat16*>(p.out)[m * p.N + n] = __float2bfloat16_rn(v);
 }
 
-template <int NT, bool TR>
-__global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __grid_constant__ LinMaps maps) {
-  using C = Cfg<NT, TR>;
+template <int NT, bool TR, bool XQ>
+__global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(LinArgs p, const __grid_constant__ LinMaps maps) {
+  using C = Cfg<NT, TR, XQ>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -220,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.w) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.x) : "memory");
     for (int i = 0; i < C::kNST; ++i) {
-      mbar_init(full + i, 1);
+      mbar_init(full + i, XQ ? 2 : 1);  // the copies, and a quantising warp
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < C::kTST; ++i) {
@@ -246,12 +277,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)s_misc[0];
-  Pieces pc(p, blockIdx.x);
+  Pieces pc(p);
   // tokens of a token tile, live columns of a column tile
   auto toks = [&](int t) { return min(p.chunk, p.M - t * p.chunk); };
   auto cols = [&](int c) { return TR ? min(NT, p.N - c * NT) : toks(c); };
 
-  if (warp < kEW0) {
+  if (warp < kEW0 || (XQ && warp >= kEW1)) {
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kPW) {
       // ================================================================ producer
@@ -261,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
         uint32_t gs = 0, ahead = 0;
         auto load_w = [&](const Pieces& q, int kb, int si) {
           uint8_t* st = ring + (size_t)si * C::kStage;
-          const int nbox = (cols(q.col) + C::kCBox - 1) / C::kCBox;
+          const int nbox = XQ ? 0 : (cols(q.col) + C::kCBox - 1) / C::kCBox;
           mbar_expect_tx(full + si, (uint32_t)(kRTile + nbox * C::kCBox * 128));
           if (TR)
             tma_load_2d(st + kRTile, &maps.w, kb * kBlock, q.col * NT, full + si);
@@ -269,18 +300,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
             tma_load_2d(st, &maps.w, kb * kBlock, q.row * kRows, full + si);
         };
         {
-          Pieces q(p, blockIdx.x);
+          Pieces q(p);
           while (ahead < (uint32_t)C::kAhead && q.next())
             for (int kb = q.k0; kb < q.k1 && ahead < (uint32_t)C::kAhead; ++kb) load_w(q, kb, (int)ahead++);
         }
-        grid_dep_wait();
-        asm volatile("fence.proxy.async.global;" ::: "memory");  // codes of the kernel before are read with TMA
+        if (!XQ) {
+          grid_dep_wait();
+          asm volatile("fence.proxy.async.global;" ::: "memory");  // codes of the kernel before are read with TMA
+        }
         int si = 0;
         uint32_t ph = 0;
         bool alive = true;
         while (alive && pc.next()) {
           const int t0 = (TR ? pc.row : pc.col) * p.chunk;
-          const int nbox = TR ? 1 : (toks(pc.col) + C::kCBox - 1) / C::kCBox;
+          const int nbox = TR ? 1 : XQ ? 0 : (toks(pc.col) + C::kCBox - 1) / C::kCBox;
           for (int kb = pc.k0; kb < pc.k1; ++kb) {
             if (gs >= ahead) {
               if (gs >= (uint32_t)C::kNST && !mbar_wait_landed(empty + si, ph ^ 1u, status)) { alive = false; break; }
@@ -328,6 +361,115 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
         mbar_wait_landed(mma_done, 0, status);
       }
       __syncwarp();
+    } else if (XQ) {
+      // ================================================================ quantisation
+      // kQW warps take cells in turn and fill their activation tile and scales:
+      // four lanes for a token's group, 32 columns each, eight tokens at a time.
+      // A warp's rows are copied kRaw of its cells ahead into shared memory, where
+      // each thread reads back only what it copied itself.  (Every CTA quantises
+      // the groups it needs for itself: at 16 tokens 4 KB of x beside a cell's
+      // 16 KB of weights, and no kernel before this one.)
+      constexpr int kIt = NT / 8;  // passes of eight tokens
+      const int me = warp < kEW0 ? warp - kSW : warp - kEW1 + 2, tok = lane >> 2, quarter = lane & 3;
+      const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + quarter * 32;
+      uint8_t* raw = smem + C::kRawAt + me * (C::kRaw * kIt * 2048) + lane * 16;  // [kRaw][kIt][4 chunks][lane]
+      // this warp's cells, one after the other
+      struct Cells {
+        Pieces pc;
+        int kb;
+        bool more;
+        MOE_DEV Cells(const LinArgs& a, int first) : pc(a) {
+          more = pc.next();
+          kb = pc.k0;
+          step(first);
+        }
+        MOE_DEV void step(int n) {
+          kb += n;
+          while (more && kb >= pc.k1) {
+            const int past = kb - pc.k1;
+            more = pc.next();
+            kb = pc.k0 + past;
+          }
+        }
+      };
+      Cells at(p, me), ahead = at;
+      uint32_t an = 0;
+      auto copy = [&]() {
+        if (ahead.more) {
+          const int t0 = ahead.pc.col * p.chunk, ntok = toks(ahead.pc.col);
+          uint8_t* to = raw + (an++ % C::kRaw) * (kIt * 2048);
+#pragma unroll
+          for (int i = 0; i < kIt; ++i) {
+            const int t = 8 * i + tok;
+            if (8 * i < ntok) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                // past the last token or column: zeros, nothing is read
+                const bool ok = t < ntok && ahead.kb * kBlock + quarter * 32 + 8 * j < p.K;
+                const uint16_t* from = ok ? x + (long long)(t0 + t) * p.ldx + ahead.kb * kBlock + 8 * j : x;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(to + i * 2048 + j * 512)),
+                             "l"(from), "r"(ok ? 16 : 0)
+                             : "memory");
+              }
+            }
+          }
+          ahead.step(C::kQW);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      for (int i = 0; i < C::kRaw - 1; ++i) copy();
+      for (uint32_t n = me, mine = 0; at.more; n += C::kQW, ++mine) {
+        const int ntok = toks(at.pc.col);
+        copy();
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::kRaw - 1) : "memory");
+        const uint8_t* from = raw + (mine % C::kRaw) * (kIt * 2048);
+        const uint32_t si = n % C::kNST, xi = n % C::kXST;
+        uint8_t* xt = ring + (size_t)si * C::kStage + kRTile;
+        uint4 code[kIt][2];
+        float s[kIt];
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          if (8 * i < ntok) {  // the same in the warp
+            uint4 v[4];
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = *reinterpret_cast<const uint4*>(from + i * 2048 + j * 512);
+              amax = fmaxf(amax, amax8(v[j]));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            s[i] = group_scale(amax, p.e8m0 != 0);
+            const Quotient q(s[i]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint2 c0 = codes8(q, v[2 * j]), c1 = codes8(q, v[2 * j + 1]);
+              code[i][j] = make_uint4(c0.x, c0.y, c1.x, c1.y);
+            }
+          }
+        }
+        if (!mbar_wait_landed(empty + si, ((n / C::kNST) & 1u) ^ 1u, status) ||
+            !mbar_wait_landed(sempty + xi, ((n / C::kXST) & 1u) ^ 1u, status))
+          break;
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          const int t = 8 * i + tok;  // (a column past the last token is not read back)
+          if (8 * i < ntok) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)  // 16-byte chunk 2 quarter + j of row t, swizzled as TMA would
+              *reinterpret_cast<uint4*>(xt + t * 128 + (((2 * quarter + j) ^ (t & 7)) << 4)) = code[i][j];
+            if (quarter == 0) xring[xi * C::kToks + t] = s[i];
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tile is read by the MMA
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full + si);
+          mbar_arrive(sfull + xi);
+        }
+        at.step(C::kQW);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kSW) {
       // ================================================================ token scales
       // A cell's xs run, copied up to kXST cells ahead of its epilogue (its own
@@ -374,9 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
       const bool whole = pc.k0 == 0 && pc.k1 == p.nkb;
       int c_first = 0, c_last = 0;
       if (!whole) {
-        const int x0 = (pc.pair - p.waves * p.G) * p.nkb;
-        c_first = pc.owner(x0);
-        c_last = pc.owner(x0 + p.nkb - 1);
+        c_first = pc.owner(0);
+        c_last = pc.owner(p.nkb - 1);
       }
 #pragma unroll
       for (int j = 0; j < C::kHalf; ++j) acc[j] = 0.f;
@@ -519,18 +660,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(LinArgs p, const __
   }
 }
 
-template <int NT, bool TR>
-cudaError_t launch_nt(const LinPlan& p, const LinArgs& a, const LinMaps& maps, bool pdl, cudaStream_t s) {
-  using C = Cfg<NT, TR>;
+template <int NT, bool TR, bool XQ>
+cudaError_t launch_nt(const LinPlan& p, const LinArgs& a, const LinMaps& maps, cudaStream_t s) {
+  using C = Cfg<NT, TR, XQ>;
   // a process-wide attribute of the kernel, set once (an atomic static)
   static const cudaError_t rc =
-      cudaFuncSetAttribute(linear_kernel<NT, TR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+      cudaFuncSetAttribute(linear_kernel<NT, TR, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (rc != cudaSuccess) return rc;
-  if (pdl) {
-    PdlLaunch L(dim3(p.G), dim3(kThreads), C::kSmem, s);
-    return cudaLaunchKernelEx(&L.cfg, linear_kernel<NT, TR>, a, maps);
+  if (a.pdl) {
+    PdlLaunch L(dim3(p.G), dim3(C::kThreads), C::kSmem, s);
+    return cudaLaunchKernelEx(&L.cfg, linear_kernel<NT, TR, XQ>, a, maps);
   }
-  linear_kernel<NT, TR><<<p.G, kThreads, C::kSmem, s>>>(a, maps);
+  linear_kernel<NT, TR, XQ><<<p.G, C::kThreads, C::kSmem, s>>>(a, maps);
   return cudaGetLastError();
 }
 
@@ -568,24 +709,30 @@ cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_linear(const LinPlan& p, const uint8_t* xq, const float* xs, const uint8_t* w, const float* w_s,
-                          void* out, int out_fp32, int* status, int* tickets, float* partials, bool pdl,
-                          cudaStream_t s) {
+cudaError_t launch_linear(const LinPlan& p, LinArgs a, const uint8_t* xq, const uint8_t* w, cudaStream_t s) {
   LinMaps maps;
-  if (!tmap_2d(&maps.w, w, p.K, p.N, 128, p.tok_rows ? 256 : kRows) ||
-      !tmap_2d(&maps.x, xq, p.K, p.M, 128, p.tok_rows ? kRows : std::min(p.nt, 32)))
+  const bool fused = a.x != nullptr;
+  if (!tmap_2d(&maps.w, w, p.K, p.N, 128, p.tok_rows ? 256 : kRows)) return cudaErrorInvalidValue;
+  if (fused)
+    maps.x = maps.w;  // (not used)
+  else if (!tmap_2d(&maps.x, xq, p.K, p.M, 128, p.tok_rows ? kRows : std::min(p.nt, 32)))
     return cudaErrorInvalidValue;
-  LinArgs a;
-  a.xs = xs; a.mp = linear_scale_stride(p.M); a.w_s = w_s; a.out = out; a.out_fp32 = out_fp32;
-  a.M = p.M; a.N = p.N; a.nkb = p.nkb; a.chunk = p.chunk; a.n_wt = p.n_wt; a.n_wblk = (p.N + kBlock - 1) / kBlock;
-  a.tok_rows = p.tok_rows; a.G = p.G; a.waves = p.waves; a.G_split = p.G_split; a.split_cells = p.split_cells;
-  a.status = status; a.tickets = tickets; a.partials = partials;
+  a.mp = linear_scale_stride(p.M);
+  a.M = p.M; a.N = p.N; a.K = p.K; a.nkb = p.nkb; a.chunk = p.chunk; a.n_wt = p.n_wt;
+  a.n_wblk = (p.N + kBlock - 1) / kBlock;
+  a.tok_rows = p.tok_rows; a.G = p.G; a.waves = p.waves; a.G_split = p.G_split;
+  for (int c = 0; c <= p.G_split; ++c) {  // CTA c's share: cells split_cells * c / G_split ...
+    const int x = (int)((long long)p.split_cells * c / p.G_split), pair = p.waves * p.G + x / p.nkb;
+    a.starts[c] = {pair % p.n_wt, pair / p.n_wt, x % p.nkb};
+  }
+  a.share_q = p.split_cells / p.G_split; a.share_r = p.split_cells % p.G_split;
+  if (fused) return launch_nt<16, false, true>(p, a, maps, s);
   switch (p.nt) {
-    case 16: return launch_nt<16, false>(p, a, maps, pdl, s);
-    case 32: return launch_nt<32, false>(p, a, maps, pdl, s);
-    case 64: return launch_nt<64, false>(p, a, maps, pdl, s);
-    case 128: return launch_nt<128, false>(p, a, maps, pdl, s);
-    default: return launch_nt<256, true>(p, a, maps, pdl, s);
+    case 16: return launch_nt<16, false, false>(p, a, maps, s);
+    case 32: return launch_nt<32, false, false>(p, a, maps, s);
+    case 64: return launch_nt<64, false, false>(p, a, maps, s);
+    case 128: return launch_nt<128, false, false>(p, a, maps, s);
+    default: return launch_nt<256, true, false>(p, a, maps, s);
   }
 }
 

@@ -217,25 +217,30 @@ struct LinPlan {
   int G_split;        // CTAs that share the cells of the remaining pairs
   int split_cells;
 };
+constexpr int kLinFusedTokens = 16;  // up to so many tokens the product quantises x itself
 struct LinArgs {
-  const float* xs;   // [nkb][mp]
-  int mp;
-  const float* w_s;  // [n_wblk][nkb]
-  void* out;
-  int out_fp32;
-  int M, N, nkb, chunk, n_wt, n_wblk, G, waves, G_split, split_cells;
+  // the caller's: x (to be quantised, M <= kLinFusedTokens) or codes and scales
+  const void* x = nullptr;     // bf16 [M, K], row stride ldx elements
+  long long ldx = 0;
+  int e8m0 = 0;
+  const float* xs = nullptr;   // [nkb][mp]
+  const float* w_s = nullptr;  // [n_wblk][nkb]
+  void* out = nullptr;
+  int out_fp32 = 0;
+  int* status = nullptr;
+  int* tickets = nullptr;      // [G], zero between calls
+  float* partials = nullptr;   // [G_split][2][nt][128]
+  bool pdl = false;            // the codes and scales come from the kernel just enqueued, a
+                               // launch_quant_rows; w and w_s do not
+  // the plan's
+  int mp, M, N, K, nkb, chunk, n_wt, n_wblk, G, waves, G_split;
+  int share_q, share_r;  // split cells = share_q * G_split + share_r
+  struct Start { int w, t, k; } starts[kLinMaxCtas + 1];  // each CTA's first split cell: weight tile, token tile, k-block
   bool tok_rows;
-  int* status;
-  int* tickets;      // [G], zero between calls
-  float* partials;   // [G_split][2][nt][128]
 };
 void plan_linear(LinPlan& p, int M, int N, int K, int sms);
 size_t linear_partial_bytes(const LinPlan& p);
-// pdl: the codes and scales come from the kernel just enqueued, a
-// launch_quant_rows; w and w_s do not
-cudaError_t launch_linear(const LinPlan& p, const uint8_t* xq, const float* xs, const uint8_t* w, const float* w_s,
-                          void* out, int out_fp32, int* status, int* tickets, float* partials, bool pdl,
-                          cudaStream_t s);
+cudaError_t launch_linear(const LinPlan& p, LinArgs a, const uint8_t* xq, const uint8_t* w, cudaStream_t s);
 
 // The FP8 paged cache: writing new tokens (kv_append.cu) and attention over it
 // (attention.cu).  Caches [num_pages][kv_heads][page_size][head_dim] codes,
