@@ -49,9 +49,10 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------- quantisation
-// One 16-lane half-warp per (token, 128-column group), 8 columns a lane: one
-// 16-byte load, a shuffle maximum, one 8-byte store.  K % 16 == 0, so a lane's
-// 8 columns lie inside a row or outside of it as a whole.
+// A warp takes eight 128-column groups of a token: a 16-lane half-warp for a group
+// at a time, 8 columns a lane, four groups of each in flight; one 16-byte load, a
+// shuffle maximum, one 8-byte store a group.  K % 16 == 0, so a lane's 8 columns
+// lie inside a row or outside of it as a whole.
 //
 // A code is E4M3(fl32(x / s)).  The quotient comes from one reciprocal a group and
 // Markstein's correction (IBM J. Res. Dev. 34, 1990): q = fl(x y) with
@@ -95,26 +96,34 @@ MOE_DEV float amax8(const uint4& v) {
 
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) {
   grid_dep_launch();  // the product may start streaming its weights now
-  const int lane16 = threadIdx.x & 15;
-  const long long n_groups = (long long)a.M * a.nkb;
-  const long long step = (long long)gridDim.x * (kQuantThreads / 16);
-  for (long long gi = (long long)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4); gi < n_groups; gi += step) {
-    const long long m = gi / a.nkb;
-    const int kb = (int)(gi - m * a.nkb);
-    const int col = kb * kBlock + lane16 * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (col < a.K) v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.x) + m * a.ldx + col));
-    float amax = amax8(v);
-    // the half-warps of a warp may be at different groups
-    const unsigned mask = 0xffffu << (threadIdx.x & 16);
+  const int lane = threadIdx.x & 31, lane16 = lane & 15;
+  const int n_runs = (a.nkb + 7) / 8, n_units = a.M * n_runs;
+  for (int u = blockIdx.x * (kQuantThreads / 32) + (threadIdx.x >> 5); u < n_units; u += gridDim.x * (kQuantThreads / 32)) {
+    const int m = u / n_runs, kb0 = (u - m * n_runs) * 8 + (lane >> 4);  // this half-warp: groups kb0, kb0 + 2, ...
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x) + m * a.ldx + lane16 * 8;
+    uint8_t* codes = a.codes + (size_t)m * a.K + lane16 * 8;
+    uint4 v[4];
+    float amax[4];
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o));
-    const float s = group_scale(amax, a.e8m0 != 0);
-    if (col < a.K) {
-      const Quotient q(s);
-      *reinterpret_cast<uint2*>(a.codes + m * a.K + col) = codes8(q, v);
+    for (int i = 0; i < 4; ++i) {
+      const int col = (kb0 + 2 * i) * kBlock;
+      v[i] = col + lane16 * 8 < a.K ? __ldg(reinterpret_cast<const uint4*>(x + col)) : make_uint4(0, 0, 0, 0);
     }
-    if (lane16 == 0) a.scales[(size_t)kb * a.mp + m] = s;  // k-blocks first: the product reads a block's scales as one run
+#pragma unroll
+    for (int i = 0; i < 4; ++i) amax[i] = amax8(v[i]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], o));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int kb = kb0 + 2 * i;
+      const float s = group_scale(amax[i], a.e8m0 != 0);
+      const uint2 c = codes8(Quotient(s), v[i]);
+      if (kb * kBlock + lane16 * 8 < a.K) *reinterpret_cast<uint2*>(codes + kb * kBlock) = c;
+      // k-blocks first: the product reads a block's scales as one run
+      if (lane16 == 0 && kb < a.nkb) a.scales[(size_t)kb * a.mp + m] = s;
+    }
   }
 }
 
@@ -703,9 +712,8 @@ size_t linear_partial_bytes(const LinPlan& p) {
 
 cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
-  const long long groups = (long long)a.M * a.nkb;
-  const long long ctas = (groups + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
-  quant_rows_kernel<<<(unsigned)std::min<long long>(ctas, (long long)sms * 8), kQuantThreads, 0, s>>>(a);
+  const int units = a.M * ((a.nkb + 7) / 8), per = kQuantThreads / 32;
+  quant_rows_kernel<<<(unsigned)std::min((units + per - 1) / per, sms * 8), kQuantThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
