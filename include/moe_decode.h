@@ -420,7 +420,8 @@ int kv_cache_append(const moe_kv_cache *cache, const void *k, long long k_stride
  * A row that sees no token gives zeros and lse = -inf.  Tokens of a page
  * outside [0, num_pages) are masked.
  *   q      bf16 [total, heads, head_dim], tokens q_stride elements apart
- *          (% 8 == 0), 16-byte aligned; heads % kv_heads == 0, heads <= 4096
+ *          (% 8 == 0), 16-byte aligned; heads % kv_heads == 0, heads <= 4096,
+ *          total * heads < 2^31
  *   out    bf16 [total, heads, head_dim];  lse fp32 [total, heads] or NULL
  *   slopes fp32 [heads] or NULL
  * Scores, statistics and sums are fp32; the weights are rounded to 11 bits for

@@ -186,12 +186,13 @@ def fp8_linear(x, w, w_s, out, workspace, e8m0: bool = False, stream=None):
     M, K = x.shape
     N = w.shape[0]
     sm, sk = x.stride()
-    wt, ot, dev = w.dtype, out.dtype, _device()
+    wt, ot, dev = w.dtype, out.dtype, x.get_device()
     if not (x.dtype is _bf16 and (wt is _u8 or wt is _e4m3) and w_s.dtype is _f32 and (ot is _bf16 or ot is _f32)
             and w.shape == (N, K) and w_s.shape == (N + 127 >> 7, K + 127 >> 7) and out.shape == (M, N)
             and (sk == 1 or K == 1) and w.is_contiguous() and w_s.is_contiguous() and out.is_contiguous()
             and workspace.is_contiguous() and x.get_device() == dev and w.get_device() == dev
-            and w_s.get_device() == dev and out.get_device() == dev and workspace.get_device() == dev):
+            and w_s.get_device() == dev and out.get_device() == dev and workspace.get_device() == dev
+            and dev >= 0 and dev == _device()):
         _linear_refused(x, w, w_s, out, workspace)
     rc = lib().fp8_linear(x.data_ptr(), sm if M > 1 else K + 7 & -8, w.data_ptr(), w_s.data_ptr(), M, N, K,
                           1 if e8m0 else 0, out.data_ptr(), 1 if ot is _f32 else 0, workspace.data_ptr(),
@@ -227,14 +228,13 @@ def _batch_refused(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens
     _want(q_start, "q_start", _i32, (lens.shape[0] + 1,))
     _want(page_table, "page_table", _i32, (lens.shape[0], None))
     _want_workspace(workspace)
-    _want_device(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
 
 
 def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, max_new: int, workspace,
                     stream=None):
     """Write new tokens' keys and values (bf16 [total, kv heads, head dim], any
     token stride) into the cache; see include/moe_decode.h for the batch."""
-    dev = _device()
+    dev = k.get_device()
     if k_cache.dim() != 4 or k.dim() != 3 or v.dim() != 3:
         _append_refused(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
     pages, hk, page, d = k_cache.shape
@@ -244,7 +244,7 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_star
     if not (_batch_ok(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace, dev)
             and k.dtype is _bf16 and v.dtype is _bf16 and k.shape == (total, hk, d) and v.shape == (total, hk, d)
             and k2 == 1 and v2 == 1 and (hk == 1 or (k1 == d and v1 == d))
-            and k.get_device() == dev and v.get_device() == dev):
+            and v.get_device() == dev and dev >= 0 and dev == _device()):
         _append_refused(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
     if total <= 1:
         k0 = v0 = hk * d
@@ -261,7 +261,7 @@ def _append_refused(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_star
     row = (k_cache.shape[1], k_cache.shape[3])
     _want_rows(k, "k", (None, *row))
     _want_rows(v, "v", (k.shape[0], *row))
-    _want_device(k, v)
+    _want_device(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
     raise ValueError("kv_cache_append: arguments refused")
 
 
@@ -271,7 +271,7 @@ def decode_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, q_start,
     """Attention of a step's tokens (q bf16 [total, heads, head dim], any token
     stride) over the cache.  out bf16 like q; lse float32 [total, heads] or
     None; sm_scale 1 / sqrt(head dim) by default; slopes float32 [heads]."""
-    dev = _device()
+    dev = q.get_device()
     if k_cache.dim() != 4 or q.dim() != 3:
         _attention_refused(q, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, out, workspace, lse, slopes)
     pages, hk, page, d = k_cache.shape
@@ -281,7 +281,7 @@ def decode_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, q_start,
     if not (_batch_ok(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace, dev)
             and q.dtype is _bf16 and out.dtype is _bf16 and dq == d and out.shape == shape
             and q2 == 1 and (h == 1 or q1 == d) and out.is_contiguous()
-            and q.get_device() == dev and out.get_device() == dev
+            and out.get_device() == dev and dev >= 0 and dev == _device()
             and (lse is None or (lse.dtype is _f32 and lse.shape == (total, h) and lse.is_contiguous()
                                  and lse.get_device() == dev))
             and (slopes is None or (slopes.dtype is _f32 and slopes.shape == (h,) and slopes.is_contiguous()
@@ -306,5 +306,5 @@ def _attention_refused(q, k_cache, v_cache, k_scale, v_scale, page_table, q_star
         _want(lse, "lse", _f32, (total, h))
     if slopes is not None:
         _want(slopes, "slopes", _f32, (h,))
-    _want_device(q, out, lse, slopes)
+    _want_device(q, out, lse, slopes, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
     raise ValueError("decode_attention: arguments refused")

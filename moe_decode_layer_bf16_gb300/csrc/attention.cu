@@ -28,7 +28,7 @@
 //   stored.  Each row of Q, scaled to a maximum in [128, 256), is the sum of an
 //   E4M3 part and a second E4M3 part of 1/16 the size: a bf16 value has 8
 //   significant bits and each part carries 4, so the split is exact for values
-//   within 2^-14 of the row's largest and off by at most 2^-22 of it below.  The two
+//   within 2^-14 of the row's largest and off by at most 2^-21 of it below.  The two
 //   parts are the upper and lower 8 of the MMA's 16 rows, so no row is wasted
 //   and their sum is an addition within a thread.
 //   O^T = V^T P^T on mma m16n8k16 (f16): the S accumulator is the B operand as it
