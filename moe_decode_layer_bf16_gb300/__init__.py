@@ -12,7 +12,8 @@ Entry points (same names as the C ABI):
 plus MoeDecodeLayer, a holder of one layer's weights and workspace, and, from
 the attention module,
   fp8_quant_rows, fp8_block_gemm, fp8_linear, kv_cache_append, decode_attention
-(with their *_workspace_size).
+(with their *_workspace_size), and AttentionDecode, the attention sublayer over
+an Fp8KvCache.
 """
 
 from __future__ import annotations
@@ -317,6 +318,6 @@ class MoeDecodeLayer:
         return moe_device_status(self.workspace)
 
 
-from .attention import (decode_attention, decode_attention_workspace_size, fp8_block_gemm,  # noqa: E402
+from .attention import (AttentionDecode, Fp8KvCache, decode_attention, decode_attention_workspace_size, fp8_block_gemm,  # noqa: E402
                         fp8_block_gemm_workspace_size, fp8_linear, fp8_linear_workspace_size, fp8_quant_rows,
                         kv_cache_append, kv_cache_workspace_size)

@@ -16,7 +16,7 @@ import math
 
 import torch
 
-from . import MOE_OK, MoeError, lib
+from . import MOE_OK, MoeError, lib, moe_device_status, moe_workspace_init
 
 _vp, _i, _f, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 _bf16, _f32, _u8, _e4m3, _i32 = torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32
@@ -308,3 +308,64 @@ def _attention_refused(q, k_cache, v_cache, k_scale, v_scale, page_table, q_star
         _want(slopes, "slopes", _f32, (h,))
     _want_device(q, out, lse, slopes, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
     raise ValueError("decode_attention: arguments refused")
+
+
+class Fp8KvCache:
+    """The tensors of an FP8 paged cache (nothing needs to be initialised)."""
+
+    def __init__(self, num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device="cuda"):
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        self.k, self.v = (torch.empty(shape, dtype=_u8, device=device) for _ in range(2))
+        self.k_scale, self.v_scale = (torch.empty(shape[:2], dtype=_f32, device=device) for _ in range(2))
+
+
+class AttentionDecode:
+    """The attention sublayer of a decode step: the fused query, key and value
+    projection, the new tokens' keys and values into the cache, attention over it,
+    the output projection.  Its output is what rmsnorm_residual adds to the
+    residual before MoeDecodeLayer.
+
+    weights: qkv (E4M3 [(heads + 2 kv_heads) * head_dim, hidden]), o (E4M3
+    [hidden, heads * head_dim]) and their float32 block scales qkv_s, o_s.
+    `rotate(q, k)`, if given, changes the step's queries and keys in place
+    (position encodings) before they are used.  softcap, window, slopes and
+    sm_scale as decode_attention's."""
+
+    def __init__(self, hidden: int, heads: int, kv_heads: int, head_dim: int, weights: dict, cache: Fp8KvCache,
+                 max_tokens: int, max_new: int = 1, e8m0: bool = False, rotate=None, **options):
+        self.hidden, self.heads, self.kv_heads, self.head_dim = hidden, heads, kv_heads, head_dim
+        self.weights, self.cache, self.max_new, self.e8m0 = weights, cache, max_new, e8m0
+        self.rotate, self.options = rotate, options
+        self.max_tokens = max_tokens
+        rows = (heads + 2 * kv_heads) * head_dim
+        device = cache.k.device
+        n = max(fp8_linear_workspace_size(max_tokens, rows, hidden),
+                fp8_linear_workspace_size(max_tokens, hidden, heads * head_dim),
+                decode_attention_workspace_size(heads, kv_heads, head_dim, max_new), kv_cache_workspace_size())
+        self.workspace = torch.empty(n, dtype=_u8, device=device)
+        moe_workspace_init(self.workspace)
+        self.qkv = torch.empty((max_tokens, heads + 2 * kv_heads, head_dim), dtype=_bf16, device=device)
+        self.mixed = torch.empty((max_tokens, heads, head_dim), dtype=_bf16, device=device)
+
+    def __call__(self, x, page_table, q_start, lens, out=None, stream=None):
+        """x bf16 [tokens, hidden] -> bf16 [tokens, hidden]; page_table, q_start
+        and lens as kv_cache_append's (lens with the step's tokens included)."""
+        n, h, hk, c, w = x.shape[0], self.heads, self.kv_heads, self.cache, self.weights
+        if n > self.max_tokens:
+            raise ValueError(f"{n} tokens: at most {self.max_tokens}")
+        if out is None:
+            out = torch.empty((n, self.hidden), dtype=_bf16, device=x.device)
+        qkv, mixed = self.qkv[:n], self.mixed[:n]
+        fp8_linear(x, w["qkv"], w["qkv_s"], qkv.view(n, -1), self.workspace, e8m0=self.e8m0, stream=stream)
+        q, k, v = qkv[:, :h], qkv[:, h:h + hk], qkv[:, h + hk:]
+        if self.rotate is not None:
+            self.rotate(q, k)
+        kv_cache_append(k, v, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, self.max_new, self.workspace,
+                        stream=stream)
+        decode_attention(q, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, self.max_new, mixed,
+                         self.workspace, stream=stream, **self.options)
+        fp8_linear(mixed.view(n, -1), w["o"], w["o_s"], out, self.workspace, e8m0=self.e8m0, stream=stream)
+        return out
+
+    def status(self) -> int:
+        return moe_device_status(self.workspace)

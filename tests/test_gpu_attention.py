@@ -545,3 +545,42 @@ def test_streams_graph_and_one_workspace():
         torch.cuda.synchronize()
         want(x2)
     assert m.moe_device_status(ws) == m.MOE_OK
+
+
+def test_attention_decode_is_its_parts():
+    rng = np.random.default_rng(41)
+    hidden, heads, hk, D, page = 384, 6, 2, 64, 16
+    rows = (heads + 2 * hk) * D
+    (qkv, qkv_s), (o, o_s) = weights(rng, rows, hidden), weights(rng, hidden, heads * D)
+    wt = {"qkv": dev(qkv), "qkv_s": dev(qkv_s), "o": dev(o), "o_s": dev(o_s)}
+    cache = m.Fp8KvCache(8, hk, D, page)
+    turned = []
+    att = m.AttentionDecode(hidden, heads, hk, D, wt, cache, max_tokens=6, max_new=3, window=20,
+                            rotate=lambda q, k: turned.append((q.mul_(-1).shape, k.shape)))
+    table = dev(np.array([[3, 1], [0, 7]], np.int32))
+    x = bf16(bf16_values(rng, (5, hidden))).to(DEV)
+    start, lens = dev(np.array([0, 3, 5], np.int32)), dev(np.array([3, 2], np.int32))
+    y = att(x, table, start, lens)
+    assert att.status() == m.MOE_OK and turned == [((5, heads, D), (5, hk, D))]
+    # the same with the functions, from the cache that the step left
+    ws = workspace()
+    p = torch.empty((5, rows), dtype=torch.bfloat16, device=DEV)
+    m.fp8_linear(x, wt["qkv"], wt["qkv_s"], p, ws)
+    q = -p.view(5, -1, D)[:, :heads]
+    mixed, want = torch.empty_like(q), torch.empty_like(y)
+    m.decode_attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, start, lens, 3, mixed, ws, window=20)
+    m.fp8_linear(mixed.view(5, -1), wt["o"], wt["o_s"], want, ws)
+    assert torch.equal(y, want)
+    with pytest.raises(ValueError, match="at most 6"):
+        att(x.repeat(2, 1), table, start, lens)
+
+
+def test_decode_block_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_block.py")
+    spec = importlib.util.spec_from_file_location("decode_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    y = mod.main(["--steps", "3", "--batch", "3", "--prompt", "5"])
+    assert torch.isfinite(y.float()).all()
