@@ -11,11 +11,11 @@
 // the head, far below the tensor cores' balance, so the cache stream from HBM
 // is the floor.  One pass with the running maximum and sum of the softmax.
 //
-// Work split.  The unit is a tile of 8 KB of the cache (32 tokens of 128, 64 of
-// 64) of one item (sequence, kv head, group of up to 8 RT rows); an item counts
-// kItemCost tiles more for its start and end.  Every CTA (one per SM) adds up the
-// sequences' units for itself and takes an equal share of all of them, and each
-// of its eight warps an equal share of that, whatever the lengths: one long
+// Work split.  The unit is a tile of 32 tokens of one item (sequence, kv head,
+// group of up to 8 RT rows); an item counts kItemCost tiles more for its start and
+// end.  Every CTA (one per SM) adds up the sequences' units for itself and takes
+// an equal share of all of them, and each of its warps (8, or 16 for heads of 64)
+// an equal share of that, whatever the lengths: one long
 // sequence fills the GPU like a batch of short ones.  A warp works alone: it
 // looks up the pages, copies them (TMA, 128- or 64-byte swizzle) into its own ring
 // of tiles, and keeps its own maximum, sum and accumulator.  An item inside one
@@ -57,8 +57,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;                 // (255 registers a thread)
-constexpr int kThreads = kWarps * 32;
 constexpr int kItemCost = 2;              // units of an item beside its tiles
 constexpr int kMinUnits = 1;              // units of a warp at least
 constexpr float kLog2e = 1.4426950408889634f;
@@ -74,7 +72,13 @@ struct Piece {
 
 template <int D, int RT>
 struct AttCfg {
-  static constexpr int kTile = 4096 / D;                   // tokens of a tile
+  // Small heads hold few accumulators, and more of their time goes into the
+  // softmax of a byte's tokens than into waiting for the byte: more warps, with
+  // 128 registers each, instead of 255 (37.1 -> 33.3 us on 48 windowed, capped
+  // sequences of 16 heads of 64).
+  static constexpr int kWarps = D == 64 ? 16 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kTile = 32;                         // tokens of a tile
   static constexpr int kGroups = kTile / 16;
   static constexpr int kRowsC = 8 * RT;                    // rows of an item
   static constexpr int kHalfTile = kTile * D;              // bytes of the K (or V) part of a tile
@@ -86,8 +90,9 @@ struct AttCfg {
   static constexpr size_t kRecAt = kPartAt + (size_t)kWarps * kPartF * 4;
   static constexpr size_t kBarsAt = kRecAt + 2 * kWarps * sizeof(Piece);
   static constexpr size_t kMiscAt = kBarsAt + kWarps * kNST * 8;
-  static constexpr size_t kSmem = 1024 + kMiscAt + 16;
-  static_assert(kPartF * 4 <= kNST * kStage && kPartF % 4 == 0 && kSmem <= 227 * 1024, "shared memory");
+  static constexpr int kAlign = D == 64 ? 512 : 1024;      // of the swizzle's pattern
+  static constexpr size_t kSmem = kAlign + kMiscAt + 16;
+  static_assert(kPartF * 4 <= kNST * kStage && kPartF % 4 == 0 && kSmem + kWarps * 8 <= 227 * 1024, "shared memory");
 };
 
 struct AttMaps {
@@ -221,47 +226,48 @@ struct OutRow {
 };
 
 // Four columns of a row over several pieces, each with its own maximum and sum.
-// Lane k of 16 holds piece k's (maximum, sum) of a row; with 32 lanes to a row the
-// upper 16 do the same again.
+// The W lanes of a row hold a piece's (maximum, sum) each.
+template <int W>
 struct Joined {
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  MOE_DEV float weight16(float2 st) {  // this lane's piece's weight; M, L and acc follow
+  MOE_DEV float weight(float2 st) {  // this lane's piece's weight; M, L and acc follow
     float Mn = st.x;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
+    for (int o = W / 2; o > 0; o >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, o));
     Mn = fmaxf(Mn, M);
     const float ms = Mn == -INFINITY ? 0.f : Mn, e0 = ex2(M - ms);
     M = Mn;
     const float e = ex2(st.x - ms);
     float l = e * st.y;
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int o = W / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     L = L * e0 + l;
     acc.x *= e0; acc.y *= e0; acc.z *= e0; acc.w *= e0;
     return e;
   }
   MOE_DEV void add(float e, int k, float4 o) {
-    const float f = __shfl_sync(0xffffffffu, e, (threadIdx.x & 16) | k);
+    const float f = __shfl_sync(0xffffffffu, e, k, W);
     acc.x += o.x * f; acc.y += o.y * f; acc.z += o.z * f; acc.w += o.w * f;
   }
 };
 
 // Four columns of a finished row, and (first column) its log-sum-exp.
-MOE_DEV void store4(const AttArgs& a, const Piece& p, int r, int D, int d, const Joined& J) {
+MOE_DEV void store4(const AttArgs& a, const Piece& p, int r, int D, int d, float4 acc, float M, float L) {
   const OutRow at(a, p.start, p.row0 + r, p.head);
-  const float inv = J.L == 0.f ? 0.f : __fdiv_rn(1.f, J.L);
+  const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
   *reinterpret_cast<uint2*>(at.out(a, D) + d) =
-      make_uint2(pack_bf16(J.acc.x * inv, J.acc.y * inv), pack_bf16(J.acc.z * inv, J.acc.w * inv));
-  if (d == 0) at.lse(a, J.M, J.L);
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (d == 0) at.lse(a, M, L);
 }
 
 template <int D, int RT, bool MODS>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const __grid_constant__ AttMaps maps) {
+__global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel(AttArgs a, const __grid_constant__ AttMaps maps) {
   using C = AttCfg<D, RT>;
   constexpr int kRowsC = C::kRowsC, kTile = C::kTile, kGroups = C::kGroups, kNST = C::kNST;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (su32(smem_raw) & 1023)) & 1023);
+  uint8_t* smem = smem_raw + ((C::kAlign - (su32(smem_raw) & (C::kAlign - 1))) & (C::kAlign - 1));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* ring = smem + (size_t)warp * kNST * C::kStage;                      // this warp's
   Piece* recs = reinterpret_cast<Piece*>(smem + C::kRecAt);                     // [warp][first, last]
@@ -314,14 +320,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   if ((int)blockIdx.x >= G) return;  // (the whole CTA; nothing is in flight)
   const int Xq = (int)total / G, Xr = (int)total - Xq * G;
   const int X0 = cta_share(Xq, Xr, G, blockIdx.x), X1 = cta_share(Xq, Xr, G, blockIdx.x + 1);
-  auto share = [&](int w) { return X0 + ((X1 - X0) >> 3) * w + (((X1 - X0) & 7) * w >> 3); };
-  static_assert(kWarps == 8, "share");
+  auto share = [&](int w) {  // X0 + (X1 - X0) * w / kWarps
+    const int n = X1 - X0;
+    return X0 + n / kWarps * w + n % kWarps * w / kWarps;
+  };
   // the sequence this warp's share starts in: the last thread whose run of
   // sequences starts at or before it (and is not empty), then along that run
   int wb = 0, wat = 0;
   const int wx = share(warp);
   {
-    int best = -1;  // lane l looks at threads 8 l ... 8 l + 7
+    int best = -1;  // lane l looks at a run of threads
 #pragma unroll
     for (int k = 0; k < kThreads / 32; ++k) {
       const int at = s_before[lane * (kThreads / 32) + k];
@@ -677,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
           const float L = __shfl_sync(0xffffffffu, l[rt], 8 * q + 4 * c);
           const float M = __shfl_sync(0xffffffffu, m[rt], 8 * q + 4 * c);
           if (r < rows) {
-            const float inv = L == 0.f ? 0.f : __fdiv_rn(ru, L);
+            const float inv = L == 0.f ? 0.f : __fdividef(ru, L);
             const OutRow o_at(a, w.s.start, w.grp * kRowsC + r, w.head);
             uint32_t v[kMT];
 #pragma unroll
@@ -721,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
   // finds the items for itself: lane x looks at piece x.
   constexpr int kVec = D / 4;          // lanes of a row, four columns each
   constexpr int kRPW = 32 / kVec;      // rows of a warp at a time
-  static_assert(2 * kWarps == 16, "a piece for each of 16 lanes");
+  static_assert(2 * kWarps <= 32, "a piece for each lane");
   const int d = lane % kVec * 4;
   const int my_item = lane < 2 * kWarps ? recs[lane].item0 : -1;
   const uint32_t there = __ballot_sync(0xffffffffu, my_item >= 0);
@@ -752,27 +760,29 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
     const Piece rec = recs[x0];
     const uint32_t pieces = item_pieces(x0);
     const bool final_ = (outs >> x0 & 1) == 0;
+    float2 st[2 * kWarps];  // (read together)
     float M = -INFINITY, L = 0.f;
-    for (uint32_t m = pieces; m; m &= m - 1) {
-      const int k = __ffs(m) - 1;
-      M = fmaxf(M, part_of(k >> 1, k & 1)[kRowsC * D + 2 * r]);
+#pragma unroll
+    for (int k = 0; k < 2 * kWarps; ++k) {
+      st[k] = make_float2(-INFINITY, 0.f);
+      if (pieces >> k & 1) st[k] = *reinterpret_cast<const float2*>(part_of(k >> 1, k & 1) + kRowsC * D + 2 * r);
+      M = fmaxf(M, st[k].x);
     }
     const float ms = M == -INFINITY ? 0.f : M;
-    for (uint32_t m = pieces; m; m &= m - 1) {
-      const int k = __ffs(m) - 1;
-      float2* st = reinterpret_cast<float2*>(part_of(k >> 1, k & 1) + kRowsC * D + 2 * r);
-      st->x = ex2(st->x - ms);
-      L += st->x * st->y;
+#pragma unroll
+    for (int k = 0; k < 2 * kWarps; ++k) {
+      st[k].x = ex2(st[k].x - ms);
+      L += st[k].x * st[k].y;
     }
-    if (final_) {
-      const float inv = L == 0.f ? 0.f : __fdiv_rn(1.f, L);
-      for (uint32_t m = pieces; m; m &= m - 1) {
-        const int k = __ffs(m) - 1;
-        part_of(k >> 1, k & 1)[kRowsC * D + 2 * r] *= inv;
-      }
-      if (r < rec.rows) OutRow(a, rec.start, rec.row0 + r, rec.head).lse(a, M, L);
-    } else if (r < rec.rows) {
-      __stcg(reinterpret_cast<float2*>(cta_part(rec) + kRowsC * D + 2 * r), make_float2(M, L));
+    const float inv = !final_ ? 1.f : L == 0.f ? 0.f : __fdividef(1.f, L);
+#pragma unroll
+    for (int k = 0; k < 2 * kWarps; ++k)
+      if (pieces >> k & 1) part_of(k >> 1, k & 1)[kRowsC * D + 2 * r] = st[k].x * inv;
+    if (r < rec.rows) {
+      if (final_)
+        OutRow(a, rec.start, rec.row0 + r, rec.head).lse(a, M, L);
+      else
+        __stcg(reinterpret_cast<float2*>(cta_part(rec) + kRowsC * D + 2 * r), make_float2(M, L));
     }
   }
   __syncthreads();
@@ -830,21 +840,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttArgs a, const
     for (int rb = warp * kRPW; rb < rec.rows; rb += kWarps * kRPW) {
       const int r = rb + lane / kVec;
       auto piece = [&](int c) { return a.partials + ((size_t)c * 2 + (c == c0)) * C::kPartF; };
-      Joined J;
-      for (int c = c0; c <= c1; c += 16) {
-        const int x = lane & 15, n = min(16, c1 + 1 - c);
+      Joined<kVec> J;
+      for (int c = c0; c <= c1; c += kVec) {
+        const int x = lane % kVec, n = min(kVec, c1 + 1 - c);
         float2 st = make_float2(-INFINITY, 0.f);
-        if (x < n && r < rec.rows) st = __ldcg(reinterpret_cast<const float2*>(piece(c + x) + kRowsC * D + 2 * r));
-        float4 v[16];  // all reads in flight
+        if (x < n) st = __ldcg(reinterpret_cast<const float2*>(piece(c + x) + kRowsC * D + 2 * r));
+        float4 v[kVec];  // all reads in flight
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          v[k] = k < n && r < rec.rows ? __ldcg(reinterpret_cast<const float4*>(piece(c + k) + (size_t)r * D + d))
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float e = J.weight16(st);
+        for (int k = 0; k < kVec; ++k)
+          v[k] = k < n ? __ldcg(reinterpret_cast<const float4*>(piece(c + k) + (size_t)r * D + d))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float e = J.weight(st);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) J.add(e, k, v[k]);
+        for (int k = 0; k < kVec; ++k) J.add(e, k, v[k]);
       }
-      if (r < rec.rows) store4(a, rec, r, D, d, J);
+      if (r < rec.rows) store4(a, rec, r, D, d, J.acc, J.M, J.L);
     }
   }
 }
@@ -854,7 +864,7 @@ bool map_cache(CUtensorMap* m, const uint8_t* base, int D, int P, long long tile
   if (!encode_fn()) return false;
   const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)P, (cuuint64_t)tiles};
   const cuuint64_t stride[2] = {(cuuint64_t)D, (cuuint64_t)P * D};
-  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)std::min(P, 4096 / D), 1};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)std::min(P, 32), 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dim, stride, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -867,7 +877,7 @@ cudaError_t launch_cfg(const AttArgs& a, const AttMaps& maps, int ctas, cudaStre
   static const cudaError_t rc =
       cudaFuncSetAttribute(attention_kernel<D, RT, MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (rc != cudaSuccess) return rc;
-  attention_kernel<D, RT, MODS><<<ctas, kThreads, C::kSmem, s>>>(a, maps);
+  attention_kernel<D, RT, MODS><<<ctas, C::kThreads, C::kSmem, s>>>(a, maps);
   return cudaGetLastError();
 }
 
