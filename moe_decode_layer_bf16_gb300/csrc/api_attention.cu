@@ -183,7 +183,7 @@ int fp8_linear(const void* x, long long x_stride, const uint8_t* w, const float*
   if ((rc = quant_launch(x, x_stride, M, K, e8m0, codes, scales, (cudaStream_t)stream)) != MOE_OK) return rc;
   // the product streams its first weights while the quantisation still runs
   a.xs = scales;
-  a.pdl = true;
+  a.after_quant = true;
   return gemm_launch(a, codes, w, M, N, K, l, partials, (cudaStream_t)stream);
 }
 

@@ -285,6 +285,10 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     recs[2 * warp].item0 = recs[2 * warp + 1].item0 = -1;
   }
 
+  // launched while the kernel before may still run: nothing of its is read, and
+  // nothing written, before it is complete
+  grid_dep_launch();
+  grid_dep_wait();
   // ---- the shares: every thread adds up a run of sequences, then a scan
   __shared__ long long s_scan[kWarps];
   int* s_before = reinterpret_cast<int*>(smem + C::kPartAt);  // [thread]: first unit of its sequences (the pieces come later)
@@ -877,8 +881,8 @@ cudaError_t launch_cfg(const AttArgs& a, const AttMaps& maps, int ctas, cudaStre
   static const cudaError_t rc =
       cudaFuncSetAttribute(attention_kernel<D, RT, MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (rc != cudaSuccess) return rc;
-  attention_kernel<D, RT, MODS><<<ctas, C::kThreads, C::kSmem, s>>>(a, maps);
-  return cudaGetLastError();
+  PdlLaunch L(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
+  return cudaLaunchKernelEx(&L.cfg, attention_kernel<D, RT, MODS>, a, maps);
 }
 
 template <int D>

@@ -95,6 +95,7 @@ MOE_DEV float amax8(const uint4& v) {
 }
 
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) {
+  grid_dep_wait();    // (launched while the kernel before may still run)
   grid_dep_launch();  // the product may start streaming its weights now
   const int lane = threadIdx.x & 31, lane16 = lane & 15;
   const int n_runs = (a.nkb + 7) / 8, n_units = a.M * n_runs;
@@ -282,6 +283,11 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // launched while the kernel before may still run.  Where that is this call's
+  // quantisation, the weights need not wait for it; else nothing is read or
+  // written before it is complete.
+  grid_dep_launch();
+  if (!p.after_quant) grid_dep_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -676,12 +682,8 @@ cudaError_t launch_nt(const LinPlan& p, const LinArgs& a, const LinMaps& maps, c
   static const cudaError_t rc =
       cudaFuncSetAttribute(linear_kernel<NT, TR, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (rc != cudaSuccess) return rc;
-  if (a.pdl) {
-    PdlLaunch L(dim3(p.G), dim3(C::kThreads), C::kSmem, s);
-    return cudaLaunchKernelEx(&L.cfg, linear_kernel<NT, TR, XQ>, a, maps);
-  }
-  linear_kernel<NT, TR, XQ><<<p.G, C::kThreads, C::kSmem, s>>>(a, maps);
-  return cudaGetLastError();
+  PdlLaunch L(dim3(p.G), dim3(C::kThreads), C::kSmem, s);
+  return cudaLaunchKernelEx(&L.cfg, linear_kernel<NT, TR, XQ>, a, maps);
 }
 
 }  // namespace
@@ -713,8 +715,8 @@ size_t linear_partial_bytes(const LinPlan& p) {
 cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s) {
   if (a.M == 0) return cudaSuccess;
   const int units = a.M * ((a.nkb + 7) / 8), per = kQuantThreads / 32;
-  quant_rows_kernel<<<(unsigned)std::min((units + per - 1) / per, sms * 8), kQuantThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  PdlLaunch L(dim3((unsigned)std::min((units + per - 1) / per, sms * 8)), dim3(kQuantThreads), 0, s);
+  return cudaLaunchKernelEx(&L.cfg, quant_rows_kernel, a);
 }
 
 cudaError_t launch_linear(const LinPlan& p, LinArgs a, const uint8_t* xq, const uint8_t* w, cudaStream_t s) {

@@ -230,8 +230,8 @@ struct LinArgs {
   int* status = nullptr;
   int* tickets = nullptr;      // [G], zero between calls
   float* partials = nullptr;   // [G_split][2][nt][128]
-  bool pdl = false;            // the codes and scales come from the kernel just enqueued, a
-                               // launch_quant_rows; w and w_s do not
+  bool after_quant = false;    // the kernel just enqueued is the launch_quant_rows that writes the
+                               // codes and scales, and no other input
   // the plan's
   int mp, M, N, K, nkb, chunk, n_wt, n_wblk, G, waves, G_split;
   int share_q, share_r;  // split cells = share_q * G_split + share_r

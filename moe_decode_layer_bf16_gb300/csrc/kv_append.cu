@@ -64,6 +64,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   const int b = a.blocks == 1 ? blockIdx.x : blockIdx.x / a.blocks, j = blockIdx.x - b * a.blocks;
   const int head = blockIdx.y;
   const bool kv = blockIdx.z != 0;  // values
+  // launched while the kernel before may still run: nothing is read before it is complete
+  grid_dep_launch();
+  grid_dep_wait();
   const int start = __ldg(a.q_start + b), stop = __ldg(a.q_start + b + 1);
   const int len = __ldg(a.lens + b);
   const int n = stop - start;
@@ -147,14 +150,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
 
 template <int D>
 cudaError_t launch_d(const AppendArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)(a.B * a.blocks), (unsigned)a.kv_heads, 2);
+  PdlLaunch L(dim3((unsigned)(a.B * a.blocks), (unsigned)a.kv_heads, 2), dim3(kThreads), 0, s);
   switch (a.page_size) {
-    case 16: kv_append_kernel<D, 16><<<grid, kThreads, 0, s>>>(a); break;
-    case 32: kv_append_kernel<D, 32><<<grid, kThreads, 0, s>>>(a); break;
-    case 64: kv_append_kernel<D, 64><<<grid, kThreads, 0, s>>>(a); break;
-    default: kv_append_kernel<D, 128><<<grid, kThreads, 0, s>>>(a); break;
+    case 16: return cudaLaunchKernelEx(&L.cfg, kv_append_kernel<D, 16>, a);
+    case 32: return cudaLaunchKernelEx(&L.cfg, kv_append_kernel<D, 32>, a);
+    case 64: return cudaLaunchKernelEx(&L.cfg, kv_append_kernel<D, 64>, a);
+    default: return cudaLaunchKernelEx(&L.cfg, kv_append_kernel<D, 128>, a);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
