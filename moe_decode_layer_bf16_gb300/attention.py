@@ -12,16 +12,13 @@ AttentionDecode runs them together as a decode step does.
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
-from . import MOE_OK, MoeError, lib, moe_device_status, moe_workspace_init
+from . import MOE_OK, MoeError, _stream, lib, moe_device_status, moe_workspace_init
 
 _vp, _i, _f, _sz, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 _bf16, _f32, _u8, _e4m3, _i32 = torch.bfloat16, torch.float32, torch.uint8, torch.float8_e4m3fn, torch.int32
-# the current stream's handle and the current device without the objects around them
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class _Cache(ctypes.Structure):
@@ -48,19 +45,34 @@ def bind(L):
         getattr(L, n).restype = ctypes.c_int
 
 
+_native = None
+
+
+def _calls():
+    """The extension module that checks the tensors and calls the library; loaded
+    with it, and as indispensable."""
+    global _native
+    if _native is None:
+        lib()
+        try:
+            from . import _calls as native
+        except ImportError as e:
+            raise RuntimeError(f"_calls.so is not built (python -m moe_decode_layer_bf16_gb300.build): {e}") from e
+        _native = native
+    return _native
+
+
 def _fail(rc: int, what: str):
     raise MoeError(rc, what)
 
 
-def _handle(stream, dev: int) -> int:
-    if stream is None:
-        return _raw_stream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+def _handle(stream):
+    """The stream's handle, or None for the current one."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
-# Every call's checks come twice: as one expression that decides, on the way of
-# each step, whether all is well (attribute reads cost about 0.1 us each), and as
-# these functions, which find what is not and say so.
+# The extension module refuses what is not as an operator wants it without a
+# word; these functions find out what it was and say so.
 def _want(t, name, dtype, shape):
     """t is a dense tensor of this dtype and shape (None: any size)."""
     if t.dtype is not dtype and not (dtype is _u8 and t.dtype is _e4m3):
@@ -90,18 +102,13 @@ def _want_device(*tensors):
         if t is not None and not t.is_cuda:
             raise ValueError(f"CUDA tensors are wanted, got one on {t.device}")
     for t in tensors:
-        if t is not None and t.get_device() != _device():
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{_device()}")
+        if t is not None and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _want_workspace(workspace):
     if not workspace.is_contiguous():
         raise ValueError("workspace: a dense tensor is wanted")
-
-
-def _row_stride(M: int, stride: int, n: int) -> int:
-    """Elements between rows of n; where there is only one, its stride says nothing."""
-    return stride if M > 1 else n + 7 & -8
 
 
 def _size(what, *args) -> int:
@@ -136,8 +143,9 @@ def fp8_quant_rows(x, codes, scales, e8m0: bool = False, stream=None):
     _want(codes, "codes", _u8, (M, K))
     _want(scales, "scales", _f32, (-(-K // 128), M + 3 & -4))
     _want_device(x, codes, scales)
-    rc = lib().fp8_quant_rows(x.data_ptr(), _row_stride(M, x.stride(0), K), M, K, 1 if e8m0 else 0, codes.data_ptr(),
-                              scales.data_ptr(), _handle(stream, x.get_device()))
+    # (where there is only one row, its stride says nothing)
+    rc = lib().fp8_quant_rows(x.data_ptr(), x.stride(0) if M > 1 else K + 7 & -8, M, K, 1 if e8m0 else 0,
+                              codes.data_ptr(), scales.data_ptr(), _stream(stream))
     if rc != MOE_OK:
         _fail(rc, "fp8_quant_rows")
 
@@ -163,7 +171,7 @@ def fp8_block_gemm(codes, scales, w, w_s, out, workspace, stream=None):
     _want_device(codes, scales, w, w_s, out, workspace)
     rc = lib().fp8_block_gemm(codes.data_ptr(), scales.data_ptr(), w.data_ptr(), w_s.data_ptr(), M, N, K,
                               out.data_ptr(), 1 if out.dtype is _f32 else 0, workspace.data_ptr(), workspace.nbytes,
-                              _handle(stream, codes.get_device()))
+                              _stream(stream))
     if rc != MOE_OK:
         _fail(rc, "fp8_block_gemm")
 
@@ -181,41 +189,9 @@ def fp8_linear(x, w, w_s, out, workspace, e8m0: bool = False, stream=None):
     """out = x . w^T: x (bf16 [M, K], any row stride) quantised per token per
     128 columns, w (E4M3 [N, K]) with float32 scales w_s for each 128 x 128
     block; out bf16 or float32 [M, N]."""
-    if x.dim() != 2 or w.dim() != 2:
-        _linear_refused(x, w, w_s, out, workspace)
-    M, K = x.shape
-    N = w.shape[0]
-    sm, sk = x.stride()
-    wt, ot, dev = w.dtype, out.dtype, x.get_device()
-    if not (x.dtype is _bf16 and (wt is _u8 or wt is _e4m3) and w_s.dtype is _f32 and (ot is _bf16 or ot is _f32)
-            and w.shape == (N, K) and w_s.shape == (N + 127 >> 7, K + 127 >> 7) and out.shape == (M, N)
-            and (sk == 1 or K == 1) and w.is_contiguous() and w_s.is_contiguous() and out.is_contiguous()
-            and workspace.is_contiguous() and x.get_device() == dev and w.get_device() == dev
-            and w_s.get_device() == dev and out.get_device() == dev and workspace.get_device() == dev
-            and dev >= 0 and dev == _device()):
-        _linear_refused(x, w, w_s, out, workspace)
-    rc = lib().fp8_linear(x.data_ptr(), sm if M > 1 else K + 7 & -8, w.data_ptr(), w_s.data_ptr(), M, N, K,
-                          1 if e8m0 else 0, out.data_ptr(), 1 if ot is _f32 else 0, workspace.data_ptr(),
-                          workspace.nbytes, _handle(stream, dev))
-    if rc != MOE_OK:
-        _fail(rc, "fp8_linear")
-
-
-def _batch_ok(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace, dev):
-    """The cache and the batch are as _batch_refused wants them."""
-    shape, st = k_cache.shape, (k_cache.shape[0], k_cache.shape[1])
-    B = lens.shape[0]
-    kt, vt = k_cache.dtype, v_cache.dtype
-    return ((kt is _u8 or kt is _e4m3) and (vt is _u8 or vt is _e4m3) and v_cache.shape == shape
-            and k_scale.dtype is _f32 and v_scale.dtype is _f32 and k_scale.shape == st and v_scale.shape == st
-            and page_table.dtype is _i32 and q_start.dtype is _i32 and lens.dtype is _i32
-            and page_table.dim() == 2 and page_table.shape[0] == B and q_start.shape == (B + 1,) and lens.dim() == 1
-            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
-            and v_scale.is_contiguous() and page_table.is_contiguous() and q_start.is_contiguous()
-            and lens.is_contiguous() and workspace.is_contiguous() and k_cache.get_device() == dev
-            and v_cache.get_device() == dev and k_scale.get_device() == dev and v_scale.get_device() == dev
-            and page_table.get_device() == dev and q_start.get_device() == dev and lens.get_device() == dev
-            and workspace.get_device() == dev)
+    rc = _calls().fp8_linear(x, w, w_s, out, workspace, e8m0, _handle(stream))
+    if rc:
+        _linear_refused(x, w, w_s, out, workspace) if rc < 0 else _fail(rc, "fp8_linear")
 
 
 def _batch_refused(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace):
@@ -234,25 +210,11 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_star
                     stream=None):
     """Write new tokens' keys and values (bf16 [total, kv heads, head dim], any
     token stride) into the cache; see include/moe_decode.h for the batch."""
-    dev = k.get_device()
-    if k_cache.dim() != 4 or k.dim() != 3 or v.dim() != 3:
+    rc = _calls().kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, max_new, workspace,
+                                  _handle(stream))
+    if rc < 0:
         _append_refused(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
-    pages, hk, page, d = k_cache.shape
-    total = k.shape[0]
-    k0, k1, k2 = k.stride()
-    v0, v1, v2 = v.stride()
-    if not (_batch_ok(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace, dev)
-            and k.dtype is _bf16 and v.dtype is _bf16 and k.shape == (total, hk, d) and v.shape == (total, hk, d)
-            and k2 == 1 and v2 == 1 and (hk == 1 or (k1 == d and v1 == d))
-            and v.get_device() == dev and dev >= 0 and dev == _device()):
-        _append_refused(k, v, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace)
-    if total <= 1:
-        k0 = v0 = hk * d
-    rc = lib().kv_cache_append(
-        _Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, hk, page, d),
-        k.data_ptr(), k0, v.data_ptr(), v0, page_table.data_ptr(), page_table.shape[1], q_start.data_ptr(),
-        lens.data_ptr(), lens.shape[0], total, max_new, workspace.data_ptr(), workspace.nbytes, _handle(stream, dev))
-    if rc != MOE_OK:
+    elif rc:
         _fail(rc, "kv_cache_append")
 
 
@@ -271,29 +233,11 @@ def decode_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, q_start,
     """Attention of a step's tokens (q bf16 [total, heads, head dim], any token
     stride) over the cache.  out bf16 like q; lse float32 [total, heads] or
     None; sm_scale 1 / sqrt(head dim) by default; slopes float32 [heads]."""
-    dev = q.get_device()
-    if k_cache.dim() != 4 or q.dim() != 3:
+    rc = _calls().decode_attention(q, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, max_new, out,
+                                   workspace, lse, sm_scale, softcap, window, slopes, _handle(stream))
+    if rc < 0:
         _attention_refused(q, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, out, workspace, lse, slopes)
-    pages, hk, page, d = k_cache.shape
-    shape = q.shape
-    total, h, dq = shape
-    q0, q1, q2 = q.stride()
-    if not (_batch_ok(k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, workspace, dev)
-            and q.dtype is _bf16 and out.dtype is _bf16 and dq == d and out.shape == shape
-            and q2 == 1 and (h == 1 or q1 == d) and out.is_contiguous()
-            and out.get_device() == dev and dev >= 0 and dev == _device()
-            and (lse is None or (lse.dtype is _f32 and lse.shape == (total, h) and lse.is_contiguous()
-                                 and lse.get_device() == dev))
-            and (slopes is None or (slopes.dtype is _f32 and slopes.shape == (h,) and slopes.is_contiguous()
-                                    and slopes.get_device() == dev))):
-        _attention_refused(q, k_cache, v_cache, k_scale, v_scale, page_table, q_start, lens, out, workspace, lse, slopes)
-    rc = lib().decode_attention(
-        _Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, hk, page, d),
-        q.data_ptr(), q0 if total > 1 else h * d, h, page_table.data_ptr(), page_table.shape[1], q_start.data_ptr(),
-        lens.data_ptr(), lens.shape[0], total, max_new, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale, softcap,
-        window, None if slopes is None else slopes.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes, _handle(stream, dev))
-    if rc != MOE_OK:
+    elif rc:
         _fail(rc, "decode_attention")
 
 

@@ -1,5 +1,7 @@
 """Build libmoe_decode.so in-tree for sm_103a (nvcc, one object per source,
-compiled in parallel, then linked).  Usage: python -m moe_decode_layer_bf16_gb300.build"""
+compiled in parallel, then linked), and beside it _calls.so, the extension module
+through which Python makes the attention operators' calls.
+Usage: python -m moe_decode_layer_bf16_gb300.build"""
 
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_decode.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["api.cu", "gemv.cu", "experts.cu", "experts_tc.cu", "rmsnorm.cu", "mtp.cu",
            "api_attention.cu", "fp8_linear.cu", "kv_append.cu", "attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -33,6 +36,20 @@ def _newer(target: str, deps) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def _torch_root() -> str:
+    import importlib.util  # (where torch is, without importing it)
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def calls_command(source: str, obj: str):
+    """Compiles calls.cpp against this interpreter's and this torch's headers."""
+    import sysconfig
+    inc = os.path.join(_torch_root(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    dirs = [inc, os.path.join(inc, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", *("-I" + d for d in dirs), "-c", source, "-o", obj]
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
@@ -42,26 +59,33 @@ def build(verbose: bool = False, extra_flags=None) -> str:
 
     def compile_one(src):
         s = os.path.join(CSRC, src)
-        o = os.path.join(BUILD, src.replace(".cu", ".o"))
+        o = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         if _newer(o, [s, *headers]) and not extra:
             return o
-        cmd = [cc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o]
+        cmd = calls_command(s, o) if src.endswith(".cpp") else [cc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {src}:\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, flush=True)
         return o
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    if not _newer(LIB, objs):
-        cmd = [cc, *ARCH, "-shared", "-o", LIB, *objs]
+    def link(target, objs, cmd):
+        if _newer(target, objs):
+            return
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        *objs, calls = ex.map(compile_one, [*SOURCES, "calls.cpp"])
+    link(LIB, objs, [cc, *ARCH, "-shared", "-o", LIB, *objs])
+    libs = os.path.join(_torch_root(), "lib")
+    link(CALLS, [calls, LIB],
+         [os.environ.get("CXX", "g++"), "-shared", "-o", CALLS, calls, "-L" + libs, "-ltorch_python", "-ltorch",
+          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libmoe_decode.so", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs])
     return LIB
 
 
