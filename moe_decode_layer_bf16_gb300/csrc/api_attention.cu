@@ -46,7 +46,7 @@ size_t linear_partial_bound(int M, int N, int K) {
   LinPlan p;
   plan_linear(p, std::max(M, 1), N, K, kLinMaxCtas);
   const long long cells = (long long)p.n_tt * p.n_wt * p.nkb;
-  const long long ctas = std::min<long long>(kLinMaxCtas, cells);
+  const long long ctas = std::min<long long>(kLinMaxCtas, p.tok_rows ? 2 * cells : cells);
   return (size_t)ctas * 2 * p.nt * kBlock * sizeof(float);
 }
 

@@ -12,9 +12,11 @@
 // The product, in two arrangements of one kernel.  Up to 128 tokens the weights are
 // the MMA's 128 rows and the tokens its columns (NT = 16 .. 128), so that one
 // token still fills the MMA's rows and the weights are streamed once.  Above,
-// 128 tokens are the rows and 256 weight rows the columns: a thread of the
-// epilogue then owns one token and one weight block, and needs one scale for
-// its 128 columns.
+// 256 tokens are the rows and 256 weight rows the columns of a pair of CTAs
+// (cta_group::2): each holds 128 of the tokens with their accumulators and 128
+// of the weight rows, so a cell of 256 x 256 takes 32 KB of copies in each CTA
+// where a CTA alone needs 48 KB for half of it.  A thread of the epilogue then
+// owns one token and one weight block, and needs one scale for its 128 columns.
 //
 // The unit of work is a cell: a pair of a row tile and a column tile in one
 // 128-column k-block, i.e. one tile of each operand through TMA (128-byte
@@ -23,8 +25,9 @@
 // are fp32 values of their own for each k-block, so they cannot ride in the
 // MMA.  Rows past N, tokens past M and columns past K are zeros of the TMA fill.
 //
-// Work split.  One CTA per SM.  Whole waves of pairs are dealt out as they are;
-// the remaining pairs are cut along K into one equal share of cells per CTA
+// Work split.  One CTA per SM (a pair of CTAs counts as one here).  Whole waves of
+// pairs of tiles are dealt out as they are; the remaining ones are cut along K
+// into one equal share of cells per CTA
 // (stream-K), so that one token's 72 row tiles keep all 152 SMs streaming.  A
 // CTA that holds a piece of a pair writes its fp32 sums to the workspace; the
 // last to arrive adds the pieces in k order (the result does not depend on who
@@ -143,8 +146,10 @@ struct Cfg {
   // token 20.0 us)
   static constexpr int kQW = XQ ? 6 : 0;
   static constexpr int kThreads = (kEW1 + (XQ ? kQW - 2 : 0)) * 32;
-  static constexpr int kCBox = TR ? NT : std::min(NT, 32);    // column rows of one copy (tokens: no more than there are)
-  static constexpr int kStage = kRTile + NT * 128;            // ring stage: a row tile and a column tile
+  static constexpr bool kPair = TR;                           // two CTAs work on a cell
+  static constexpr int kCRows = kPair ? NT / 2 : NT;          // rows of this CTA's column tile
+  static constexpr int kCBox = TR ? kCRows : std::min(NT, 32);  // of them in one copy (tokens: no more than there are)
+  static constexpr int kStage = kRTile + kCRows * 128;        // ring stage: a row tile and a column tile
   static constexpr int kRaw = XQ ? 2 : 1;                     // cells of a quantising warp whose rows of x are on their way
   static constexpr size_t kRawBytes = (size_t)kQW * kRaw * NT * 256;
   static constexpr int kNST = std::min(12, (int)((212 * 1024 - kRawBytes) / kStage));
@@ -183,17 +188,18 @@ struct Pieces {
   int w, t, k;       // next cell of the split pairs: weight tile, token tile, k-block
   int we, te, ke;    // where the CTA's share of them ends
   int k0, k1;        // the current piece: k-blocks
-  int row, col;      // its row and column tile
+  int cw, ct;        // its weight tile and token tile (of both CTAs)
+  int row, col;      // this CTA's row tile, and the column tile
   MOE_DEV explicit Pieces(const LinArgs& a) : p(a), i(0) {
-    const int c = min((int)blockIdx.x, p.G_split), e = min((int)blockIdx.x + 1, p.G_split);
+    const int c = min(cta(), p.G_split), e = min(cta() + 1, p.G_split);
     w = p.starts[c].w; t = p.starts[c].t; k = p.starts[c].k;
     we = p.starts[e].w; te = p.starts[e].t; ke = p.starts[e].k;
   }
+  MOE_DEV int cta() const { return p.tok_rows ? blockIdx.x >> 1 : blockIdx.x; }
   MOE_DEV bool next() {
-    int cw, ct;
     if (i < p.waves) {
       // weight tiles follow one another within a token tile
-      const int pair = i++ * p.G + blockIdx.x;
+      const int pair = i++ * p.G + cta();
       ct = pair / p.n_wt;
       cw = pair - ct * p.n_wt;
       k0 = 0;
@@ -208,13 +214,12 @@ struct Pieces {
       k = last ? ke : 0;
       if (!last && ++w == p.n_wt) { w = 0; ++t; }
     }
-    row = p.tok_rows ? ct : cw;
+    row = p.tok_rows ? 2 * ct + (blockIdx.x & 1) : cw;
     col = p.tok_rows ? cw : ct;
     return true;
   }
   // CTA that holds k-block kb of the current (split) pair
   MOE_DEV int owner(int kb) const {
-    const int cw = p.tok_rows ? col : row, ct = p.tok_rows ? row : col;
     const int x = (ct * p.n_wt + cw - p.waves * p.G) * p.nkb + kb;  // of all split cells
     int o = min(x / p.share_q, p.G_split - 1);
     while (p.share_q * o + p.share_r * o / p.G_split > x) --o;
@@ -261,12 +266,12 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.w) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.x) : "memory");
     for (int i = 0; i < C::kNST; ++i) {
-      mbar_init(full + i, XQ ? 2 : 1);  // the copies, and a quantising warp
+      mbar_init(full + i, XQ || C::kPair ? 2 : 1);  // the copies (of both CTAs), and a quantising warp
       mbar_init(empty + i, 1);
     }
     for (int i = 0; i < C::kTST; ++i) {
       mbar_init(tfull + i, 1);
-      mbar_init(tempty + i, kNEpi);
+      mbar_init(tempty + i, C::kPair ? 2 * kNEpi : kNEpi);  // (a pair's MMAs wait for both CTAs' epilogues)
     }
     for (int i = 0; i < C::kXST; ++i) {
       mbar_init(sfull + i, 1);
@@ -278,10 +283,17 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMW) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32((const void*)s_misc)),
-                 "r"(C::kTCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (C::kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32((const void*)s_misc)),
+                   "r"(C::kTCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32((const void*)s_misc)),
+                   "r"(C::kTCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   // launched while the kernel before may still run.  Where that is this call's
   // quantisation, the weights need not wait for it; else nothing is read or
@@ -289,9 +301,10 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
   grid_dep_launch();
   if (!p.after_quant) grid_dep_wait();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (C::kPair) cluster_sync(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)s_misc[0];
+  const int rank = C::kPair ? blockIdx.x & 1 : 0;  // CTA of the pair; CTA 0 issues the MMAs
   Pieces pc(p);
   // tokens of a token tile, live columns of a column tile
   auto toks = [&](int t) { return min(p.chunk, p.M - t * p.chunk); };
@@ -308,11 +321,15 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
         auto load_w = [&](const Pieces& q, int kb, int si) {
           uint8_t* st = ring + (size_t)si * C::kStage;
           const int nbox = XQ ? 0 : (cols(q.col) + C::kCBox - 1) / C::kCBox;
-          mbar_expect_tx(full + si, (uint32_t)(kRTile + nbox * C::kCBox * 128));
-          if (TR)
-            tma_load_2d(st + kRTile, &maps.w, kb * kBlock, q.col * NT, full + si);
-          else
+          if constexpr (C::kPair) {
+            // both CTAs' copies count on CTA 0's barrier
+            const uint32_t bar = mapa(su32(full + si), 0);
+            mbar_expect_tx_at(bar, (uint32_t)(kRTile + C::kCRows * 128));
+            tma_load_2d_pair(st + kRTile, &maps.w, kb * kBlock, q.col * NT + rank * C::kCRows, bar);
+          } else {
+            mbar_expect_tx(full + si, (uint32_t)(kRTile + nbox * C::kCBox * 128));
             tma_load_2d(st, &maps.w, kb * kBlock, q.row * kRows, full + si);
+          }
         };
         {
           Pieces q(p);
@@ -335,25 +352,29 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
               load_w(pc, kb, si);
             }
             uint8_t* xt = ring + (size_t)si * C::kStage + (TR ? 0 : kRTile);
-            for (int b = 0; b < nbox; ++b)
-              tma_load_2d(xt + b * C::kCBox * 128, &maps.x, kb * kBlock, t0 + b * C::kCBox, full + si);
+            if constexpr (C::kPair)
+              tma_load_2d_pair(xt, &maps.x, kb * kBlock, t0, mapa(su32(full + si), 0));
+            else
+              for (int b = 0; b < nbox; ++b)
+                tma_load_2d(xt + b * C::kCBox * 128, &maps.x, kb * kBlock, t0 + b * C::kCBox, full + si);
             ++gs;
             if (++si == C::kNST) { si = 0; ph ^= 1u; }
           }
         }
-        // every copy this CTA issued lands before it ends
-        for (uint32_t j = (gs > (uint32_t)C::kNST ? gs - C::kNST : 0); j < gs; ++j)
+        // every copy this CTA issued lands before it ends (a pair's, before both end)
+        for (uint32_t j = (gs > (uint32_t)C::kNST ? gs - C::kNST : 0); j < gs && rank == 0; ++j)
           mbar_wait_landed(full + (j % C::kNST), (j / C::kNST) & 1u, status);
       }
       __syncwarp();
     } else if (warp == kMW) {
       // ================================================================ MMA issue
-      if (elect_one()) {
+      if (rank == 0 && elect_one()) {
         int si = 0, ti = 0;
         uint32_t ph = 0, tp = 0;
         bool alive = true;
         while (alive && pc.next()) {
-          const uint32_t idesc = instr_desc(kRows, (cols(pc.col) + 15) & ~15);
+          // (a pair's columns are always 256: those past N are zeros)
+          const uint32_t idesc = C::kPair ? instr_desc(2 * kRows, NT) : instr_desc(kRows, (cols(pc.col) + 15) & ~15);
           for (int kb = pc.k0; kb < pc.k1; ++kb) {
             if (!mbar_wait_landed(tempty + ti, tp ^ 1u, status) || !mbar_wait_landed(full + si, ph, status)) {
               alive = false;
@@ -363,16 +384,23 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
             const uint32_t sb = su32(ring + (size_t)si * C::kStage);
             const uint64_t da = smem_desc(sb), db = smem_desc(sb + kRTile);
             const uint32_t dt = tmem + (uint32_t)(ti * NT);
+            if constexpr (C::kPair) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) tc_mma(dt, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1 : 0);
-            tc_commit(empty + si);
-            tc_commit(tfull + ti);
+              for (int kk = 0; kk < 4; ++kk) tc_mma_pair(dt, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1 : 0);
+              tc_commit_pair(empty + si);
+              tc_commit_pair(tfull + ti);
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) tc_mma(dt, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1 : 0);
+              tc_commit(empty + si);
+              tc_commit(tfull + ti);
+            }
             if (++si == C::kNST) { si = 0; ph ^= 1u; }
             if (++ti == C::kTST) { ti = 0; tp ^= 1u; }
           }
         }
         // every MMA this thread issued is complete before the memory is freed
-        tc_commit(mma_done);
+        if constexpr (C::kPair) tc_commit_pair(mma_done); else tc_commit(mma_done);
         mbar_wait_landed(mma_done, 0, status);
       }
       __syncwarp();
@@ -496,12 +524,13 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
         bool alive = true;
         while (alive && pc.next()) {
           const int t = TR ? pc.row : pc.col;
-          const uint32_t bytes = (uint32_t)((toks(t) + 3) & ~3) * 4u;
+          const int ntok = toks(t);  // (a pair's second CTA may have none)
+          const uint32_t bytes = ntok > 0 ? (uint32_t)((ntok + 3) & ~3) * 4u : 0u;
           for (int kb = pc.k0; kb < pc.k1; ++kb, ++n) {
             const uint32_t xi = n % C::kXST;
             if (!mbar_wait_landed(sempty + xi, ((n / C::kXST) & 1u) ^ 1u, status)) { alive = false; break; }
             mbar_expect_tx(sfull + xi, bytes);
-            bulk_load(xring + xi * C::kToks, p.xs + (size_t)kb * p.mp + t * p.chunk, bytes, sfull + xi);
+            if (bytes) bulk_load(xring + xi * C::kToks, p.xs + (size_t)kb * p.mp + t * p.chunk, bytes, sfull + xi);
           }
         }
         for (uint32_t j = (n > (uint32_t)C::kXST ? n - C::kXST : 0); j < n; ++j)
@@ -581,7 +610,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(tempty + ti);
+          if constexpr (C::kPair) mbar_arrive_at(mapa(su32(tempty + ti), 0)); else mbar_arrive(tempty + ti);
           mbar_arrive(sempty + xi);
         }
         if (++ti == C::kTST) { ti = 0; tp ^= 1u; }
@@ -602,9 +631,10 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
         if (lane == 0) mbar_arrive(pdone);
         if (!mbar_wait_landed(pdone, np & 1u, status)) break;
         if (tid == kEW0 * 32) {
-          const int got = atom_add_acq_rel(p.tickets + c_first, 1);
+          int* ticket = p.tickets + (C::kPair ? 2 * c_first + rank : c_first);
+          const int got = atom_add_acq_rel(ticket, 1);
           const bool last = got == c_last - c_first;
-          if (last) p.tickets[c_first] = 0;  // ready for the next call
+          if (last) *ticket = 0;  // ready for the next call
           s_misc[1] = last;
           mbar_arrive(pdec);
         }
@@ -623,7 +653,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
             for (int i = 0; i < kC; ++i) {
               const int c = min(c0 + i, c_last);
               const float4* ps = reinterpret_cast<const float4*>(
-                  p.partials + ((size_t)c * 2 + (c == c_first ? 1 : 0)) * NT * kRows);
+                  p.partials + ((size_t)(C::kPair ? 2 * c + rank : c) * 2 + (c == c_first ? 1 : 0)) * NT * kRows);
 #pragma unroll
               for (int j = 0; j < kJ; j += 4)
                 v[i][j / 4] = j0 + j < ncol ? __ldcg(ps + (size_t)(col0 + j0 + j) / 4 * kRows + r)
@@ -668,10 +698,14 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
     }
     tc_fence_before();
   }
-  __syncthreads();
+  __syncwarp();
+  if constexpr (C::kPair) cluster_sync(); else __syncthreads();
   if (warp == kMW) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTCols) : "memory");
+    if constexpr (C::kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTCols) : "memory");
   }
 }
 
@@ -682,34 +716,39 @@ cudaError_t launch_nt(const LinPlan& p, const LinArgs& a, const LinMaps& maps, c
   static const cudaError_t rc =
       cudaFuncSetAttribute(linear_kernel<NT, TR, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (rc != cudaSuccess) return rc;
-  PdlLaunch L(dim3(p.G), dim3(C::kThreads), C::kSmem, s);
+  PdlLaunch L(dim3(C::kPair ? 2 * p.G : p.G), dim3(C::kThreads), C::kSmem, s);
+  cudaLaunchAttribute attr[2] = {L.attr[0], {}};
+  if (C::kPair) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    L.cfg.attrs = attr;
+    L.cfg.numAttrs = 2;
+  }
   return cudaLaunchKernelEx(&L.cfg, linear_kernel<NT, TR, XQ>, a, maps);
 }
 
 }  // namespace
 
 // Up to 128 tokens: the tokens are the columns, at the smallest width that holds
-// them.  Above: token tiles of 128 rows, weight tiles of 256 columns.
+// them.  Above: token tiles of 256 rows (128 a CTA), weight tiles of 256 columns.
 void plan_linear(LinPlan& p, int M, int N, int K, int sms) {
   p.M = M; p.N = N; p.K = K;
   p.nkb = (K + kBlock - 1) / kBlock;
   p.tok_rows = M > 128;
   p.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
   p.chunk = std::min(p.nt, kRows);
-  p.n_tt = (M + p.chunk - 1) / p.chunk;
+  p.n_tt = p.tok_rows ? (M + 2 * kRows - 1) / (2 * kRows) : (M + p.chunk - 1) / p.chunk;
   p.n_wt = p.tok_rows ? (N + 255) / 256 : (N + kRows - 1) / kRows;
   const long long pairs = (long long)p.n_tt * p.n_wt;
   const long long cells = pairs * p.nkb;
-  p.G = (int)std::min<long long>({cells, (long long)sms, (long long)kLinMaxCtas});
+  const int ctas = std::min(sms, kLinMaxCtas);
+  p.G = (int)std::min<long long>(cells, p.tok_rows ? std::max(1, ctas / 2) : ctas);
   p.waves = (int)(pairs / p.G);
   const long long rest = pairs - (long long)p.waves * p.G;
   p.split_cells = (int)(rest * p.nkb);
   // at least kLinMinRun cells a CTA: shorter pieces cost more to add than they save
   p.G_split = (int)std::max<long long>(1, std::min<long long>(p.G, std::max(rest * p.nkb / kLinMinRun, rest)));
-}
-
-size_t linear_partial_bytes(const LinPlan& p) {
-  return p.split_cells > 0 && p.G_split > 1 ? (size_t)p.G_split * 2 * p.nt * kRows * sizeof(float) : 0;
 }
 
 cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s) {
@@ -722,7 +761,7 @@ cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s) {
 cudaError_t launch_linear(const LinPlan& p, LinArgs a, const uint8_t* xq, const uint8_t* w, cudaStream_t s) {
   LinMaps maps;
   const bool fused = a.x != nullptr;
-  if (!tmap_2d(&maps.w, w, p.K, p.N, 128, p.tok_rows ? 256 : kRows)) return cudaErrorInvalidValue;
+  if (!tmap_2d(&maps.w, w, p.K, p.N, 128, kRows)) return cudaErrorInvalidValue;
   if (fused)
     maps.x = maps.w;  // (not used)
   else if (!tmap_2d(&maps.x, xq, p.K, p.M, 128, p.tok_rows ? kRows : std::min(p.nt, 32)))

@@ -210,9 +210,9 @@ struct LinPlan {
   int M, N, K, nkb;
   bool tok_rows;      // the tokens are the MMA's rows (else its columns)
   int nt;             // the kernel's columns: 16, 32, 64, 128 (tokens) or 256 (weight rows)
-  int chunk;          // tokens of a token tile
-  int n_tt, n_wt;     // token tiles, weight tiles
-  int G;              // CTAs
+  int chunk;          // tokens of a CTA's token tile
+  int n_tt, n_wt;     // token tiles (tok_rows: of both CTAs of a pair), weight tiles
+  int G;              // CTAs (tok_rows: pairs of CTAs)
   int waves;          // whole (row tile, column tile) pairs of each CTA
   int G_split;        // CTAs that share the cells of the remaining pairs
   int split_cells;
@@ -228,8 +228,8 @@ struct LinArgs {
   void* out = nullptr;
   int out_fp32 = 0;
   int* status = nullptr;
-  int* tickets = nullptr;      // [G], zero between calls
-  float* partials = nullptr;   // [G_split][2][nt][128]
+  int* tickets = nullptr;      // one a CTA, zero between calls
+  float* partials = nullptr;   // [CTA][2][nt][128]
   bool after_quant = false;    // the kernel just enqueued is the launch_quant_rows that writes the
                                // codes and scales, and no other input
   // the plan's
@@ -239,7 +239,6 @@ struct LinArgs {
   bool tok_rows;
 };
 void plan_linear(LinPlan& p, int M, int N, int K, int sms);
-size_t linear_partial_bytes(const LinPlan& p);
 cudaError_t launch_linear(const LinPlan& p, LinArgs a, const uint8_t* xq, const uint8_t* w, cudaStream_t s);
 
 // The FP8 paged cache: writing new tokens (kv_append.cu) and attention over it

@@ -1,6 +1,7 @@
-// Wrappers of the 5th-generation tensor-core instructions (tcgen05, one CTA)
-// shared by the FP8 kernels: operand descriptors of TMA's 128-byte swizzled
-// K-major tiles, the E4M3 MMA, its completion, and accumulator reads.
+// Wrappers of the 5th-generation tensor-core instructions (tcgen05) shared by the
+// FP8 kernels: operand descriptors of TMA's 128-byte swizzled K-major tiles, the
+// E4M3 MMA of one CTA and of a pair of CTAs, its completion, accumulator reads,
+// and what a pair needs of its cluster.
 #pragma once
 
 #include <stdint.h>
@@ -78,5 +79,54 @@ MOE_DEV void tc_ld32(uint32_t taddr, float* v) {
   for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 MOE_DEV void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------- a pair of CTAs
+// Shared-memory address of the same place in CTA `rank` of the cluster.
+MOE_DEV uint32_t mapa(uint32_t saddr, int rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
+  return a;
+}
+// Arrivals on a barrier of either CTA.  What they hand over is a tensor-memory
+// buffer that has been read (ordered by the tcgen05 fences) or a count of bytes,
+// no shared or global memory, so they do not carry a release at cluster scope:
+// it would wait for every access the thread has in flight (1000 to 2000 clocks a
+// cell; a prompt chunk of 4096 tokens 443 us).
+MOE_DEV void mbar_arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+MOE_DEV void mbar_expect_tx_at(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
+// Every thread of both CTAs meets; what each wrote to shared memory is visible.
+MOE_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A copy into this CTA whose bytes count on a barrier of either CTA of the pair.
+MOE_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(su32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(bar_cluster)
+      : "memory");
+}
+// One MMA over both CTAs' shared memory: 256 rows, 128 in each CTA's operand A and
+// tensor memory; each holds half of operand B's rows.
+MOE_DEV void tc_mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, int accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// one arrival on the barrier at this place in both CTAs
+MOE_DEV void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          su32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
 
 }  // namespace moe
