@@ -158,6 +158,7 @@ struct Cfg {
   // token 23.1 us, first cell 4.7 us after the start).  XQ: all (holding the
   // others back until the first rows of x are here: 18.4 -> 19.1 us)
   static constexpr int kAhead = XQ ? kNST : std::min(kNST, 4);
+  static constexpr int kPrefetch = 12;                        // weight tiles brought into L2 before the kernel before is complete
   static constexpr int kTST = NT <= 128 ? 4 : 2;              // accumulator buffers in tensor memory
   static constexpr int kTCols = NT * kTST;                    // 64 .. 512, a power of two
   static constexpr int kHalf = NT / 2;                        // columns of an epilogue warp
@@ -295,11 +296,11 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
   }
-  // launched while the kernel before may still run.  Where that is this call's
-  // quantisation, the weights need not wait for it; else nothing is read or
-  // written before it is complete.
+  // launched while the kernel before may still run: each role waits for it before
+  // it reads or writes.  Only where that kernel is this call's quantisation do the
+  // weights' copies not wait for it; else their first tiles are brought into L2
+  // meanwhile.
   grid_dep_launch();
-  if (!p.after_quant) grid_dep_wait();
   tc_fence_before();
   if constexpr (C::kPair) cluster_sync(); else __syncthreads();
   tc_fence_after();
@@ -331,13 +332,21 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
             tma_load_2d(st, &maps.w, kb * kBlock, q.row * kRows, full + si);
           }
         };
+        if (!p.after_quant) {
+          Pieces q(p);
+          int n = 0;
+          while (n < C::kPrefetch && q.next())
+            for (int kb = q.k0; kb < q.k1 && n < C::kPrefetch; ++kb, ++n)
+              tma_prefetch_2d(&maps.w, kb * kBlock, TR ? q.col * NT + rank * C::kCRows : q.row * kRows);
+          grid_dep_wait();
+        }
         {
           Pieces q(p);
           while (ahead < (uint32_t)C::kAhead && q.next())
             for (int kb = q.k0; kb < q.k1 && ahead < (uint32_t)C::kAhead; ++kb) load_w(q, kb, (int)ahead++);
         }
         if (!XQ) {
-          grid_dep_wait();
+          if (p.after_quant) grid_dep_wait();
           asm volatile("fence.proxy.async.global;" ::: "memory");  // codes of the kernel before are read with TMA
         }
         int si = 0;
@@ -412,6 +421,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
       // each thread reads back only what it copied itself.  (Every CTA quantises
       // the groups it needs for itself: at 16 tokens 4 KB of x beside a cell's
       // 16 KB of weights, and no kernel before this one.)
+      grid_dep_wait();
       constexpr int kIt = NT / 8;  // passes of eight tokens
       const int me = warp < kEW0 ? warp - kSW : warp - kEW1 + 2, tok = lane >> 2, quarter = lane & 3;
       const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + quarter * 32;
@@ -541,6 +551,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
   } else {
     // ================================================================ epilogue
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    grid_dep_wait();
     const int qd = warp & 3, hf = (warp - kEW0) >> 2;
     const int r = 32 * qd + lane;                 // row of the row tile
     const int col0 = hf * C::kHalf;
