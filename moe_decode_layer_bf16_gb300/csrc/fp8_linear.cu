@@ -158,7 +158,7 @@ struct Cfg {
   // token 23.1 us, first cell 4.7 us after the start).  XQ: all (holding the
   // others back until the first rows of x are here: 18.4 -> 19.1 us)
   static constexpr int kAhead = XQ ? kNST : std::min(kNST, 4);
-  static constexpr int kPrefetch = 12;                        // weight tiles brought into L2 before the kernel before is complete
+  static constexpr int kPrefetch = 20;                        // weight tiles brought into L2 before the kernel before is complete
   static constexpr int kTST = NT <= 128 ? 4 : 2;              // accumulator buffers in tensor memory
   static constexpr int kTCols = NT * kTST;                    // 64 .. 512, a power of two
   static constexpr int kHalf = NT / 2;                        // columns of an epilogue warp
