@@ -143,13 +143,24 @@ MOE_DEV uint32_t chunk_at(uint32_t base, int t, int c) {
 struct Seq {
   int start, n, len, tile0, tiles, groups;  // groups: row groups
 };
+struct Raw {  // as read (through L2: a hint's reads must leave nothing behind in L1)
+  int start, stop, len;
+  MOE_DEV Raw(const AttArgs& a, int b) {
+    start = __ldcg(a.q_start + b);
+    stop = __ldcg(a.q_start + b + 1);
+    len = __ldcg(a.lens + b);
+  }
+  MOE_DEV bool operator==(const Raw& o) const { return start == o.start && stop == o.stop && len == o.len; }
+};
 template <int D, int RT>
-MOE_DEV Seq load_seq(const AttArgs& a, int b, bool report) {
+MOE_DEV Seq make_seq(const AttArgs& a, const Raw& r, bool report) {
   constexpr int kTile = AttCfg<D, RT>::kTile;
   Seq s;
-  s.start = __ldg(a.q_start + b);
-  s.n = __ldg(a.q_start + b + 1) - s.start;
-  s.len = __ldg(a.lens + b);
+  s.start = r.start;
+  // (a difference that does not fit counts as negative)
+  const long long n = (long long)r.stop - r.start;
+  s.n = n > a.total ? -1 : (int)max(n, -1ll);
+  s.len = r.len;
   const long long cap = (long long)a.width * a.page_size;
   bool bad = false;
   if (s.start < 0 || s.n < 0 || s.start > a.total || s.n > a.total - s.start) { s.n = 0; s.start = 0; bad = true; }
@@ -176,10 +187,10 @@ template <int D, int RT>
 MOE_DEV void walk_start(Walk& w, const AttArgs& a, int b, int b_first, int x, int count) {
   w.left = count;
   w.b = b;
-  w.s = load_seq<D, RT>(a, b, false);
+  w.s = make_seq<D, RT>(a, Raw(a, b), false);
   const int units = w.s.tiles + kItemCost;
   const int it = (x - b_first) / units;
-  w.head = it / w.s.groups;
+  w.head = it / max(1, w.s.groups);  // (none: only a hint's lengths that changed)
   w.grp = it - w.head * w.s.groups;
   w.item0 = b_first + it * units;
   w.u0 = x - w.item0;
@@ -196,7 +207,7 @@ MOE_DEV bool walk_next(Walk& w, const AttArgs& a) {  // to the next piece
       w.head = 0;
       do {  // (a sequence without rows has no units; one with rows follows, since units are left)
         if (++w.b >= a.B) return false;
-        w.s = load_seq<D, RT>(a, w.b, false);
+        w.s = make_seq<D, RT>(a, Raw(a, w.b), false);
       } while (w.s.groups == 0);
     }
   }
@@ -285,84 +296,116 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     recs[2 * warp].item0 = recs[2 * warp + 1].item0 = -1;
   }
 
-  // launched while the kernel before may still run: nothing of its is read, and
-  // nothing written, before it is complete
   grid_dep_launch();
-  grid_dep_wait();
   // ---- the shares: every thread adds up a run of sequences, then a scan
   __shared__ long long s_scan[kWarps];
   int* s_before = reinterpret_cast<int*>(smem + C::kPartAt);  // [thread]: first unit of its sequences (the pieces come later)
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Seq s = load_seq<D, RT>(a, b, blockIdx.x == 0);
-    mine += (long long)(s.tiles + kItemCost) * s.groups * a.kv_heads;
-  }
-  long long incl = mine;
+  const int P = a.page_size;
+  const int box = min(P, kTile);          // token rows of one copy
+  const int nbox = kTile / box, gpb = box >> 4;
+  long long total = 0;
+  int G = 0, Xq = 0, Xr = 0, X0 = 0, X1 = 0, wb = 0, wat = 0, wx = 0, wn = 0;
+  // Launched while the kernel before may still run.  What it may write is read
+  // early all the same, but as a hint: the shares are worked out and the first tiles
+  // brought into L2 from it.  After the kernel before is complete the lengths are
+  // read again, and where they are others the shares are worked out again.
+  // Nothing is written and no copy into shared memory made before.
+  bool hint = per == 1;
+  if (!hint) grid_dep_wait();
+  for (;;) {
+    long long mine = 0;
+    Raw seen(a, b0 < a.B ? b0 : 0);
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = make_seq<D, RT>(a, per == 1 ? seen : Raw(a, b), blockIdx.x == 0 && !hint);
+      mine += (long long)(s.tiles + kItemCost) * s.groups * a.kv_heads;
+    }
+    long long incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  long long before = incl - mine, total = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine;
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+    }
+    const bool fits = total <= INT_MAX;
+    s_before[tid] = mine > 0 && fits ? (int)before : -1;
+    __syncthreads();
+    // CTAs that get work
+    G = fits ? (int)min((long long)gridDim.x, (total + kWarps * kMinUnits - 1) / (kWarps * kMinUnits)) : 0;
+    wn = 0;
+    if ((int)blockIdx.x < G) {
+      Xq = (int)total / G;
+      Xr = (int)total - Xq * G;
+      X0 = cta_share(Xq, Xr, G, blockIdx.x);
+      X1 = cta_share(Xq, Xr, G, blockIdx.x + 1);
+      auto share = [&](int w) {  // X0 + (X1 - X0) * w / kWarps
+        const int n = X1 - X0;
+        return X0 + n / kWarps * w + n % kWarps * w / kWarps;
+      };
+      wx = share(warp);
+      wn = share(warp + 1) - wx;
+      // the sequence this warp's share starts in: the last thread whose run of
+      // sequences starts at or before it (and is not empty), then along that run
+      int best = -1;  // lane l looks at a run of threads
+#pragma unroll
+      for (int k = 0; k < kThreads / 32; ++k) {
+        const int at = s_before[lane * (kThreads / 32) + k];
+        if (at >= 0 && at <= wx) best = k;
+      }
+      const uint32_t have = __ballot_sync(0xffffffffu, best >= 0);
+      const int src = 31 - __clz(have);  // (unit 0 is somebody's, so there is one)
+      const int t = __shfl_sync(0xffffffffu, lane * (kThreads / 32) + best, src);
+      wat = s_before[t];
+      for (wb = min(a.B, t * per); per > 1; ++wb) {
+        const Seq s = make_seq<D, RT>(a, Raw(a, wb), false);
+        const int nb = (s.tiles + kItemCost) * s.groups * a.kv_heads;
+        if (wx < wat + nb || wb + 1 >= a.B) break;
+        wat += nb;
+      }
+    }
+    if (!hint) break;
+    if (wn > 0) {
+      Walk h;
+      walk_start<D, RT>(h, a, wb, wat, wx, wn);
+      const int t0 = h.s.tile0 + max(0, h.u0 - kItemCost), t1 = min(h.s.tile0 + max(0, h.u1 - kItemCost), t0 + kNST);
+      const int pos = t0 * kTile + 16 * lane;  // a lane for each 16-token group
+      if (t0 >= 0 && t0 + lane / kGroups < t1 && lane % gpb == 0 && pos < h.s.len && h.head < a.kv_heads) {
+        const int page = __ldcg(a.page_table + (size_t)h.b * a.width + pos / P);
+        if (page >= 0 && page < a.num_pages) {
+          tma_prefetch_3d(&maps.k, 0, pos % P, page * a.kv_heads + h.head);
+          tma_prefetch_3d(&maps.v, 0, pos % P, page * a.kv_heads + h.head);
+        }
+      }
+    }
+    grid_dep_wait();
+    hint = false;
+    if (__syncthreads_and(b0 >= a.B || Raw(a, b0) == seen)) {
+      // (what the hint did not report)
+      if (b0 < b1 && blockIdx.x == 0) make_seq<D, RT>(a, seen, true);
+      break;
+    }
   }
-  s_before[tid] = mine > 0 && total <= INT_MAX ? (int)before : -1;
-  __syncthreads();
-  if (total > INT_MAX) {  // rows counted more than once: q_start does not ascend
-    if (tid == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
-    return;
-  }
-  // CTAs that get work
-  const int G = (int)min((long long)gridDim.x, (total + kWarps * kMinUnits - 1) / (kWarps * kMinUnits));
+  if (total > INT_MAX && tid == 0) atomicExch(status, MOE_ERR_INVALID_ARG);  // rows counted more than once
   if ((int)blockIdx.x >= G) return;  // (the whole CTA; nothing is in flight)
-  const int Xq = (int)total / G, Xr = (int)total - Xq * G;
-  const int X0 = cta_share(Xq, Xr, G, blockIdx.x), X1 = cta_share(Xq, Xr, G, blockIdx.x + 1);
-  auto share = [&](int w) {  // X0 + (X1 - X0) * w / kWarps
-    const int n = X1 - X0;
-    return X0 + n / kWarps * w + n % kWarps * w / kWarps;
-  };
-  // the sequence this warp's share starts in: the last thread whose run of
-  // sequences starts at or before it (and is not empty), then along that run
-  int wb = 0, wat = 0;
-  const int wx = share(warp);
-  {
-    int best = -1;  // lane l looks at a run of threads
-#pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
-      const int at = s_before[lane * (kThreads / 32) + k];
-      if (at >= 0 && at <= wx) best = k;
-    }
-    const uint32_t have = __ballot_sync(0xffffffffu, best >= 0);
-    const int src = 31 - __clz(have);  // (unit 0 is somebody's, so there is one)
-    const int t = __shfl_sync(0xffffffffu, lane * (kThreads / 32) + best, src);
-    wat = s_before[t];
-    for (wb = min(a.B, t * per); per > 1; ++wb) {
-      const Seq s = load_seq<D, RT>(a, wb, false);
-      const int nb = (s.tiles + kItemCost) * s.groups * a.kv_heads;
-      if (wx < wat + nb || wb + 1 >= a.B) break;
-      wat += nb;
-    }
-  }
   __syncthreads();  // s_before has been read
 
   const int g = lane >> 2, q = lane & 3;
   const int fg = D == 128 ? ((g & 1) << 2 | g >> 1) : g;   // this thread's chunk of a V row (16 or 8 values)
   constexpr int kMT = D / 16;                              // 16-row tiles of V^T
-  const int P = a.page_size;
-  const int box = min(P, kTile);          // token rows of one copy
-  const int nbox = kTile / box, gpb = box >> 4;
   uint32_t issued = 0, used = 0;          // tiles copied and consumed so far (ring position and phase)
   bool alive = true;
   Walk w;
-  bool more = share(warp) < share(warp + 1);
-  if (more) walk_start<D, RT>(w, a, wb, wat, wx, share(warp + 1) - wx);
+  bool more = wn > 0;
+  if (more) walk_start<D, RT>(w, a, wb, wat, wx, wn);
   while (more) {
     const int rows = min(kRowsC, w.s.n * a.G - w.grp * kRowsC);
     const int pos0 = w.s.len - w.s.n;  // position of the step's first token
