@@ -47,7 +47,7 @@ size_t linear_partial_bound(int M, int N, int K) {
   plan_linear(p, std::max(M, 1), N, K, kLinMaxCtas);
   const long long cells = (long long)p.n_tt * p.n_wt * p.nkb;
   const long long ctas = std::min<long long>(kLinMaxCtas, p.tok_rows ? 2 * cells : cells);
-  return (size_t)ctas * 2 * p.nt * kBlock * sizeof(float);
+  return (size_t)ctas * p.nt * kBlock * sizeof(float);
 }
 
 size_t codes_bytes(int M, int K) { return up256((size_t)M * K); }

@@ -27,8 +27,8 @@
 //
 // Work split.  One CTA per SM (a pair of CTAs counts as one here).  Whole waves of
 // pairs of tiles are dealt out as they are; the remaining ones are cut along K
-// into one equal share of cells per CTA
-// (stream-K), so that one token's 72 row tiles keep all 152 SMs streaming.  A
+// into pieces of equal length where that is worth the exchange of their sums, one
+// a CTA, so that one token's 72 row tiles keep 144 SMs streaming.  A
 // CTA that holds a piece of a pair writes its fp32 sums to the workspace; the
 // last to arrive adds the pieces in k order (the result does not depend on who
 // is last).
@@ -175,8 +175,8 @@ struct Cfg {
   static constexpr size_t kTurnAt = (kRawAt + kRawBytes + 15) / 16 * 16;
   static constexpr size_t kSmem = 1024 + kTurnAt + (TR ? (size_t)kNEpi * 32 * kTurnRow : 0);
   // registers: 12 warps start with 168 a thread; with 128 accumulators the
-  // epilogue takes 216 of them and the other four warps keep 72
-  // (256 x 216 + 128 x 72 = 384 x 168)
+  // epilogue takes 232 of them (it spills with 216) and the other four warps keep 40
+  // (256 x 232 + 128 x 40 = 384 x 168)
   static constexpr bool kSplitRegs = TR;
 };
 
@@ -184,51 +184,36 @@ struct LinMaps {
   CUtensorMap w, x;
 };
 
-// The pieces of work of CTA c: whole pairs c, c + G, ..., then its share of the
-// cells of the remaining pairs, one pair after the other, from the host's
-// starts[c] up to starts[c + 1] (no division is left for the kernel's first steps).
+// The pieces of work of CTA c: whole pairs c, c + G, ..., then at most one piece of
+// a remaining pair, from a table (no division is left for the kernel's first steps).
 struct Pieces {
   const LinArgs& p;
   int i;             // next whole pair of this CTA
-  int w, t, k;       // next cell of the split pairs: weight tile, token tile, k-block
-  int we, te, ke;    // where the CTA's share of them ends
   int k0, k1;        // the current piece: k-blocks
   int cw, ct;        // its weight tile and token tile (of both CTAs)
   int row, col;      // this CTA's row tile, and the column tile
-  MOE_DEV explicit Pieces(const LinArgs& a) : p(a), i(0) {
-    const int c = min(cta(), p.G_split), e = min(cta() + 1, p.G_split);
-    w = p.starts[c].w; t = p.starts[c].t; k = p.starts[c].k;
-    we = p.starts[e].w; te = p.starts[e].t; ke = p.starts[e].k;
-  }
+  MOE_DEV explicit Pieces(const LinArgs& a) : p(a), i(0) {}
   MOE_DEV int cta() const { return p.tok_rows ? blockIdx.x >> 1 : blockIdx.x; }
   MOE_DEV bool next() {
     if (i < p.waves) {
       // weight tiles follow one another within a token tile
-      const int pair = i++ * p.G + cta();
+      const int pair = i * p.G + cta();
       ct = pair / p.n_wt;
       cw = pair - ct * p.n_wt;
       k0 = 0;
       k1 = p.nkb;
     } else {
-      const bool last = w == we && t == te;
-      if (last && k >= ke) return false;
-      cw = w;
-      ct = t;
-      k0 = k;
-      k1 = last ? ke : p.nkb;
-      k = last ? ke : 0;
-      if (!last && ++w == p.n_wt) { w = 0; ++t; }
+      const LinArgs::Piece& q = p.piece[cta()];
+      if (i > p.waves || q.k0 == q.k1) return false;
+      cw = q.w;
+      ct = q.t;
+      k0 = q.k0;
+      k1 = q.k1;
     }
+    ++i;
     row = p.tok_rows ? 2 * ct + (blockIdx.x & 1) : cw;
     col = p.tok_rows ? cw : ct;
     return true;
-  }
-  // CTA that holds k-block kb of the current (split) pair
-  MOE_DEV int owner(int kb) const {
-    const int x = (ct * p.n_wt + cw - p.waves * p.G) * p.nkb + kb;  // of all split cells
-    int o = min(x / p.share_q, p.G_split - 1);
-    while (p.share_q * o + p.share_r * o / p.G_split > x) --o;
-    return o;
   }
 };
 
@@ -364,7 +349,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
   auto cols = [&](int c) { return TR ? min(NT, p.N - c * NT) : toks(c); };
 
   if (warp < kEW0 || (XQ && warp >= kEW1)) {
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kPW) {
       // ================================================================ producer
       // Weights do not depend on the kernel before this one (the quantisation):
@@ -602,7 +587,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
     }
   } else {
     // ================================================================ epilogue
-    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     grid_dep_wait();
     const int qd = warp & 3, hf = (warp - kEW0) >> 2;
     const int r = 32 * qd + lane;                 // row of the row tile
@@ -610,8 +595,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
     constexpr int kStep = TR ? 32 : C::kHalf < 16 ? C::kHalf : 16;   // columns of one read of the accumulator
     float acc[C::kHalf];
     int ti = 0;
-    uint32_t tp = 0, np = 0;  // np: split pieces so far (phases of pdone and pdec)
-    uint32_t nc = 0;          // cells so far
+    uint32_t tp = 0, nc = 0;  // nc: cells so far
     bool alive = true;
     while (alive && pc.next()) {
       const int ncol = cols(pc.col) - col0;       // live columns of this warp (may be none)
@@ -621,11 +605,6 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
       const float* wr = p.w_s + (size_t)wblk * p.nkb;
       float ws = pc.k0 + lane < pc.k1 ? __ldg(wr + pc.k0 + lane) : 0.f, wn = 0.f;
       const bool whole = pc.k0 == 0 && pc.k1 == p.nkb;
-      int c_first = 0, c_last = 0;
-      if (!whole) {
-        c_first = pc.owner(0);
-        c_last = pc.owner(p.nkb - 1);
-      }
 #pragma unroll
       for (int j = 0; j < C::kHalf; ++j) acc[j] = 0.f;
       for (int kb = pc.k0; kb < pc.k1; ++kb, ++nc) {
@@ -681,10 +660,10 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
       if (!alive) break;
       if (!whole) {
         // this piece's sums go to the workspace; the last CTA of the pair to
-        // arrive adds all pieces in k order.  A CTA's pieces: slot 0 continues
-        // a pair of the CTA before it, slot 1 starts one.  The counter's
-        // release and acquire reach the other warps through the barriers.
-        float* part = p.partials + ((size_t)blockIdx.x * 2 + (pc.k0 == 0 ? 1 : 0)) * NT * kRows;
+        // arrive adds all pieces in k order.  The counter's release and acquire
+        // reach the other warps through the barriers.
+        const int c_first = p.piece[pc.cta()].first, c_last = c_first + p.pieces - 1;
+        float* part = p.partials + (size_t)blockIdx.x * NT * kRows;
 #pragma unroll
         for (int j = 0; j < C::kHalf; j += 4)
           if (j < ncol)
@@ -692,7 +671,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
                    make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(pdone);
-        if (!mbar_wait_landed(pdone, np & 1u, status)) break;
+        if (!mbar_wait_landed(pdone, 0, status)) break;
         if (tid == kEW0 * 32) {
           int* ticket = p.tickets + (C::kPair ? 2 * c_first + rank : c_first);
           const int got = atom_add_acq_rel(ticket, 1);
@@ -701,8 +680,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
           s_misc[1] = last;
           mbar_arrive(pdec);
         }
-        if (!mbar_wait_landed(pdec, np & 1u, status)) break;
-        ++np;
+        if (!mbar_wait_landed(pdec, 0, status)) break;
         if (!s_misc[1]) continue;
 #pragma unroll
         for (int j = 0; j < C::kHalf; ++j) acc[j] = 0.f;
@@ -716,7 +694,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
             for (int i = 0; i < kC; ++i) {
               const int c = min(c0 + i, c_last);
               const float4* ps = reinterpret_cast<const float4*>(
-                  p.partials + ((size_t)(C::kPair ? 2 * c + rank : c) * 2 + (c == c_first ? 1 : 0)) * NT * kRows);
+                  p.partials + (size_t)(C::kPair ? 2 * c + rank : c) * NT * kRows);
 #pragma unroll
               for (int j = 0; j < kJ; j += 4)
                 v[i][j / 4] = j0 + j < ncol ? __ldcg(ps + (size_t)(col0 + j0 + j) / 4 * kRows + r)
@@ -803,14 +781,29 @@ void plan_linear(LinPlan& p, int M, int N, int K, int sms) {
   p.n_tt = p.tok_rows ? (M + 2 * kRows - 1) / (2 * kRows) : (M + p.chunk - 1) / p.chunk;
   p.n_wt = p.tok_rows ? (N + 255) / 256 : (N + kRows - 1) / kRows;
   const long long pairs = (long long)p.n_tt * p.n_wt;
-  const long long cells = pairs * p.nkb;
   const int ctas = std::min(sms, kLinMaxCtas);
-  p.G = (int)std::min<long long>(cells, p.tok_rows ? std::max(1, ctas / 2) : ctas);
+  p.G = p.tok_rows ? std::max(1, ctas / 2) : ctas;
   p.waves = (int)(pairs / p.G);
-  const long long rest = pairs - (long long)p.waves * p.G;
-  p.split_cells = (int)(rest * p.nkb);
-  // at least kLinMinRun cells a CTA: shorter pieces cost more to add than they save
-  p.G_split = (int)std::max<long long>(1, std::min<long long>(p.G, std::max(rest * p.nkb / kLinMinRun, rest)));
+  p.rest = (int)(pairs - (long long)p.waves * p.G);
+  // Pieces of each remaining pair: as many as make the last CTA end earliest.  In
+  // units of the time a cell takes (0.25 us), / 128: the longest piece's cells,
+  // and for the exchange of sums a fixed part, one that grows with a CTA's
+  // sums, and (weights as rows) one with the CTAs that exchange at a time.
+  // Measured over 1 .. 64 pieces (M x K -> N): us whole / with the best number / as
+  // chosen: 1 x 4720 -> 354 11.6 / 5.5 / 5.5, 22 x 1408 -> 2763 7.1 / 7.1 / 7.0,
+  // 96 x 6880 -> 844 29.3 / 13.6 / 14.1, 145 x 4032 -> 186 18.9 / 15.0 / 16.3,
+  // 1908 x 6320 -> 117 35.8 / 27.6 / 28.3, 482 x 2144 -> 651 14.7 / 14.7 / 15.3.
+  // Equal shares of all remaining cells for every CTA, whose pieces cross from one
+  // pair into the next, were slower throughout (two pieces to exchange a CTA:
+  // 1 x 7168 -> 9216 16.0 us for 14.5, 256 x 7168 -> 9216 32.6 for 27.6).
+  p.pieces = 1;
+  long long best = 128LL * p.nkb;
+  for (int s = 2; p.rest > 0 && s <= p.nkb && (long long)s * p.rest <= p.G; ++s) {
+    const long long exchange = p.tok_rows ? 640 + s * (576LL * std::min(N, 256) / 256) : 512 + s * (8LL * p.rest + p.nt);
+    const long long cost = 128LL * ((p.nkb + s - 1) / s) + exchange;
+    if (cost < best) { best = cost; p.pieces = s; }
+  }
+  if (p.waves == 0) p.G = p.rest * p.pieces;
 }
 
 cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s) {
@@ -831,12 +824,14 @@ cudaError_t launch_linear(const LinPlan& p, LinArgs a, const uint8_t* xq, const 
   a.mp = linear_scale_stride(p.M);
   a.M = p.M; a.N = p.N; a.K = p.K; a.nkb = p.nkb; a.chunk = p.chunk; a.n_wt = p.n_wt;
   a.n_wblk = (p.N + kBlock - 1) / kBlock;
-  a.tok_rows = p.tok_rows; a.G = p.G; a.waves = p.waves; a.G_split = p.G_split;
-  for (int c = 0; c <= p.G_split; ++c) {  // CTA c's share: cells split_cells * c / G_split ...
-    const int x = (int)((long long)p.split_cells * c / p.G_split), pair = p.waves * p.G + x / p.nkb;
-    a.starts[c] = {pair % p.n_wt, pair / p.n_wt, x % p.nkb};
+  a.tok_rows = p.tok_rows; a.G = p.G; a.waves = p.waves; a.pieces = p.pieces;
+  for (int c = 0; c < p.G; ++c) {
+    const int r = c / p.pieces, i = c - r * p.pieces;
+    const long long pair = (long long)p.waves * p.G + r;
+    if (r >= p.rest) { a.piece[c] = {}; continue; }
+    a.piece[c] = {(uint16_t)(pair % p.n_wt), (uint16_t)(pair / p.n_wt), (uint16_t)(p.nkb * i / p.pieces),
+                  (uint16_t)(p.nkb * (i + 1) / p.pieces), (uint16_t)(r * p.pieces)};
   }
-  a.share_q = p.split_cells / p.G_split; a.share_r = p.split_cells % p.G_split;
   if (fused) return launch_nt<16, false, true>(p, a, maps, s);
   switch (p.nt) {
     case 16: return launch_nt<16, false, false>(p, a, maps, s);

@@ -205,7 +205,6 @@ inline int linear_scale_stride(int M) { return (M + 3) & ~3; }
 cudaError_t launch_quant_rows(const QuantArgs& a, int sms, cudaStream_t s);
 
 constexpr int kLinMaxCtas = 160;  // CTAs of the product at most (one per SM)
-constexpr int kLinMinRun = 8;     // k-blocks of a CTA's share of the split pairs at least
 struct LinPlan {
   int M, N, K, nkb;
   bool tok_rows;      // the tokens are the MMA's rows (else its columns)
@@ -214,8 +213,8 @@ struct LinPlan {
   int n_tt, n_wt;     // token tiles (tok_rows: of both CTAs of a pair), weight tiles
   int G;              // CTAs (tok_rows: pairs of CTAs)
   int waves;          // whole (row tile, column tile) pairs of each CTA
-  int G_split;        // CTAs that share the cells of the remaining pairs
-  int split_cells;
+  int rest;           // pairs after those,
+  int pieces;         // each cut along K into so many
 };
 constexpr int kLinFusedTokens = 16;  // up to so many tokens the product quantises x itself
 struct LinArgs {
@@ -229,13 +228,14 @@ struct LinArgs {
   int out_fp32 = 0;
   int* status = nullptr;
   int* tickets = nullptr;      // one a CTA, zero between calls
-  float* partials = nullptr;   // [CTA][2][nt][128]
+  float* partials = nullptr;   // [CTA][nt][128]
   bool after_quant = false;    // the kernel just enqueued is the launch_quant_rows that writes the
                                // codes and scales, and no other input
   // the plan's
-  int mp, M, N, K, nkb, chunk, n_wt, n_wblk, G, waves, G_split;
-  int share_q, share_r;  // split cells = share_q * G_split + share_r
-  struct Start { int w, t, k; } starts[kLinMaxCtas + 1];  // each CTA's first split cell: weight tile, token tile, k-block
+  int mp, M, N, K, nkb, chunk, n_wt, n_wblk, G, waves, pieces;
+  // each CTA's piece of the remaining pairs: weight tile, token tile, k-blocks
+  // (none: k0 == k1), and the CTA with the pair's first piece
+  struct Piece { uint16_t w, t, k0, k1, first; } piece[kLinMaxCtas];
   bool tok_rows;
 };
 void plan_linear(LinPlan& p, int M, int N, int K, int sms);
