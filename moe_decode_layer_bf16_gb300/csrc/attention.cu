@@ -283,6 +283,12 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   using C = AttCfg<D, RT>;
   constexpr int kRowsC = C::kRowsC, kTile = C::kTile, kGroups = C::kGroups, kNST = C::kNST;
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
+  // Items of up to so many units (and more than kWholeTiles tiles) stay within a CTA where
+  // a CTA's share is smaller than that: no joining through memory (80 drawn cases,
+  // geometric mean: 0 10.8 us, kWarps 10.9, 2 kWarps 10.5, 3 kWarps 10.7; 19 sequences
+  // of 374 to 496 tokens, windowed, 14.1 us for 10.8; the items of 4 x 3 rows of 52 to
+  // 1514 tokens, which then wait for their longest, 13.0 for 14.6).
+  constexpr int kCtaUnits = 2 * kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((C::kAlign - (su32(smem_raw) & (C::kAlign - 1))) & (C::kAlign - 1));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -306,6 +312,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   // ---- the shares: every thread adds up a run of sequences, then a scan
   __shared__ long long s_scan[kWarps];
   int* s_before = reinterpret_cast<int*>(smem + C::kPartAt);  // [thread]: first unit of its sequences (the pieces come later)
+  int* s_tiles = s_before + kThreads;  // tiles of its sequence, where it has one
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   const int P = a.page_size;
@@ -322,10 +329,12 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   if (!hint) grid_dep_wait();
   for (;;) {
     long long mine = 0;
+    int tiles = 0;
     Raw seen(a, b0 < a.B ? b0 : 0);
     for (int b = b0; b < b1; ++b) {
       const Seq s = make_seq<D, RT>(a, per == 1 ? seen : Raw(a, b), blockIdx.x == 0 && !hint);
       mine += (long long)(s.tiles + kItemCost) * s.groups * a.kv_heads;
+      tiles = s.tiles;
     }
     long long incl = mine;
 #pragma unroll
@@ -344,6 +353,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     }
     const bool fits = total <= INT_MAX;
     s_before[tid] = mine > 0 && fits ? (int)before : -1;
+    s_tiles[tid] = tiles;
     __syncthreads();
     // CTAs that get work
     G = fits ? (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps) : 0;
@@ -353,29 +363,44 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
       Xr = (int)total - Xq * G;
       X0 = cta_share(Xq, Xr, G, blockIdx.x);
       X1 = cta_share(Xq, Xr, G, blockIdx.x + 1);
-      auto share = [&](int w) {  // X0 + (X1 - X0) * w / kWarps
-        const int n = X1 - X0;
-        return X0 + n / kWarps * w + n % kWarps * w / kWarps;
-      };
-      wx = share(warp);
-      wn = share(warp + 1) - wx;
-      // the sequence this warp's share starts in: the last thread whose run of
-      // sequences starts at or before it (and is not empty), then along that run
-      int best = -1;  // lane l looks at a run of threads
+      // Where the shares are small, so are the items that stay within a CTA (the one
+      // that holds the first of their units takes all): the first two steps move
+      // the share's ends.  The last one is for the warp's share.  (One loop: the
+      // kernel's first steps wait for their instructions.)
+#pragma unroll 1
+      for (int step = Xq < kCtaUnits ? 0 : 2; step < 3; ++step) {
+        if (step == 2) {
+          const int n = X1 - X0;
+          auto share = [&](int w) { return X0 + n / kWarps * w + n % kWarps * w / kWarps; };  // X0 + n * w / kWarps
+          wx = share(warp);
+          wn = share(warp + 1) - wx;
+        }
+        const int x = step == 0 ? X0 : step == 1 ? X1 : wx;
+        if (x >= (int)total) continue;
+        // the sequence unit x lies in, and its first unit: the last thread whose run
+        // of sequences starts at or before x (and is not empty), then along that run
+        int best = -1;  // lane l looks at a run of threads
 #pragma unroll
-      for (int k = 0; k < kThreads / 32; ++k) {
-        const int at = s_before[lane * (kThreads / 32) + k];
-        if (at >= 0 && at <= wx) best = k;
-      }
-      const uint32_t have = __ballot_sync(0xffffffffu, best >= 0);
-      const int src = 31 - __clz(have);  // (unit 0 is somebody's, so there is one)
-      const int t = __shfl_sync(0xffffffffu, lane * (kThreads / 32) + best, src);
-      wat = s_before[t];
-      for (wb = min(a.B, t * per); per > 1; ++wb) {
-        const Seq s = make_seq<D, RT>(a, Raw(a, wb), false);
-        const int nb = (s.tiles + kItemCost) * s.groups * a.kv_heads;
-        if (wx < wat + nb || wb + 1 >= a.B) break;
-        wat += nb;
+        for (int k = 0; k < kThreads / 32; ++k) {
+          const int at = s_before[lane * (kThreads / 32) + k];
+          if (at >= 0 && at <= x) best = k;
+        }
+        const uint32_t have = __ballot_sync(0xffffffffu, best >= 0);
+        const int src = 31 - __clz(have);  // (unit 0 is somebody's, so there is one)
+        const int t = __shfl_sync(0xffffffffu, lane * (kThreads / 32) + best, src);
+        wat = s_before[t];
+        int units = s_tiles[t] + kItemCost;
+        for (wb = min(a.B, t * per); per > 1; ++wb) {
+          const Seq s = make_seq<D, RT>(a, Raw(a, wb), false);
+          units = s.tiles + kItemCost;
+          const int nb = units * s.groups * a.kv_heads;
+          if (x < wat + nb || wb + 1 >= a.B) break;
+          wat += nb;
+        }
+        if (step < 2 && units > kItemCost + kWholeTiles && units <= kCtaUnits) {
+          const int off = (x - wat) % units, to = off > 0 ? x - off + units : x;
+          if (step == 0) X0 = to; else X1 = to;
+        }
       }
     }
     if (!hint) break;
