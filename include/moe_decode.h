@@ -350,9 +350,9 @@ int fp8_block_gemm(const uint8_t *codes, const float *scales, const uint8_t *w, 
 /*
  * The linear layer out = x . w^T: fp8_quant_rows into the workspace, then
  * fp8_block_gemm, launched so that it streams its first weights while the
- * quantisation still runs; up to 16 tokens the product quantises x itself.
- * The results are those of the two calls.  Arguments and limits as theirs.  Two
- * kernels, up to 16 tokens one.
+ * quantisation still runs; for a few tokens (up to 8, or 16 of a small layer)
+ * one kernel, the product quantising x itself.  The results are those of the
+ * two calls.  Arguments and limits as theirs.
  */
 int fp8_linear_workspace_size(int M, int N, int K, size_t *bytes);
 int fp8_linear(const void *x, long long x_stride, const uint8_t *w, const float *w_s, int M, int N, int K, int e8m0,

@@ -53,13 +53,15 @@ size_t linear_partial_bound(int M, int N, int K) {
 size_t codes_bytes(int M, int K) { return up256((size_t)M * K); }
 size_t scales_bytes(int M, int K) { return up256((size_t)linear_scale_stride(M) * ((K + kBlock - 1) / kBlock) * sizeof(float)); }
 
-int gemm_launch(LinArgs a, const uint8_t* codes, const uint8_t* w, int M, int N, int K, const Ws& ws,
-                uint8_t* partials, cudaStream_t s) {
+int plan_here(LinPlan& p, int M, int N, int K) {
   int sms = 0;
   const int rc = current_device_sms(&sms);
-  if (rc != MOE_OK) return rc;
-  LinPlan p;
-  plan_linear(p, M, N, K, sms);
+  if (rc == MOE_OK) plan_linear(p, M, N, K, sms);
+  return rc;
+}
+
+int gemm_launch(const LinPlan& p, LinArgs a, const uint8_t* codes, const uint8_t* w, const Ws& ws, uint8_t* partials,
+                cudaStream_t s) {
   a.status = ws.status;
   a.tickets = ws.tickets;
   a.partials = reinterpret_cast<float*>(partials);
@@ -148,9 +150,11 @@ int fp8_block_gemm(const uint8_t* codes, const float* scales, const uint8_t* w, 
   if (!al16(codes) || !al16(scales) || !al16(w) || !al16(out) || !al16(ws)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const Ws l(ws);
+  LinPlan p;
+  if (const int bad = plan_here(p, M, N, K); bad != MOE_OK) return bad;
   LinArgs a;
   a.xs = scales; a.w_s = w_s; a.out = out; a.out_fp32 = out_fp32 ? 1 : 0;
-  return gemm_launch(a, codes, w, M, N, K, l, l.data, (cudaStream_t)stream);
+  return gemm_launch(p, a, codes, w, l, l.data, (cudaStream_t)stream);
 }
 
 int fp8_linear_workspace_size(int M, int N, int K, size_t* bytes) {
@@ -176,15 +180,17 @@ int fp8_linear(const void* x, long long x_stride, const uint8_t* w, const float*
   uint8_t* partials = codes + codes_bytes(M, K) + scales_bytes(M, K);
   LinArgs a;
   a.w_s = w_s; a.out = out; a.out_fp32 = out_fp32 ? 1 : 0;
-  if (M <= kLinFusedTokens) {
+  LinPlan p;
+  if ((rc = plan_here(p, M, N, K)) != MOE_OK) return rc;
+  if (linear_fused(p)) {
     a.x = x; a.ldx = x_stride; a.e8m0 = e8m0 ? 1 : 0;
-    return gemm_launch(a, nullptr, w, M, N, K, l, partials, (cudaStream_t)stream);
+    return gemm_launch(p, a, nullptr, w, l, partials, (cudaStream_t)stream);
   }
   if ((rc = quant_launch(x, x_stride, M, K, e8m0, codes, scales, (cudaStream_t)stream)) != MOE_OK) return rc;
   // the product streams its first weights while the quantisation still runs
   a.xs = scales;
   a.after_quant = true;
-  return gemm_launch(a, codes, w, M, N, K, l, partials, (cudaStream_t)stream);
+  return gemm_launch(p, a, codes, w, l, partials, (cudaStream_t)stream);
 }
 
 int kv_cache_workspace_size(size_t* bytes) {

@@ -960,7 +960,9 @@ cudaError_t launch_d(const AttArgs& a, const AttMaps& maps, int ctas, cudaStream
 
 }  // namespace
 
-// Rows that share one read of the cache: 8 where a sequence has no more, else 16.
+// Rows that share one read of the cache: 8 where a sequence has no more, else 16 (16
+// sequences of up to 8200 tokens, 7 rows a head and token, us with 8 / with 16: one
+// token each 19.9 / 22.3, two 26.5 / 25.0, four 41.0 / 32.0).
 int attention_row_tiles(int G, int max_new) { return (long long)G * max_new <= 8 ? 1 : 2; }
 
 size_t attention_partial_bytes(int D, int G, int max_new) {

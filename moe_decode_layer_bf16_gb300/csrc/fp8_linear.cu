@@ -5,9 +5,16 @@
 // every sum in fp32, rounded once at the end.  The weight format is the one of
 // the expert layers, so the attention projections around them use it too.
 //
+// What bounds it.  One token of 7168 -> 9216 is 66 MB of weights: 14.5 us, 4.6 TB/s (0.67
+// of the copy rate; start and exchange of sums are about 5 us of it).  4096 tokens are
+// 541 GFLOP: 220 us in a graph, 2460 TFLOP/s, of which the quantisation takes 15 and
+// the MMAs alone 160; between MMAs of a cell the accumulator buffer goes to the epilogue
+// and back, and with two buffers of 256 columns (all of tensor memory) that round trip
+// shows.
+//
 // Two kernels: the quantisation (a stream over x), and the product on
 // tcgen05.mma.kind::f8f6f4 (E4M3 x E4M3, fp32 accumulators in tensor memory);
-// up to 16 tokens one, the product quantising what it needs as it goes.
+// for a few tokens one, the product quantising what it needs as it goes.
 //
 // The product, in two arrangements of one kernel.  Up to 128 tokens the weights are
 // the MMA's 128 rows and the tokens its columns (NT = 16 .. 128), so that one
@@ -34,8 +41,8 @@
 // is last).
 //
 // Roles (12 warps): TMA producer, MMA issuer, a warp that copies each cell's
-// token scales and an idle one (or two that quantise), eight epilogue warps (four lane quadrants x two
-// column halves).  Every wait is bounded.
+// token scales and an idle one (or two of the six that quantise), eight epilogue
+// warps (four lane quadrants x two column halves).  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -160,7 +167,9 @@ struct Cfg {
   // token 23.1 us, first cell 4.7 us after the start).  XQ: all (holding the
   // others back until the first rows of x are here: 18.4 -> 19.1 us)
   static constexpr int kAhead = XQ ? kNST : std::min(kNST, 4);
-  static constexpr int kPrefetch = 20;                        // weight tiles brought into L2 before the kernel before is complete
+  // weight tiles brought into L2 before the kernel before is complete (one token, us:
+  // 6 16.8, 12 16.6, 20 16.0, 32 16.6)
+  static constexpr int kPrefetch = 20;
   static constexpr int kTST = NT <= 128 ? 4 : 2;              // accumulator buffers in tensor memory
   static constexpr int kTCols = NT * kTST;                    // 64 .. 512, a power of two
   static constexpr int kHalf = NT / 2;                        // columns of an epilogue warp
@@ -771,7 +780,10 @@ cudaError_t launch_nt(const LinPlan& p, const LinArgs& a, const LinMaps& maps, c
 }  // namespace
 
 // Up to 128 tokens: the tokens are the columns, at the smallest width that holds
-// them.  Above: token tiles of 256 rows (128 a CTA), weight tiles of 256 columns.
+// them.  Above: token tiles of 256 rows (128 a CTA), weight tiles of 256 columns
+// (tiles of 128 tokens as columns instead, us: 4096 x 7168 -> 9216 495 for 230, 256 x
+// 7168 -> 9216 36.5 for 30.4, 343 x 1392 -> 4957 12.5 for 12.9, 388 x 336 -> 3465 7.5
+// for 9.4: only launches of a few cells lose).
 void plan_linear(LinPlan& p, int M, int N, int K, int sms) {
   p.M = M; p.N = N; p.K = K;
   p.nkb = (K + kBlock - 1) / kBlock;

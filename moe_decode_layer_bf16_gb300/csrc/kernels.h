@@ -216,9 +216,17 @@ struct LinPlan {
   int rest;           // pairs after those,
   int pieces;         // each cut along K into so many
 };
-constexpr int kLinFusedTokens = 16;  // up to so many tokens the product quantises x itself
+// Whether the product quantises x itself: it saves the quantisation's launch, but every
+// CTA quantises the tokens of all its cells, eight at a time.  Up to 8 tokens it always
+// pays, up to 16 where a CTA has few cells.  Measured, us itself / by a kernel of its
+// own: 7168 -> 9216 (28 cells a CTA) 1 token 14.6 / 16.1, 8 16.2 / 16.6, 16 18.8 / 17.2;
+// 2048 -> 1536 (4 cells a CTA) 1 token 5.2 / 6.1, 8 5.5 / 6.5, 16 6.5 / 6.9.
+inline bool linear_fused(const LinPlan& p) {
+  const int cells = p.waves * p.nkb + (p.rest > 0 ? (p.nkb + p.pieces - 1) / p.pieces : 0);
+  return p.M <= 8 || (p.M <= 16 && cells <= 8);
+}
 struct LinArgs {
-  // the caller's: x (to be quantised, M <= kLinFusedTokens) or codes and scales
+  // the caller's: x (to be quantised: linear_fused) or codes and scales
   const void* x = nullptr;     // bf16 [M, K], row stride ldx elements
   long long ldx = 0;
   int e8m0 = 0;
