@@ -104,6 +104,7 @@ MOE_DEV float amax8(const uint4& v) {
   return m;
 }
 
+// (No read-only loads: the kernels here start while others may still write their inputs.)
 __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) {
   grid_dep_wait();    // (launched while the kernel before may still run)
   grid_dep_launch();  // the product may start streaming its weights now
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant_rows_kernel(QuantArgs a) 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int col = (kb0 + 2 * i) * kBlock;
-      v[i] = col + lane16 * 8 < a.K ? __ldg(reinterpret_cast<const uint4*>(x + col)) : make_uint4(0, 0, 0, 0);
+      v[i] = col + lane16 * 8 < a.K ? __ldcg(reinterpret_cast<const uint4*>(x + col)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) amax[i] = amax8(v[i]);
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
       // read ahead; this warp's columns (TR) or the rows are one weight block
       const int wblk = min(TR ? pc.col * (NT / kBlock) + hf : pc.row, p.n_wblk - 1);
       const float* wr = p.w_s + (size_t)wblk * p.nkb;
-      float ws = pc.k0 + lane < pc.k1 ? __ldg(wr + pc.k0 + lane) : 0.f, wn = 0.f;
+      float ws = pc.k0 + lane < pc.k1 ? __ldcg(wr + pc.k0 + lane) : 0.f, wn = 0.f;
       const bool whole = pc.k0 == 0 && pc.k1 == p.nkb;
 #pragma unroll
       for (int j = 0; j < C::kHalf; ++j) acc[j] = 0.f;
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
         const int off = (kb - pc.k0) & 31;
         if (off == 0) {
           if (kb != pc.k0) ws = wn;
-          wn = kb + 32 + lane < pc.k1 ? __ldg(wr + kb + 32 + lane) : 0.f;
+          wn = kb + 32 + lane < pc.k1 ? __ldcg(wr + kb + 32 + lane) : 0.f;
         }
         const float w = __shfl_sync(0xffffffffu, ws, off);
         const uint32_t xi = nc % C::kXST;

@@ -54,6 +54,7 @@ MOE_DEV uint32_t rescale4(uint32_t c, float from, float to) {
                          e4m3_to_f32((c >> 16) & 0xff) * k, e4m3_to_f32(c >> 24) * k);
 }
 
+// (No read-only loads: this kernel starts while others may still write its inputs.)
 template <int D, int P>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = D / 8;                       // threads of a token's row, 8 values each
@@ -67,8 +68,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   // launched while the kernel before may still run: nothing is read before it is complete
   grid_dep_launch();
   grid_dep_wait();
-  const int start = __ldg(a.q_start + b), stop = __ldg(a.q_start + b + 1);
-  const int len = __ldg(a.lens + b);
+  const int start = a.q_start[b], stop = a.q_start[b + 1];
+  const int len = a.lens[b];
   const int n = stop - start;
   if (n == 0 && start >= 0 && start <= a.total) return;
   const long long cap = (long long)a.width * P;
@@ -85,11 +86,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
 #pragma unroll
   for (int p = 0; p < kPass; ++p) {
     const int t = p * kTok + row0;
-    r[p] = t < hi - lo ? __ldg(reinterpret_cast<const uint4*>(rows + (long long)t * stride)) : make_uint4(0, 0, 0, 0);
+    r[p] = t < hi - lo ? __ldcg(reinterpret_cast<const uint4*>(rows + (long long)t * stride)) : make_uint4(0, 0, 0, 0);
   }
   int page = -1;
   if (!bad) {
-    page = __ldg(a.page_table + (size_t)b * a.width + blk);
+    page = a.page_table[(size_t)b * a.width + blk];
     bad = page < 0 || page >= a.num_pages;
   }
   if (bad) {  // nothing is written for this block
