@@ -145,6 +145,7 @@ struct Seq {
 // loads anywhere: the kernel starts while others may still write its inputs.)
 struct Raw {
   int start, stop, len;
+  Raw() = default;
   MOE_DEV Raw(const AttArgs& a, int b) {
     start = __ldcg(a.q_start + b);
     stop = __ldcg(a.q_start + b + 1);
@@ -210,10 +211,10 @@ MOE_DEV bool walk_next(Walk& w, const AttArgs& a) {  // to the next piece
 }
 // The first piece of units x ... x + count, if there is one.
 template <int D, int RT>
-MOE_DEV bool walk_start(Walk& w, const AttArgs& a, int b, int b_first, int x, int count) {
+MOE_DEV bool walk_start(Walk& w, const AttArgs& a, int b, const Raw& r, int b_first, int x, int count) {
   w.left = count;
   w.b = b;
-  w.s = make_seq<D, RT>(a, Raw(a, b), false);
+  w.s = make_seq<D, RT>(a, r, false);
   const int units = w.s.tiles + kItemCost;
   const int it = (x - b_first) / units;
   w.head = it / max(1, w.s.groups);  // (none: only a hint's lengths that changed)
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   // ---- the shares: every thread adds up a run of sequences, then a scan
   __shared__ long long s_scan[kWarps];
   int* s_before = reinterpret_cast<int*>(smem + C::kPartAt);  // [thread]: first unit of its sequences (the pieces come later)
-  int* s_tiles = s_before + kThreads;  // tiles of its sequence, where it has one
+  int* s_tiles = s_before + kThreads;                          // where it has one sequence: its tiles,
+  Raw* s_raw = reinterpret_cast<Raw*>(s_tiles + kThreads);     // and what was read for it
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   const int P = a.page_size;
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   // brought into L2 from it.  After the kernel before is complete the lengths are
   // read again, and where they are others the shares are worked out again.
   // Nothing is written and no copy into shared memory made before.
+  Raw wr;  // of sequence wb
   bool hint = per == 1;
   if (!hint) grid_dep_wait();
   for (;;) {
@@ -356,6 +359,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     const bool fits = total <= INT_MAX;
     s_before[tid] = mine > 0 && fits ? (int)before : -1;
     s_tiles[tid] = tiles;
+    s_raw[tid] = seen;
     __syncthreads();
     // CTAs that get work
     G = fits ? (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps) : 0;
@@ -392,8 +396,10 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
         const int t = __shfl_sync(0xffffffffu, lane * (kThreads / 32) + best, src);
         wat = s_before[t];
         int units = s_tiles[t] + kItemCost;
+        wr = s_raw[t];
         for (wb = min(a.B, t * per); per > 1; ++wb) {
-          const Seq s = make_seq<D, RT>(a, Raw(a, wb), false);
+          wr = Raw(a, wb);
+          const Seq s = make_seq<D, RT>(a, wr, false);
           units = s.tiles + kItemCost;
           const int nb = units * s.groups * a.kv_heads;
           if (x < wat + nb || wb + 1 >= a.B) break;
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     if (!hint) break;
     if (wn > 0) {
       Walk h;
-      const bool any = walk_start<D, RT>(h, a, wb, wat, wx, wn);
+      const bool any = walk_start<D, RT>(h, a, wb, wr, wat, wx, wn);
       const int t0 = h.s.tile0 + max(0, h.u0 - kItemCost), t1 = min(h.s.tile0 + max(0, h.u1 - kItemCost), t0 + kNST);
       const int pos = t0 * kTile + 16 * lane;  // a lane for each 16-token group
       if (any && t0 >= 0 && t0 + lane / kGroups < t1 && lane % gpb == 0 && pos < h.s.len && h.head < a.kv_heads) {
@@ -438,7 +444,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   bool alive = true;
   Walk w;
   bool more = wn > 0;
-  if (more) more = walk_start<D, RT>(w, a, wb, wat, wx, wn);
+  if (more) more = walk_start<D, RT>(w, a, wb, wr, wat, wx, wn);
   while (more) {
     const int rows = min(kRowsC, w.s.n * a.G - w.grp * kRowsC);
     const int pos0 = w.s.len - w.s.n;  // position of the step's first token
