@@ -547,6 +547,48 @@ def test_streams_graph_and_one_workspace():
     assert m.moe_device_status(ws) == m.MOE_OK
 
 
+@pytest.mark.parametrize("D,G", [(128, 4), (64, 12)])
+def test_lengths_written_by_the_kernel_before(D, G):
+    """The attention starts while the kernel before it runs and may look at the lengths
+    early; what counts is what that kernel leaves there.  Here it is a quantisation
+    whose last row of codes is the lengths, other ones each time."""
+    rng = np.random.default_rng(43)
+    hk, page, rows = 2, 32, 20000
+    both = np.array([[300, 5, 832], [64, 777, 3]], np.int32)
+    b = Batch(rng, [832, 832, 832], [1, 1, 1], hk, D, page)
+    t = b.tensors(DEV)
+    q = bf16(bf16_values(rng, (3, hk * G, D))).to(DEV)
+    ws = workspace()
+    x = []
+    for lens in both:
+        last = np.zeros(16, np.uint8)
+        last[:12] = np.frombuffer(lens.tobytes(), np.uint8)
+        last[15] = 0x7E  # 448: the scale is 1, and the codes are the values' own
+        v = np.zeros((rows, 16))
+        v[-1] = orc.e4m3_decode(last)
+        x.append(bf16(v).to(DEV))
+    codes = torch.zeros((rows, 16), dtype=torch.uint8, device=DEV)
+    scales = torch.empty((1, (rows + 3) // 4 * 4), dtype=torch.float32, device=DEV)
+    lens = codes[-1].view(torch.int32)[:3]
+
+    def attend(lens, out):
+        m.decode_attention(q, t["k"], t["v"], t["k_scale"], t["v_scale"], t["table"], t["q_start"], lens, 1, out, ws)
+
+    want = [torch.empty_like(q) for _ in both]
+    for n, o in zip(both, want):
+        attend(torch.from_numpy(n).to(DEV), o)
+    got = [torch.empty_like(q) for _ in range(40)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        m.fp8_quant_rows(x[i % 2], codes, scales)
+        attend(lens, o)
+    torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2]), i
+    assert m.moe_device_status(ws) == m.MOE_OK
+
+
 def test_attention_decode_is_its_parts():
     rng = np.random.default_rng(41)
     hidden, heads, hk, D, page = 384, 6, 2, 64, 16
