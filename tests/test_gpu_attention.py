@@ -443,6 +443,14 @@ def test_linear(M, N, K, e8m0, f32):
     assert (err <= tol).all(), float((err - tol).max())
 
 
+# whole waves of tiles with a remainder, and tiles cut along K, in both arrangements
+@pytest.mark.parametrize("M,N,K", [(3, 19500, 1040), (20, 19457, 528), (12, 700, 3600), (150, 301, 6016), (260, 70, 5136),
+                                   (2000, 2500, 4112)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_linear_waves_and_pieces(M, N, K, f32):
+    test_linear(M, N, K, False, f32)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 1152, 7168), (13, 260, 1040), (40, 1001, 1552), (200, 700, 2064)])
 def test_linear_is_its_two_parts_and_repeats(M, N, K):
     rng = np.random.default_rng(M)
