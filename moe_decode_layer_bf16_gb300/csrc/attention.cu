@@ -10,6 +10,10 @@
 // What bounds it: each cached byte is read once for the 8 or 16 rows that share
 // the head, far below the tensor cores' balance, so the cache stream from HBM
 // is the floor.  One pass with the running maximum and sum of the softmax.
+// Measured: 61 sequences of 300 to 16384 tokens, 526 MB, 87.9 us, 6.0 TB/s (0.88 of the
+// copy rate); one of 131001 tokens 51.2 us, 5.2 TB/s; about 2 us until the lengths, the
+// page numbers and the first tile are there, and 4 until the pieces are joined, are
+// what short caches cost (777 tokens 9.4 us).
 //
 // Work split.  The unit is a tile of 32 tokens of one item (sequence, kv head,
 // group of up to 8 RT rows); an item counts kItemCost tiles more for its start and
@@ -57,7 +61,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kItemCost = 2;              // units of an item beside its tiles
+// Units of an item beside its tiles: its start and end take a warp as long as two tiles (61
+// sequences of 300 to 16384 tokens, us: 1 100.7, 2 87.9, 3 88.2, 4 89.2).
+constexpr int kItemCost = 2;
 // Items of so many tiles at most are not cut: a tile takes a warp 1.3 us, joining pieces
 // 5 us (80 drawn cases, geometric mean: 0 13.1 us, 1 11.2, 2 11.0, 4 11.0, 8 11.5; 3
 // sequences of 2 tokens, 96 heads on 8: 14.1 us cut, 7.4 whole).
