@@ -915,7 +915,9 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     s_last[warp] = last ? c0 | c1 << 16 : -1;
   }
   __syncthreads();
-  constexpr int kJoin = kVec < 16 ? kVec : 16;  // pieces read together (32: 25 long sequences 34.7 us, 16 33.5, 8 33.1; 1 x 51673 tokens 34.3, 34.9, 35.8)
+  // pieces read together (all D / 4 at once: more code that runs once; 25 long sequences,
+  // 128 heads, us: 32 34.7, 16 33.5, 8 33.1; one of 51673 tokens 34.3, 34.9, 35.8)
+  constexpr int kJoin = kVec < 16 ? kVec : 16;
   for (int i = 0; i < n_out; ++i) {
     const int last = s_last[i];
     if (last < 0) continue;
