@@ -140,7 +140,7 @@ def prepare(case, seed):
         w = _to_e4m3((pad / w_s[:, None, :, None]).view(nb * BLOCK, kb * BLOCK)[:n, :k]).view(torch.uint8).contiguous()
         return {"op": "linear", "e8m0": case["e8m0"], "x": x, "w": w, "w_s": w_s.contiguous(),
                 "out": torch.empty((m, n), dtype=torch.bfloat16, device=DEV),
-                "workspace": torch.zeros((256 << 20,), dtype=torch.uint8, device=DEV)}
+                "workspace": torch.zeros((64 << 20,), dtype=torch.uint8, device=DEV)}
     lens = _lens(case)
     news = _news(case, lens)
     b, hk, d, page = case["b"], case["kv_heads"], case["dim"], case["page"]
@@ -156,7 +156,7 @@ def prepare(case, seed):
     s = {"op": case["op"], "page": page, "max_new": max(news), "table": table,
          "lens": torch.tensor(lens, dtype=torch.int32, device=DEV),
          "q_start": torch.tensor(sums, dtype=torch.int32, device=DEV),
-         "workspace": torch.zeros((256 << 20,), dtype=torch.uint8, device=DEV)}
+         "workspace": torch.zeros((64 << 20,), dtype=torch.uint8, device=DEV)}
 
     def cache():
         # keys and values of unit size with a loudness of their own for each page and head
