@@ -71,6 +71,9 @@ constexpr int kWholeTiles = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.f;        // weights are rounded to f16 in units of 2^-15
+// Where the largest V scale seen starts from: the smallest normal number, so that its
+// reciprocal is finite.  (A block of zeros has this scale: 2^15 over it is not.)
+constexpr float kMinUnit = 1.17549435e-38f;
 
 // A piece of an item that a warp (or, in the workspace, a CTA) could not finish.
 struct Piece {
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[rt][mt][i] = 0.f;
     }
-    float R = 0.f;  // largest V scale so far: the accumulators' unit is R 2^-15
+    float R = kMinUnit;  // largest V scale so far: the accumulators' unit is R 2^-15
     for (int t = t0; t < t1; ++t) {
       const int si = used % kNST;
       if (t - cur0 == kBatch) {
@@ -665,7 +668,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
       float Rn = R;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) Rn = fmaxf(Rn, vsg[i]);  // (0 where a group was not read)
-      const float Rq = Rn > 0.f ? __fdividef(kPScale, Rn) : 0.f;
+      const float Rq = __fdividef(1.f, Rn);
       const float rr = Rn == R ? 1.f : __fdividef(R, Rn);
       float al[RT];
       bool turn = Rn != R;
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kTile / 8; ++j) {
-          const float F = vsg[j >> 1] * Rq;
+          const float F = vsg[j >> 1] * Rq * kPScale;
           const float p0 = ex2(s[rt][2 * j] - ms), p1 = ex2(s[rt][2 * j + 1] - ms);
           sum += p0 + p1;
           // masked tokens of a group that was not loaded: vs is 0, p is 0
@@ -756,7 +759,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
       l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 1);
       l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 2);
     }
-    const float ru = R * (1.f / kPScale);
+    // (R and 2^-15 one after the other: their product may be no normal number)
     if (whole) {
       // columns 2 q and 2 q + 1 of the accumulator are rows; this thread has
       // D / 8 consecutive values of each from fg * D / 8
@@ -768,11 +771,11 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
           const float L = __shfl_sync(0xffffffffu, l[rt], 8 * q + 4 * c);
           const float M = __shfl_sync(0xffffffffu, m[rt], 8 * q + 4 * c);
           if (r < rows) {
-            const float inv = L == 0.f ? 0.f : __fdividef(ru, L);
+            const float inv = L == 0.f ? 0.f : __fdividef(1.f / kPScale, L);
             const OutRow o_at(a, w.s.start, w.grp * kRowsC + r, w.head);
             uint32_t v[kMT];
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) v[mt] = pack_bf16(o[rt][mt][c] * inv, o[rt][mt][2 + c] * inv);
+            for (int mt = 0; mt < kMT; ++mt) v[mt] = pack_bf16(o[rt][mt][c] * inv * R, o[rt][mt][2 + c] * inv * R);
             uint4* dst = reinterpret_cast<uint4*>(o_at.out(a, D) + fg * (D / 8));
 #pragma unroll
             for (int k = 0; k < kMT / 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
@@ -782,6 +785,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     } else {
       const int last = w.u0 == 0 ? 1 : 0;  // (a warp's piece that starts an item and does not end it is its last)
       float* p = part_of(warp, last);
+      auto unit = [&](float x) { return x * (1.f / kPScale) * R; };
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
@@ -789,7 +793,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
 #pragma unroll
           for (int mt = 0; mt < kMT; mt += 2)
             *reinterpret_cast<float4*>(p + (rt * 8 + 2 * q + c) * D + fg * (D / 8) + 2 * mt) =
-                make_float4(o[rt][mt][c] * ru, o[rt][mt][2 + c] * ru, o[rt][mt + 1][c] * ru, o[rt][mt + 1][2 + c] * ru);
+                make_float4(unit(o[rt][mt][c]), unit(o[rt][mt][2 + c]), unit(o[rt][mt + 1][c]), unit(o[rt][mt + 1][2 + c]));
         if (q == 0) *reinterpret_cast<float2*>(p + kRowsC * D + 2 * (rt * 8 + g)) = make_float2(m[rt], l[rt]);
       }
       if (lane == 0) {

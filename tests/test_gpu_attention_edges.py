@@ -1,0 +1,114 @@
+"""The attention sublayer's operators at the ends of their range on the GPU, against
+the float64 oracle (oracle/attention_oracle.py)."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import moe_decode_layer_bf16_gb300 as m
+from tests.fixtures_attention import BF16, F16, F32, Batch, bf16, bf16_values, orc, weights
+from tests.test_gpu_attention import dev, f64, run_attention, workspace
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def largest_value(b):
+    """Of the batch's V, NaN aside."""
+    v = orc.e4m3_decode(b.cache["v"]) * b.cache["v_scale"].astype(np.float64)[:, :, None, None]
+    return float(np.nanmax(np.abs(v), initial=0.0))
+
+
+def tolerance(ref, D, count, vmax, score=0.0):
+    """(for out, for lse) of ref = oracle's (out, lse, mag, unit).
+
+    A score: q's f16 values are within 2^-39 of the row's largest (times sum |k|), the
+    products are exact, each of the D / 16 steps of 16 products takes two fp32 roundings of
+    sum |q k|, and the scales, the bias, the change to base 2, the cap's products and the
+    difference from the maximum 16 more; `score` is what the caller adds (the tanh).  A
+    weight: its score's error and the sum's, the exponential's 2^-22 twice, one rounding to
+    f16, and the floor of f16's subnormals, 2^-25 in units of 2^-15 of the largest weight.
+    Sums over the tokens and the pieces: an fp32 rounding for each group of 16 tokens, and
+    at most 300 pieces.  Then the output's rounding (2^-134: half a subnormal step)."""
+    out, lse, mag, unit = ref
+    e = 2.0 ** -39 * unit[..., 1] + (D / 8 + 16) * F32 * unit[..., 0] + score
+    sums = (count / 16 + 300) * F32
+    t = (2 * e + 2.0 ** -21 + F16 + sums)[..., None] * mag + count * 2.0 ** -40 * vmax
+    t = t + BF16 * (np.abs(out) + t) + 2.0 ** -134
+    return t, e + 2.0 ** -21 + sums + 4 * F32 * np.abs(np.where(np.isfinite(lse), lse, 0.0))
+
+
+def check(b, q, got, lse, sm, score=0.0, rows=None, **kw):
+    """The oracle's values; where it has no number, neither has the kernel."""
+    ref = orc.attention(q, b.cache, b.table, b.q_start, b.lens, sm, **kw)
+    t_out, t_lse = tolerance(ref, b.D, int(max(b.lens.max(), 1)), largest_value(b), score)
+    rows = slice(None) if rows is None else rows
+    nan = np.isnan(ref[0])[rows]
+    assert np.array_equal(np.isnan(got[rows]), nan)
+    off = np.abs(got - ref[0])[rows]
+    assert ((off <= t_out[rows]) | nan).all(), float(np.nanmax(off - t_out[rows]))
+    if lse is not None:
+        same = (lse == ref[1]) | (np.isnan(lse) & np.isnan(ref[1]))  # (both -inf)
+        with np.errstate(invalid="ignore"):
+            assert (same | (np.abs(lse - ref[1]) <= t_lse))[rows].all()
+
+
+# ---------------------------------------------------------------- blocks of zeros
+TINY = np.float32(2.0 ** -126)  # the scale that the append gives a block of zeros
+
+
+@pytest.mark.parametrize("D,hk,G,page", [(64, 2, 2, 16), (128, 1, 4, 64), (128, 2, 12, 32), (64, 1, 9, 128)])
+def test_values_of_zeros_give_zeros(D, hk, G, page):
+    """All V zero, written by the append: out is zero exactly, lse as ever."""
+    rng = np.random.default_rng(50)
+    lens = [5, 40, 300, 1, 2000]
+    b = Batch(rng, lens, lens, hk, D, page)
+    t = b.tensors(DEV)
+    ws = workspace()
+    k = bf16_values(rng, (b.total, hk, D))
+    m.kv_cache_append(bf16(k).to(DEV), torch.zeros((b.total, hk, D), dtype=torch.bfloat16, device=DEV), t["k"], t["v"],
+                      t["k_scale"], t["v_scale"], t["table"], t["q_start"], t["lens"], 2000, ws)
+    b.cache = {n: t[n].cpu().numpy() for n in b.cache}
+    assert (b.cache["v_scale"][b.table[b.table >= 0]] == TINY).all()
+    b.q_start, b.total, b.news = np.arange(6, dtype=np.int32), 5, [1] * 5
+    t["q_start"] = dev(b.q_start)
+    q = bf16_values(rng, (5, hk * G, D))
+    got, lse, status = run_attention(b, q, hk * G, tensors=t)
+    assert status == m.MOE_OK
+    assert (got == 0).all()
+    check(b, q, got, lse, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("where", ["first", "last", "every other", "middle", "all but one", "a warp's start"])
+@pytest.mark.parametrize("D,hk,G,page", [(64, 2, 2, 16), (128, 1, 7, 64), (128, 2, 12, 32)])
+def test_blocks_of_zeros_among_others(where, D, hk, G, page):
+    rng = np.random.default_rng(51)
+    b = Batch(rng, [9000, 700, 64, 90], [1, 2, 1, 1], hk, D, page)
+    for s in range(4):
+        n = -(-int(b.lens[s]) // page)
+        at = {"first": [0], "last": [n - 1], "every other": range(0, n, 2), "middle": range(n // 3, n // 2 + 1),
+              "all but one": [i for i in range(n) if i != n // 2], "a warp's start": range(0, n, 5)}[where]
+        for i in at:
+            b.cache["v"][b.table[s, i]] &= 0x80  # zeros of either sign
+            b.cache["v_scale"][b.table[s, i]] = TINY
+    q = bf16_values(rng, (b.total, hk * G, D))
+    got, lse, status = run_attention(b, q, hk * G)
+    assert status == m.MOE_OK
+    check(b, q, got, lse, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("D,hk,G,page", [(64, 2, 2, 16), (128, 1, 7, 64), (128, 2, 12, 32)])
+@pytest.mark.parametrize("spread", [0, 8, 20])
+def test_values_of_the_smallest_scales(D, hk, G, page, spread):
+    """V scales from 2^-126 up: small, but values like any others."""
+    rng = np.random.default_rng(52)
+    b = Batch(rng, [3000, 33, 150], [1, 2, 1], hk, D, page)
+    shape = b.cache["v_scale"].shape
+    b.cache["v_scale"] = np.where(np.isnan(b.cache["v_scale"]), np.nan,
+                                  np.exp2(-126 + np.round(rng.uniform(0, spread, shape)))).astype(np.float32)
+    q = bf16_values(rng, (b.total, hk * G, D))
+    got, lse, status = run_attention(b, q, hk * G)
+    assert status == m.MOE_OK
+    check(b, q, got, lse, 1 / math.sqrt(D))
