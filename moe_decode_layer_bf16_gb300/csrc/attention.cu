@@ -53,6 +53,7 @@
 #include "async.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "step_rows.h"
 #include "tcgen05.cuh"
 #include "tmap.h"
 #include "../../include/moe_decode.h"
@@ -166,14 +167,11 @@ template <int D, int RT>
 MOE_DEV Seq make_seq(const AttArgs& a, const Raw& r, bool report) {
   constexpr int kTile = AttCfg<D, RT>::kTile;
   Seq s;
-  s.start = r.start;
-  // (a difference that does not fit counts as negative)
-  const long long n = (long long)r.stop - r.start;
-  s.n = n > a.total ? -1 : (int)max(n, -1ll);
+  bool bad = !step_rows_ok(r.start, r.stop, a.total);
+  s.start = bad ? 0 : r.start;
+  s.n = bad ? 0 : r.stop - r.start;
   s.len = r.len;
   const long long cap = (long long)a.width * a.page_size;
-  bool bad = false;
-  if (s.start < 0 || s.n < 0 || s.start > a.total || s.n > a.total - s.start) { s.n = 0; s.start = 0; bad = true; }
   if (s.len < 0 || s.len > cap) { s.len = 0; bad = true; }
   if (bad && report) atomicExch(a.status, MOE_ERR_INVALID_ARG);
   // the first token any row sees (the first row's window), then whole tiles

@@ -16,6 +16,7 @@
 // by latency for a token each and by DRAM for prompt chunks.
 #include "common.cuh"
 #include "kernels.h"
+#include "step_rows.h"
 #include "../../include/moe_decode.h"
 
 namespace moe {
@@ -70,10 +71,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   grid_dep_wait();
   const int start = a.q_start[b], stop = a.q_start[b + 1];
   const int len = a.lens[b];
-  const int n = stop - start;
-  if (n == 0 && start >= 0 && start <= a.total) return;
+  const bool rows_ok = step_rows_ok(start, stop, a.total);
+  const int n = rows_ok ? stop - start : 0;
+  if (rows_ok && n == 0) return;
   const long long cap = (long long)a.width * P;
-  bool bad = start < 0 || n < 0 || stop > a.total || n > a.max_new || len < n || len > cap;
+  bool bad = !rows_ok || n > a.max_new || len < n || len > cap;
   const int blk = bad ? 0 : (len - n) / P + j;
   if (!bad && blk > (len - 1) / P) return;  // the call touches fewer blocks of this sequence
   const int lo = max(blk * P, len - n), hi = bad ? lo : min((blk + 1) * P, len);  // new positions in this block

@@ -9,7 +9,7 @@ import torch
 
 import moe_decode_layer_bf16_gb300 as m
 from tests.fixtures_attention import BF16, F16, F32, Batch, bf16, bf16_values, orc, weights
-from tests.test_gpu_attention import dev, f64, run_attention, workspace
+from tests.test_gpu_attention import assert_cache, dev, f64, run_attention, workspace
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -112,3 +112,36 @@ def test_values_of_the_smallest_scales(D, hk, G, page, spread):
     got, lse, status = run_attention(b, q, hk * G)
     assert status == m.MOE_OK
     check(b, q, got, lse, 1 / math.sqrt(D))
+
+
+# ---------------------------------------------------------------- row numbers of every size
+def wild_rows(b):
+    """Sequences 1 to 3 of five get rows that are none: their ends are the largest and the
+    smallest int32, whose differences wrap to small numbers."""
+    b.q_start = np.array([0, 5, 2 ** 31 - 1, -2 ** 31, 5, 6], np.int32)
+    b.total = 6
+    return b
+
+
+def test_append_row_numbers_whose_difference_wraps():
+    rng = np.random.default_rng(60)
+    b = wild_rows(Batch(rng, [70, 40, 33, 20, 9], [5, 1, 1, 1, 1], 2, 64, 32))
+    k, v = (bf16_values(rng, (6, 2, 64)) for _ in range(2))
+    want = {n: a.copy() for n, a in b.cache.items()}
+    orc.append(k, v, want, b.table, [0, 5, 5, 5, 5, 6], b.lens)
+    t = b.tensors(DEV)
+    ws = workspace(m.kv_cache_workspace_size())
+    m.kv_cache_append(bf16(k).to(DEV), bf16(v).to(DEV), t["k"], t["v"], t["k_scale"], t["v_scale"], t["table"],
+                      t["q_start"], t["lens"], 5, ws)
+    assert m.moe_device_status(ws) == m.MOE_ERR_INVALID_ARG
+    assert_cache(t, want)
+
+
+def test_attention_row_numbers_whose_difference_wraps():
+    rng = np.random.default_rng(61)
+    b = wild_rows(Batch(rng, [70, 40, 33, 20, 9], [5, 1, 1, 1, 1], 2, 64, 32))
+    q = bf16_values(rng, (6, 4, 64))
+    got, lse, status = run_attention(b, q, 4)
+    assert status == m.MOE_ERR_INVALID_ARG
+    b.q_start = np.array([0, 5, 5, 5, 5, 6], np.int32)
+    check(b, q, got, lse, 0.125)
