@@ -71,6 +71,14 @@ def _handle(stream):
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
+def _torch_stream(stream, device):
+    """torch's stream of a stream or a handle (0 is the default stream's)."""
+    if isinstance(stream, torch.Stream):
+        return stream
+    handle = _handle(stream)
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
 # The extension module refuses what is not as an operator wants it without a
 # word; these functions find out what it was and say so.
 def _want(t, name, dtype, shape):
@@ -272,8 +280,8 @@ class AttentionDecode:
     weights: qkv (E4M3 [(heads + 2 kv_heads) * head_dim, hidden]), o (E4M3
     [hidden, heads * head_dim]) and their float32 block scales qkv_s, o_s.
     `rotate(q, k)`, if given, changes the step's queries and keys in place
-    (position encodings) before they are used.  softcap, window, slopes and
-    sm_scale as decode_attention's."""
+    (position encodings) before they are used; the step's stream is then torch's
+    current one.  softcap, window, slopes and sm_scale as decode_attention's."""
 
     def __init__(self, hidden: int, heads: int, kv_heads: int, head_dim: int, weights: dict, cache: Fp8KvCache,
                  max_tokens: int, max_new: int = 1, e8m0: bool = False, rotate=None, **options):
@@ -294,21 +302,23 @@ class AttentionDecode:
     def __call__(self, x, page_table, q_start, lens, out=None, stream=None):
         """x bf16 [tokens, hidden] -> bf16 [tokens, hidden]; page_table, q_start
         and lens as kv_cache_append's (lens with the step's tokens included)."""
+        if stream is not None:  # (rotate and a new output's memory belong to it as well)
+            with torch.cuda.stream(_torch_stream(stream, x.device)):
+                return self(x, page_table, q_start, lens, out)
         n, h, hk, c, w = x.shape[0], self.heads, self.kv_heads, self.cache, self.weights
         if n > self.max_tokens:
             raise ValueError(f"{n} tokens: at most {self.max_tokens}")
         if out is None:
             out = torch.empty((n, self.hidden), dtype=_bf16, device=x.device)
         qkv, mixed = self.qkv[:n], self.mixed[:n]
-        fp8_linear(x, w["qkv"], w["qkv_s"], qkv.view(n, -1), self.workspace, e8m0=self.e8m0, stream=stream)
+        fp8_linear(x, w["qkv"], w["qkv_s"], qkv.view(n, -1), self.workspace, e8m0=self.e8m0)
         q, k, v = qkv[:, :h], qkv[:, h:h + hk], qkv[:, h + hk:]
         if self.rotate is not None:
             self.rotate(q, k)
-        kv_cache_append(k, v, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, self.max_new, self.workspace,
-                        stream=stream)
+        kv_cache_append(k, v, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, self.max_new, self.workspace)
         decode_attention(q, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, self.max_new, mixed,
-                         self.workspace, stream=stream, **self.options)
-        fp8_linear(mixed.view(n, -1), w["o"], w["o_s"], out, self.workspace, e8m0=self.e8m0, stream=stream)
+                         self.workspace, **self.options)
+        fp8_linear(mixed.view(n, -1), w["o"], w["o_s"], out, self.workspace, e8m0=self.e8m0)
         return out
 
     def status(self) -> int:

@@ -1,13 +1,15 @@
 """Host-side rules of the attention sublayer's operators (no GPU)."""
 
+import contextlib
 import ctypes
 import itertools
 import os
 import subprocess
 
-import pytest
+import torch
 
 import moe_decode_layer_bf16_gb300 as m
+from moe_decode_layer_bf16_gb300 import attention as att
 
 CSRC = os.path.join(os.path.dirname(m.__file__), "csrc")
 
@@ -30,3 +32,38 @@ def test_rows_of_a_step_that_do_not_fit(tmp_path):
     for total in (0, 1, 6, 1 << 24):
         for start, stop in itertools.product(ends, ends):
             assert bool(L.ok(start, stop, total)) == (0 <= start <= stop <= total), (start, stop, total)
+
+
+def test_attention_decode_stays_on_the_stream_it_is_given(monkeypatch):
+    """Everything of a step, `rotate` and a new output among it, runs with that stream current."""
+    current, seen = [None], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, current[0] = current[0], s
+        yield
+        current[0] = before
+
+    def note(what):
+        return lambda *args, stream=None, **kw: seen.append((what, current[0] if stream is None else stream))
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(att, "moe_workspace_init", lambda ws: None)
+    for name in ("fp8_linear", "kv_cache_append", "decode_attention"):
+        monkeypatch.setattr(att, name, note(name))
+    empty = torch.empty
+
+    def allocate(*args, **kw):
+        seen.append(("empty", current[0]))
+        return empty(*args, **kw)
+
+    layer = m.AttentionDecode(128, 2, 1, 64, dict.fromkeys(("qkv", "qkv_s", "o", "o_s")),
+                              m.Fp8KvCache(2, 1, 64, 16, device="cpu"), max_tokens=2, rotate=note("rotate"))
+    monkeypatch.setattr(torch, "empty", allocate)
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    for s in (None, torch.Stream(device="cpu")):
+        seen.clear()
+        layer(x, None, None, None, stream=s)
+        assert [w for w, _ in seen] == ["empty", "fp8_linear", "rotate", "kv_cache_append", "decode_attention", "fp8_linear"]
+        assert all(at is s for _, at in seen)
+    assert current == [None]

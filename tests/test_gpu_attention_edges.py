@@ -145,3 +145,41 @@ def test_attention_row_numbers_whose_difference_wraps():
     assert status == m.MOE_ERR_INVALID_ARG
     b.q_start = np.array([0, 5, 5, 5, 5, 6], np.int32)
     check(b, q, got, lse, 0.125)
+
+
+# ---------------------------------------------------------------- streams
+@pytest.mark.parametrize("handle", [False, True])
+def test_attention_decode_on_a_side_stream_with_rotated_keys(handle):
+    """The side stream is busy as the step is called: what of it ran elsewhere would read
+    and write the projection before it is there."""
+    rng = np.random.default_rng(62)
+    hidden, heads, hk, D, page = 384, 6, 2, 64, 16
+    (qkv, qkv_s), (o, o_s) = weights(rng, (heads + 2 * hk) * D, hidden), weights(rng, hidden, heads * D)
+    wt = {"qkv": dev(qkv), "qkv_s": dev(qkv_s), "o": dev(o), "o_s": dev(o_s)}
+    side, at = torch.cuda.Stream(), []
+
+    def rotate(q, k):
+        at.append(torch.cuda.current_stream().cuda_stream)
+        q.mul_(-2)
+        k.mul_(0.5)
+
+    table = dev(np.array([[3, 1], [0, 7]], np.int32))
+    start, lens = dev(np.array([0, 3, 5], np.int32)), dev(np.array([3, 2], np.int32))
+    xs = [bf16(bf16_values(rng, (5, hidden))).to(DEV) for _ in range(4)]
+    both, busy = [], torch.randn((8192, 8192), device=DEV, dtype=torch.bfloat16)
+    for stream in (None, side):
+        att = m.AttentionDecode(hidden, heads, hk, D, wt, m.Fp8KvCache(8, hk, D, page), max_tokens=6, max_new=3,
+                                rotate=rotate)
+        ys = []
+        torch.cuda.synchronize()
+        for x in xs:
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    torch.mm(busy, busy)
+            ys.append(att(x, table, start, lens, stream=stream.cuda_stream if stream and handle else stream))
+        torch.cuda.synchronize()
+        assert att.status() == m.MOE_OK
+        both.append(ys)
+    assert at == [torch.cuda.current_stream().cuda_stream] * 4 + [side.cuda_stream] * 4
+    for a, b in zip(*both):
+        assert torch.equal(a, b)
