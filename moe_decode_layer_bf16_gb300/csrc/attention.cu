@@ -962,9 +962,8 @@ bool map_cache(CUtensorMap* m, const uint8_t* base, int D, int P, long long tile
 template <int D, int RT, bool MODS>
 cudaError_t launch_cfg(const AttArgs& a, const AttMaps& maps, int ctas, cudaStream_t s) {
   using C = AttCfg<D, RT>;
-  static const cudaError_t rc =
-      cudaFuncSetAttribute(attention_kernel<D, RT, MODS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-  if (rc != cudaSuccess) return rc;
+  static OncePerDevice once;
+  if (const cudaError_t rc = allow_smem(once, attention_kernel<D, RT, MODS>, C::kSmem); rc != cudaSuccess) return rc;
   PdlLaunch L(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
   return cudaLaunchKernelEx(&L.cfg, attention_kernel<D, RT, MODS>, a, maps);
 }

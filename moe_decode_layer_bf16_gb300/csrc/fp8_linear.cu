@@ -762,10 +762,8 @@ __global__ void __launch_bounds__((Cfg<NT, TR, XQ>::kThreads), 1) linear_kernel(
 template <int NT, bool TR, bool XQ>
 cudaError_t launch_nt(const LinPlan& p, const LinArgs& a, const LinMaps& maps, cudaStream_t s) {
   using C = Cfg<NT, TR, XQ>;
-  // a process-wide attribute of the kernel, set once (an atomic static)
-  static const cudaError_t rc =
-      cudaFuncSetAttribute(linear_kernel<NT, TR, XQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-  if (rc != cudaSuccess) return rc;
+  static OncePerDevice once;
+  if (const cudaError_t rc = allow_smem(once, linear_kernel<NT, TR, XQ>, C::kSmem); rc != cudaSuccess) return rc;
   PdlLaunch L(dim3(C::kPair ? 2 * p.G : p.G), dim3(C::kThreads), C::kSmem, s);
   cudaLaunchAttribute attr[2] = {L.attr[0], {}};
   if (C::kPair) {

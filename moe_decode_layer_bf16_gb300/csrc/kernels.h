@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "per_device.h"
+
 namespace moe {
 
 constexpr int kBlock = 128;  // weight scale block side / activation group length
@@ -284,6 +286,14 @@ struct AttArgs {
 int attention_row_tiles(int G, int max_new);
 size_t attention_partial_bytes(int D, int G, int max_new);
 cudaError_t launch_attention(const AttArgs& a, int sms, cudaStream_t s);
+
+// Lets launches of `kernel` on the current device take `bytes` of dynamic shared memory.
+template <class K>
+cudaError_t allow_smem(OncePerDevice& once, K kernel, size_t bytes) {
+  int dev = 0;
+  if (const cudaError_t rc = cudaGetDevice(&dev); rc != cudaSuccess) return rc;
+  return once(dev, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
+}
 
 // Launch configuration that lets a kernel start while its predecessor in the
 // stream finishes (it waits with griddepcontrol.wait before using its results).

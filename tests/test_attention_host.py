@@ -4,6 +4,7 @@ import contextlib
 import ctypes
 import itertools
 import os
+import re
 import subprocess
 
 import torch
@@ -67,3 +68,31 @@ def test_attention_decode_stays_on_the_stream_it_is_given(monkeypatch):
         assert [w for w, _ in seen] == ["empty", "fp8_linear", "rotate", "kv_cache_append", "decode_attention", "fp8_linear"]
         assert all(at is s for _, at in seen)
     assert current == [None]
+
+
+def test_a_setting_is_made_once_on_each_device(tmp_path):
+    """The second device of a process gets its own, and a failure is not kept."""
+    L = compiled(tmp_path, "devices", '#include "per_device.h"\n'
+                 "static moe::OncePerDevice once;\n"
+                 'extern "C" int set(int dev, int rc, int* calls) { return once(dev, [&] { ++*calls; return rc; }); }\n')
+    calls = ctypes.c_int(0)
+
+    def made(dev, rc=0):
+        before = calls.value
+        return L.set(dev, rc, ctypes.byref(calls)), calls.value - before
+
+    assert made(0) == (0, 1) and made(0) == (0, 0)
+    assert made(1) == (0, 1) and made(1) == (0, 0) and made(0) == (0, 0)
+    assert made(2, 7) == (7, 1) and made(2, 7) == (7, 1) and made(2) == (0, 1) and made(2) == (0, 0)
+    assert made(63) == (0, 1) and made(63) == (0, 0)
+    for dev in (-1, 64, 1000):  # not kept: asked for each time
+        assert made(dev) == (0, 1) and made(dev) == (0, 1)
+
+
+def test_no_kernel_keeps_its_shared_memory_limit_for_the_process():
+    """cudaFuncSetAttribute acts on the current device: behind a static of the process it
+    would leave the next device without."""
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name)) as f:
+            text = " ".join(f.read().split())
+        assert not re.search(r"static[^;]*cudaFuncSetAttribute", text), name
