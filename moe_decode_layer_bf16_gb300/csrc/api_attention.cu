@@ -14,6 +14,8 @@ namespace moe {
 namespace {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+// No sequence is longer, so no window is wider (and its differences fit in 32 bits).
+constexpr int kMaxLen = 1 << 30;
 bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Start of every workspace of these operators: the status word, then the
@@ -105,7 +107,7 @@ int check_batch(const moe_kv_cache* c, const int32_t* page_table, int width, con
                 const int32_t* lens, int B, int total, int max_new) {
   if (B < 0 || total < 0 || width < 1 || max_new < 1) return MOE_ERR_INVALID_ARG;
   if (!page_table || !q_start || !lens) return MOE_ERR_INVALID_ARG;
-  if ((long long)width * c->page_size > (1 << 30) || B > (1 << 20) || total > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if ((long long)width * c->page_size > kMaxLen || B > (1 << 20) || total > (1 << 24)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -257,7 +259,7 @@ int decode_attention(const moe_kv_cache* cache, const void* q, long long q_strid
   a.page_table = page_table; a.q_start = q_start; a.lens = lens; a.slopes = slopes; a.out = out; a.lse = lse;
   a.num_pages = cache->num_pages; a.kv_heads = cache->kv_heads; a.page_size = cache->page_size;
   a.head_dim = cache->head_dim; a.width = width; a.B = B; a.total = total; a.max_new = max_new;
-  a.G = heads / cache->kv_heads; a.window = window; a.sm_scale = sm_scale; a.softcap = softcap;
+  a.G = heads / cache->kv_heads; a.window = std::min(window, kMaxLen); a.sm_scale = sm_scale; a.softcap = softcap;
   a.status = l.status; a.tickets = l.tickets; a.partials = reinterpret_cast<float*>(l.data);
   return launch_attention(a, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -183,3 +183,15 @@ def test_attention_decode_on_a_side_stream_with_rotated_keys(handle):
     assert at == [torch.cuda.current_stream().cuda_stream] * 4 + [side.cuda_stream] * 4
     for a, b in zip(*both):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- windows
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30, 2 ** 30 - 1])
+def test_windows_beyond_every_length(window):
+    """No window at all, also for a sequence with more new rows than tokens."""
+    rng = np.random.default_rng(53)
+    b = Batch(rng, [1, 300, 40, 2], [4, 2, 40, 5], 2, 64, 16)
+    q = bf16_values(rng, (b.total, 4, 64))
+    got, lse, status = run_attention(b, q, 4, window=window)
+    assert status == m.MOE_OK
+    check(b, q, got, lse, 0.125)
