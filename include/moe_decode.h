@@ -421,7 +421,8 @@ int kv_cache_append(const moe_kv_cache *cache, const void *k, long long k_stride
  * outside [0, num_pages) are masked.
  *   q      bf16 [total, heads, head_dim], tokens q_stride elements apart
  *          (% 8 == 0), 16-byte aligned; heads % kv_heads == 0, heads <= 4096,
- *          total * heads < 2^31
+ *          total * heads < 2^31,
+ *          min(B, total) * kv_heads + total * heads / 8 <= 7 * 10^8
  *   out    bf16 [total, heads, head_dim];  lse fp32 [total, heads] or NULL
  *   slopes fp32 [heads] or NULL
  * Scores, statistics and sums are fp32; the weights are rounded to 11 bits for

@@ -246,6 +246,8 @@ int decode_attention(const moe_kv_cache* cache, const void* q, long long q_strid
   if ((rc = decode_attention_workspace_size(heads, cache->kv_heads, cache->head_dim, max_new, &need)) != MOE_OK) return rc;
   if (!std::isfinite(sm_scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return MOE_ERR_INVALID_ARG;
   if ((long long)total * heads > INT_MAX) return MOE_ERR_UNSUPPORTED;
+  if ((long long)std::min(B, total) * cache->kv_heads + (long long)total * heads / 8 > kAttMaxItems)
+    return MOE_ERR_UNSUPPORTED;
   if (B == 0 || total == 0) return MOE_OK;
   if ((rc = check_rows(q, q_stride, (long long)heads * cache->head_dim)) != MOE_OK) return rc;
   if (!out || !ws || !al16(out) || !al16(ws)) return MOE_ERR_INVALID_ARG;

@@ -69,6 +69,10 @@ constexpr int kItemCost = 2;
 // 5 us (80 drawn cases, geometric mean: 0 13.1 us, 1 11.2, 2 11.0, 4 11.0, 8 11.5; 3
 // sequences of 2 tokens, 96 heads on 8: 14.1 us cut, 7.4 whole).
 constexpr int kWholeTiles = 2;
+// Where tiles as units come to more than 31 bits (a prompt of 93000 tokens, 128 heads on 8),
+// a unit is 2^5 of them, or 2^10, ...: one unit more or less a warp is nothing there.
+constexpr int kCoarser = 5, kCoarsest = 25;  // (2^25 tiles are the longest sequence)
+static_assert((long long)kAttMaxItems * (kItemCost + 1) <= INT_MAX, "the coarsest units fit");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPScale = 32768.f;        // weights are rounded to f16 in units of 2^-15
@@ -149,7 +153,11 @@ MOE_DEV uint32_t chunk_at(uint32_t base, int t, int c) {
 // What a sequence asks for, from the device-side lengths; the same in every
 // CTA.  Lengths out of range count as an empty sequence and are reported.
 struct Seq {
-  int start, n, len, tile0, tiles, groups;  // groups: row groups
+  int start, n, len, tile0, units, groups;  // units of an item; groups: row groups
+  // the first tile past the item's first u units, of 2^sh tiles each
+  template <int kTile>
+  MOE_DEV int tile_at(int u, int sh) const { return min((len + kTile - 1) / kTile, tile0 + (max(0, u - kItemCost) << sh)); }
+  MOE_DEV bool cut() const { return units > kItemCost + kWholeTiles; }
 };
 // As read, through L2: a hint's reads must leave nothing behind in L1.  (And no read-only
 // loads anywhere: the kernel starts while others may still write its inputs.)
@@ -164,7 +172,7 @@ struct Raw {
   MOE_DEV bool operator==(const Raw& o) const { return start == o.start && stop == o.stop && len == o.len; }
 };
 template <int D, int RT>
-MOE_DEV Seq make_seq(const AttArgs& a, const Raw& r, bool report) {
+MOE_DEV Seq make_seq(const AttArgs& a, const Raw& r, int sh, bool report) {
   constexpr int kTile = AttCfg<D, RT>::kTile;
   Seq s;
   bool bad = !step_rows_ok(r.start, r.stop, a.total);
@@ -177,7 +185,7 @@ MOE_DEV Seq make_seq(const AttArgs& a, const Raw& r, bool report) {
   // the first token any row sees (the first row's window), then whole tiles
   const int lo = a.window > 0 ? max(0, s.len - s.n + 1 - a.window) : 0;
   s.tile0 = lo / kTile;
-  s.tiles = max(0, (s.len + kTile - 1) / kTile - s.tile0);
+  s.units = kItemCost + (((s.len + kTile - 1) / kTile - s.tile0 + (1 << sh) - 1) >> sh);
   s.groups = (int)(((long long)s.n * a.G + 8 * RT - 1) / (8 * RT));
   return s;
 }
@@ -192,44 +200,41 @@ struct Walk {
   Seq s;
 };
 // Short items are not cut: the warp whose share holds an item's first unit takes all of it.
-template <int D, int RT>
 MOE_DEV void walk_end(Walk& w) {  // u1 from u0 and left
-  const int units = w.s.tiles + kItemCost;
-  w.u1 = w.s.tiles <= kWholeTiles ? units : min(units, w.u0 + w.left);
+  w.u1 = w.s.cut() ? min(w.s.units, w.u0 + w.left) : w.s.units;
 }
 template <int D, int RT>
-MOE_DEV bool walk_next(Walk& w, const AttArgs& a) {  // to the next piece
+MOE_DEV bool walk_next(Walk& w, const AttArgs& a, int sh) {  // to the next piece
   w.left -= w.u1 - w.u0;
   if (w.left <= 0) return false;
-  w.item0 += w.s.tiles + kItemCost;
+  w.item0 += w.s.units;
   if (++w.grp == w.s.groups) {
     w.grp = 0;
     if (++w.head == a.kv_heads) {
       w.head = 0;
       do {  // (a sequence without rows has no units; one with rows follows, since units are left)
         if (++w.b >= a.B) return false;
-        w.s = make_seq<D, RT>(a, Raw(a, w.b), false);
+        w.s = make_seq<D, RT>(a, Raw(a, w.b), sh, false);
       } while (w.s.groups == 0);
     }
   }
   w.u0 = 0;
-  walk_end<D, RT>(w);
+  walk_end(w);
   return true;
 }
 // The first piece of units x ... x + count, if there is one.
 template <int D, int RT>
-MOE_DEV bool walk_start(Walk& w, const AttArgs& a, int b, const Raw& r, int b_first, int x, int count) {
+MOE_DEV bool walk_start(Walk& w, const AttArgs& a, int b, const Raw& r, int b_first, int x, int count, int sh) {
   w.left = count;
   w.b = b;
-  w.s = make_seq<D, RT>(a, r, false);
-  const int units = w.s.tiles + kItemCost;
-  const int it = (x - b_first) / units;
+  w.s = make_seq<D, RT>(a, r, sh, false);
+  const int it = (x - b_first) / w.s.units;
   w.head = it / max(1, w.s.groups);  // (none: only a hint's lengths that changed)
   w.grp = it - w.head * w.s.groups;
-  w.item0 = b_first + it * units;
+  w.item0 = b_first + it * w.s.units;
   w.u0 = x - w.item0;
-  walk_end<D, RT>(w);
-  return w.u0 == 0 || w.s.tiles > kWholeTiles || walk_next<D, RT>(w, a);
+  walk_end(w);
+  return w.u0 == 0 || w.s.cut() || walk_next<D, RT>(w, a, sh);
 }
 // total * c / G without 64-bit divisions: c, G <= kAttMaxCtas
 MOE_DEV int cta_share(int q, int r, int G, int c) { return q * c + r * c / G; }
@@ -322,15 +327,15 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   // ---- the shares: every thread adds up a run of sequences, then a scan
   __shared__ long long s_scan[kWarps];
   int* s_before = reinterpret_cast<int*>(smem + C::kPartAt);  // [thread]: first unit of its sequences (the pieces come later)
-  int* s_tiles = s_before + kThreads;                          // where it has one sequence: its tiles,
-  Raw* s_raw = reinterpret_cast<Raw*>(s_tiles + kThreads);     // and what was read for it
+  int* s_units = s_before + kThreads;                          // where it has one sequence: an item's units,
+  Raw* s_raw = reinterpret_cast<Raw*>(s_units + kThreads);     // and what was read for it
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   const int P = a.page_size;
   const int box = min(P, kTile);          // token rows of one copy
   const int nbox = kTile / box, gpb = box >> 4;
   long long total = 0;
-  int G = 0, Xq = 0, Xr = 0, X0 = 0, X1 = 0, wb = 0, wat = 0, wx = 0, wn = 0;
+  int sh = 0, G = 0, Xq = 0, Xr = 0, X0 = 0, X1 = 0, wb = 0, wat = 0, wx = 0, wn = 0;
   // Launched while the kernel before may still run.  What it may write is read
   // early all the same, but as a hint: the shares are worked out and the first tiles
   // brought into L2 from it.  After the kernel before is complete the lengths are
@@ -341,12 +346,12 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   if (!hint) grid_dep_wait();
   for (;;) {
     long long mine = 0;
-    int tiles = 0;
+    int units1 = 0;
     Raw seen(a, b0 < a.B ? b0 : 0);
     for (int b = b0; b < b1; ++b) {
-      const Seq s = make_seq<D, RT>(a, per == 1 ? seen : Raw(a, b), blockIdx.x == 0 && !hint);
-      mine += (long long)(s.tiles + kItemCost) * s.groups * a.kv_heads;
-      tiles = s.tiles;
+      const Seq s = make_seq<D, RT>(a, per == 1 ? seen : Raw(a, b), sh, blockIdx.x == 0 && !hint);
+      mine = min(mine + (long long)s.units * s.groups * a.kv_heads, 1ll << 40);  // (too many either way)
+      units1 = s.units;
     }
     long long incl = mine;
 #pragma unroll
@@ -364,8 +369,14 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
       total += s_scan[w];
     }
     const bool fits = total <= INT_MAX;
+    if (!fits && (hint || sh < kCoarsest)) {  // (a hint's lengths say nothing about the units' size)
+      if (hint) grid_dep_wait(); else sh += kCoarser;
+      hint = false;
+      __syncthreads();  // the sums have been read
+      continue;
+    }
     s_before[tid] = mine > 0 && fits ? (int)before : -1;
-    s_tiles[tid] = tiles;
+    s_units[tid] = units1;
     s_raw[tid] = seen;
     __syncthreads();
     // CTAs that get work
@@ -402,12 +413,12 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
         const int src = 31 - __clz(have);  // (unit 0 is somebody's, so there is one)
         const int t = __shfl_sync(0xffffffffu, lane * (kThreads / 32) + best, src);
         wat = s_before[t];
-        int units = s_tiles[t] + kItemCost;
+        int units = s_units[t];
         wr = s_raw[t];
         for (wb = min(a.B, t * per); per > 1; ++wb) {
           wr = Raw(a, wb);
-          const Seq s = make_seq<D, RT>(a, wr, false);
-          units = s.tiles + kItemCost;
+          const Seq s = make_seq<D, RT>(a, wr, sh, false);
+          units = s.units;
           const int nb = units * s.groups * a.kv_heads;
           if (x < wat + nb || wb + 1 >= a.B) break;
           wat += nb;
@@ -421,8 +432,8 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     if (!hint) break;
     if (wn > 0) {
       Walk h;
-      const bool any = walk_start<D, RT>(h, a, wb, wr, wat, wx, wn);
-      const int t0 = h.s.tile0 + max(0, h.u0 - kItemCost), t1 = min(h.s.tile0 + max(0, h.u1 - kItemCost), t0 + kNST);
+      const bool any = walk_start<D, RT>(h, a, wb, wr, wat, wx, wn, sh);
+      const int t0 = h.s.tile_at<kTile>(h.u0, sh), t1 = min(h.s.tile_at<kTile>(h.u1, sh), t0 + kNST);
       const int pos = t0 * kTile + 16 * lane;  // a lane for each 16-token group
       if (any && t0 >= 0 && t0 + lane / kGroups < t1 && lane % gpb == 0 && pos < h.s.len && h.head < a.kv_heads) {
         const int page = __ldcg(a.page_table + (size_t)h.b * a.width + pos / P);
@@ -436,11 +447,12 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     hint = false;
     if (__syncthreads_and(b0 >= a.B || Raw(a, b0) == seen)) {
       // (what the hint did not report)
-      if (b0 < b1 && blockIdx.x == 0) make_seq<D, RT>(a, seen, true);
+      if (b0 < b1 && blockIdx.x == 0) make_seq<D, RT>(a, seen, sh, true);
       break;
     }
   }
-  if (total > INT_MAX && tid == 0) atomicExch(status, MOE_ERR_INVALID_ARG);  // rows counted more than once
+  // (rows that several sequences count as theirs: the host has refused what rows counted once can come to)
+  if (total > INT_MAX && tid == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
   if ((int)blockIdx.x >= G) return;  // (the whole CTA; nothing is in flight)
   __syncthreads();  // s_before has been read
 
@@ -451,7 +463,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   bool alive = true;
   Walk w;
   bool more = wn > 0;
-  if (more) more = walk_start<D, RT>(w, a, wb, wr, wat, wx, wn);
+  if (more) more = walk_start<D, RT>(w, a, wb, wr, wat, wx, wn, sh);
   while (more) {
     const int rows = min(kRowsC, w.s.n * a.G - w.grp * kRowsC);
     const int pos0 = w.s.len - w.s.n;  // position of the step's first token
@@ -459,7 +471,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     const int hi_all = pos0 + 1;
     const int lo_all = a.window > 0 ? max(0, w.s.len - a.window) : 0;
     const int lo_any = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
-    const int t0 = w.s.tile0 + max(0, w.u0 - kItemCost), t1 = w.s.tile0 + max(0, w.u1 - kItemCost);
+    const int t0 = w.s.tile_at<kTile>(w.u0, sh), t1 = w.s.tile_at<kTile>(w.u1, sh);
 
     // ---- Q rows on their way before the cache's stream starts
     uint4 qv[RT][D / 64][2];
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
     if (!alive) break;
 
     // ---- the end of a piece
-    const bool whole = w.u0 == 0 && w.u1 == w.s.tiles + kItemCost;
+    const bool whole = w.u0 == 0 && w.u1 == w.s.units;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 1);
@@ -797,14 +809,14 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
       if (lane == 0) {
         Piece& rec = recs[2 * warp + last];
         rec.item0 = w.item0;
-        rec.units = w.s.tiles + kItemCost;
+        rec.units = w.s.units;
         rec.start = w.s.start;
         rec.row0 = w.grp * kRowsC;
         rec.rows = rows;
         rec.head = w.head;
       }
     }
-    more = walk_next<D, RT>(w, a);
+    more = walk_next<D, RT>(w, a, sh);
   }
   // every copy this warp issued lands before the CTA ends
   for (; used < issued; ++used) mbar_wait_landed(full + used % kNST, (used / kNST) & 1u, status);

@@ -267,6 +267,8 @@ struct AppendArgs {
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
 constexpr int kAttMaxCtas = 160;  // CTAs of the attention kernel at most (one per SM)
+// Items (a sequence's and kv head's groups of rows) of a call at most.
+constexpr int kAttMaxItems = 700000000;
 struct AttArgs {
   const void* q;  // bf16 [total][G * kv_heads][head_dim], token stride in elements
   long long q_stride;

@@ -96,3 +96,19 @@ def test_no_kernel_keeps_its_shared_memory_limit_for_the_process():
         with open(os.path.join(CSRC, name)) as f:
             text = " ".join(f.read().split())
         assert not re.search(r"static[^;]*cudaFuncSetAttribute", text), name
+
+
+def test_attention_of_more_items_than_can_be_counted_is_refused():
+    fake = ctypes.c_void_p(0x10000)
+    L = m.lib()
+
+    def call(B, total, heads, kv_heads):
+        c = att._Cache(0x10000, 0x10000, 0x10000, 0x10000, 8, kv_heads, 64, 64)
+        return L.decode_attention(c, fake, heads * 64, heads, fake, 4, fake, fake, B, total, 1, 0.1, 0.0, 0, None, fake,
+                                  None, None, 0, None)  # (no workspace: refused, where nothing refuses before)
+
+    assert call(1 << 20, 1 << 20, 1024, 1024) == m.MOE_ERR_UNSUPPORTED
+    assert call(700000, 700000, 1024, 1024) == m.MOE_ERR_UNSUPPORTED
+    for ok in ((600000, 600000, 1024, 1024), (1, 1 << 20, 1024, 1024), (1 << 20, 1, 1024, 1024), (4, 93000, 128, 8),
+               (1, 1 << 24, 127, 1)):
+        assert call(*ok) == m.MOE_ERR_INVALID_ARG, ok

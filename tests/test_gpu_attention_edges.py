@@ -195,3 +195,57 @@ def test_windows_beyond_every_length(window):
     got, lse, status = run_attention(b, q, 4, window=window)
     assert status == m.MOE_OK
     check(b, q, got, lse, 0.125)
+
+
+# ---------------------------------------------------------------- work beyond 2^31 units
+def test_more_work_than_a_31_bit_count():
+    """A long chunk behind a long context: 32768 tiles of 32 tokens, 8192 groups of 16
+    rows, 8 heads.  The table names 64 pages over and over, so a few rows are checked
+    against a direct softmax over the pages with their multiplicities."""
+    hk, G, D, page, pages, n, new = 8, 16, 64, 128, 64, 1 << 20, 8192
+    heads = hk * G
+    assert (n // 32 + 2) * (new * G // 16) * hk > 2 ** 31 - 1
+    g = torch.Generator(device=DEV)
+    g.manual_seed(58)
+    cache = [torch.randn((pages, hk, page, D), generator=g, device=DEV).to(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.exp2(torch.randint(-2, 3, (pages, hk), generator=g, device=DEV).float()) for _ in range(2)]
+    table = torch.arange(n // page, device=DEV, dtype=torch.int32).remainder(pages)[None].contiguous()
+    q = torch.randn((new, heads, D), generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.full((new, heads, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((new, heads), float("nan"), device=DEV)
+    ws = workspace(m.decode_attention_workspace_size(heads, hk, D, new))
+    m.decode_attention(q, *cache, *scales, table, dev(np.array([0, new], np.int32)), dev(np.array([n], np.int32)), new,
+                       out, ws, lse=lse)
+    assert m.moe_device_status(ws) == m.MOE_OK
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+    assert int(ws[4:1024].sum()) == 0
+    for i, h in ((0, 0), (1, 127), (4095, 16), (4096, 64), (8000, 77), (8191, 127), (8191, 0)):
+        kv = h // G
+        k, v = ((c[:, kv].float() * s[:, kv, None, None]).double().reshape(-1, D) for c, s in zip(cache, scales))
+        seen = n - new + i + 1
+        times = torch.full((pages * page,), seen // (pages * page), device=DEV, dtype=torch.float64)
+        times[:seen % (pages * page)] += 1
+        s = k @ q[i, h].double() / math.sqrt(D)
+        p = torch.exp(s - s.max()) * times
+        want, mag = p @ v / p.sum(), p @ v.abs() / p.sum()
+        ref = [x.cpu().numpy() for x in (want, s.max() + p.sum().log(), mag,
+                                         torch.stack([(k.abs() @ q[i, h].double().abs()).max(),
+                                                      q[i, h].abs().max().double() * k.abs().sum(1).max()]) / math.sqrt(D))]
+        t_out, t_lse = tolerance(ref, D, n, float(v.abs().max()))
+        assert (np.abs(f64(out[i, h]) - ref[0]) <= t_out).all(), (i, h)
+        assert abs(float(lse[i, h]) - float(ref[1])) <= t_lse, (i, h)
+
+
+def test_rows_that_too_many_sequences_count_as_theirs():
+    """Numbers of rows that no batch can have are reported, and nothing is written."""
+    total, hk, D = 1 << 20, 8, 64
+    cache = m.Fp8KvCache(4, hk, D, 16)
+    start = dev(np.array([0, total] * 3000 + [0], np.int32))
+    lens = torch.zeros(6000, dtype=torch.int32, device=DEV)
+    table = torch.zeros((6000, 1), dtype=torch.int32, device=DEV)
+    q = torch.zeros((total, hk, D), dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(q, 3.0)
+    ws = workspace(m.decode_attention_workspace_size(hk, hk, D, 1 << 20))
+    m.decode_attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, start, lens, 1 << 20, out, ws)
+    assert m.moe_device_status(ws) == m.MOE_ERR_INVALID_ARG
+    assert bool((out == 3.0).all()) and int(ws[4:1024].sum()) == 0
