@@ -428,7 +428,8 @@ int kv_cache_append(const moe_kv_cache *cache, const void *k, long long k_stride
  * Scores, statistics and sums are fp32; the weights are rounded to 11 bits for
  * their product with V.  V scales of one sequence and head may differ by up to
  * 2^29 before weights lose bits.  An infinity or a NaN in a row of q makes the
- * row NaN; a NaN in a new token's v reaches every row of its sequence's step.
+ * row NaN; a NaN in a token's k or v reaches the rows that see the token, and no
+ * other.
  * One kernel; results do not depend on the order in which CTAs finish.
  */
 int decode_attention_workspace_size(int heads, int kv_heads, int head_dim, int max_new, size_t *bytes);

@@ -107,8 +107,12 @@ struct AttCfg {
   static constexpr size_t kRecAt = kPartAt + (size_t)kWarps * kPartF * 4;
   static constexpr size_t kBarsAt = kRecAt + 2 * kWarps * sizeof(Piece);
   static constexpr size_t kMiscAt = kBarsAt + kWarps * kNST * 8;
+  static constexpr size_t kNanAt = kMiscAt + 8;            // a bit for each warp that met a NaN
   static constexpr int kAlign = D == 64 ? 512 : 1024;      // of the swizzle's pattern
   static constexpr size_t kSmem = kAlign + kMiscAt + 16;
+  static MOE_DEV float* part_of(uint8_t* smem, int w, int last) {  // where warp w leaves its first or last piece
+    return reinterpret_cast<float*>(last ? smem + (size_t)w * kNST * kStage : smem + kPartAt + (size_t)w * kPartF * 4);
+  }
   static_assert(kPartF * 4 <= kNST * kStage && kPartF % 4 == 0 && kSmem + kWarps * 8 <= 227 * 1024, "shared memory");
 };
 
@@ -143,11 +147,35 @@ MOE_DEV uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
+// The bytes of w that are NaN codes, as 1 each
+MOE_DEV uint32_t e4m3x4_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u; }
 // 16-byte chunk c of token row t of a tile of D-byte rows, as TMA swizzles it
 template <int D>
 MOE_DEV uint32_t chunk_at(uint32_t base, int t, int c) {
   if constexpr (D == 128) return base + t * 128 + ((c ^ (t & 7)) << 4);
   return base + t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
+}
+
+// A thread's chunk (D / 8 values) of a V row
+template <int D>
+MOE_DEV void load_v(uint32_t* v, uint32_t vt, int row, int fg) {
+  if constexpr (D == 128) {
+    const uint4 x = lds128(chunk_at<D>(vt, row, fg));
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+  } else {
+    const uint2 x = lds64(chunk_at<D>(vt, row, fg >> 1) + 8 * (fg & 1));
+    v[0] = x.x; v[1] = x.y;
+  }
+}
+template <int D>
+MOE_DEV void store_v(const uint32_t* v, uint32_t vt, int row, int fg) {
+  if constexpr (D == 128)
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(chunk_at<D>(vt, row, fg)), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3])
+                 : "memory");
+  else
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(chunk_at<D>(vt, row, fg >> 1) + 8 * (fg & 1)), "r"(v[0]), "r"(v[1])
+                 : "memory");
 }
 
 // What a sequence asks for, from the device-side lengths; the same in every
@@ -222,7 +250,8 @@ MOE_DEV bool walk_next(Walk& w, const AttArgs& a, int sh) {  // to the next piec
   walk_end(w);
   return true;
 }
-// The first piece of units x ... x + count, if there is one.
+// The first piece of units x ... x + count, if there is one: x lies in sequence b, whose
+// units begin with b_first.
 template <int D, int RT>
 MOE_DEV bool walk_start(Walk& w, const AttArgs& a, int b, const Raw& r, int b_first, int x, int count, int sh) {
   w.left = count;
@@ -293,8 +322,467 @@ MOE_DEV void store4(const AttArgs& a, const Piece& p, int r, int D, int d, float
   if (d == 0) at.lse(a, M, L);
 }
 
+// Where a warp's ring stands: tiles copied and consumed so far, and whether no wait gave up.
+struct Ring {
+  uint32_t issued, used;
+  bool alive;
+};
+
+// Every copy a warp issued lands before its CTA ends.
+template <class C>
+MOE_DEV void wait_ring(uint8_t* smem, Ring& st, int* status) {
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt) + (threadIdx.x >> 5) * C::kNST;
+  for (; st.used < st.issued; ++st.used) mbar_wait_landed(full + st.used % C::kNST, (st.used / C::kNST) & 1u, status);
+}
+
+// One piece of an item; kCareful: with the rows that do not see a token kept from the NaN
+// in its V.
+template <int D, int RT, bool MODS, bool kMulti, bool kCareful>
+__device__ __forceinline__ void run_piece(const AttArgs& a, const AttMaps& maps, uint8_t* smem, const Walk& w, int sh,
+                                          Ring& st) {
+  using C = AttCfg<D, RT>;
+  constexpr int kRowsC = C::kRowsC, kTile = C::kTile, kGroups = C::kGroups, kNST = C::kNST;
+  constexpr int kMT = D / 16;  // 16-row tiles of V^T
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, q = lane & 3;
+  const int fg = D == 128 ? ((g & 1) << 2 | g >> 1) : g;  // this thread's chunk of a V row (16 or 8 values)
+  uint8_t* ring = smem + (size_t)warp * kNST * C::kStage;  // this warp's
+  Piece* recs = reinterpret_cast<Piece*>(smem + C::kRecAt);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt) + warp * kNST;
+  int* status = a.status;
+  const int P = a.page_size;
+  const int box = min(P, kTile);  // token rows of one copy
+  const int nbox = kTile / box, gpb = box >> 4;
+  const int rows = min(kRowsC, w.s.n * a.G - w.grp * kRowsC);
+  const int pos0 = w.s.len - w.s.n;  // position of the step's first token
+  // tokens every row sees lie in [lo_all, hi_all), those some row sees in [lo_any, len)
+  const int hi_all = pos0 + 1;
+  const int lo_all = a.window > 0 ? max(0, w.s.len - a.window) : 0;
+  const int lo_any = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
+  const int t0 = w.s.tile_at<kTile>(w.u0, sh), t1 = w.s.tile_at<kTile>(w.u1, sh);
+
+  // ---- Q rows on their way before the cache's stream starts
+  uint4 qv[RT][D / 64][2];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = w.grp * kRowsC + rt * 8 + g;
+    const bool live = rt * 8 + g < rows;
+    const int i = live ? r / a.G : 0, hq = w.head * a.G + (live ? r - i * a.G : 0);
+    const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (long long)(w.s.start + i) * a.q_stride + hq * D;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        qv[rt][h][e] = live ? __ldcg(reinterpret_cast<const uint4*>(qp + 64 * h + 16 * q + 8 * e)) : make_uint4(0, 0, 0, 0);
+  }
+  // ---- pages: lane i looks up 16-token group i of a batch of 32 / kGroups
+  // tiles.  The next batch's page numbers are read as this one begins, its
+  // scales half-way through, so that neither read is waited for.
+  constexpr int kBatch = 32 / kGroups;
+  struct Look { int page; float ks, vs; uint32_t ok; };
+  auto look_page = [&](Look& k, int tb) {
+    const int pos = tb * kTile + 16 * lane;
+    k.page = -2;  // not wanted
+    if (tb + lane / kGroups < t1 && pos < w.s.len && pos + 16 > lo_any)
+      k.page = __ldcg(a.page_table + (size_t)w.b * a.width + pos / P);
+  };
+  auto look_scale = [&](Look& k) {
+    bool ok = k.page >= 0 && k.page < a.num_pages;
+    if (!ok && k.page != -2) atomicExch(status, MOE_ERR_INVALID_ARG);  // its tokens are masked
+    k.ks = k.vs = 0.f;
+    if (ok) {
+      k.ks = __ldcg(a.k_scale + (size_t)k.page * a.kv_heads + w.head);
+      k.vs = __ldcg(a.v_scale + (size_t)k.page * a.kv_heads + w.head);
+    }
+    k.ok = __ballot_sync(0xffffffffu, ok);
+  };
+  Look cur, nxt;
+  look_page(cur, t0);
+  look_scale(cur);
+  int cur0 = t0;  // first tile of cur
+  int ti = t0;    // next tile to copy
+  auto issue = [&]() {
+    const Look& k = ti - cur0 < kBatch ? cur : nxt;
+    const int r = (ti - cur0) % kBatch * kGroups;           // lane of the tile's first group
+    const uint32_t m = (k.ok >> r) & ((1u << kGroups) - 1);
+    const uint32_t bm = (1u << gpb) - 1;
+    const int si = st.issued % kNST;
+    uint8_t* dst = ring + (size_t)si * C::kStage;
+    const int at = ti * kTile % P;  // first row inside the page: 0 unless a page holds several tiles
+    // a box is copied if any of its groups is wanted
+    int copies = 0;
+    for (int i = 0; i < nbox; ++i) copies += ((m >> (i * gpb)) & bm) != 0;
+    const bool one = elect_one();
+    if (one) mbar_expect_tx(full + si, (uint32_t)(2 * copies * box * D));
+    for (int i = 0; i < nbox; ++i) {
+      const uint32_t want = (m >> (i * gpb)) & bm;
+      if (!want) continue;
+      const int pg = __shfl_sync(0xffffffffu, k.page, r + i * gpb + __ffs(want) - 1) * a.kv_heads + w.head;
+      if (one) {
+        tma_load_3d(dst + i * box * D, &maps.k, 0, at, pg, full + si);
+        tma_load_3d(dst + C::kHalfTile + i * box * D, &maps.v, 0, at, pg, full + si);
+      }
+    }
+    ++st.issued;
+    ++ti;
+  };
+  nxt = cur;
+  for (int i = 0; i < kNST && ti < t1; ++i) issue();
+  look_page(nxt, t0 + kBatch);
+
+  // ---- Q fragments: rows g of row tile 0 in a0 / a2, of row tile 1 in a1 / a3.  Step
+  // 4 h + i takes columns 64 h + 16 q + 4 i ... + 3 from lane q: a word of the lane's
+  // 16-byte chunk of K.
+  uint32_t qf[D / 16][2 * RT];
+  float qs[RT];      // 1 / (row's scale), times the softmax scale
+  int pos_r[RT];
+  float slope[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int r = w.grp * kRowsC + rt * 8 + g;
+    const bool live = rt * 8 + g < rows;
+    const int i = live ? r / a.G : 0, hq = w.head * a.G + (live ? r - i * a.G : 0);
+    pos_r[rt] = live ? pos0 + i : -1;
+    slope[rt] = 0.f;
+    if (MODS && a.slopes && live) slope[rt] = __ldcg(a.slopes + hq) * kLog2e;
+    const uint4(&v)[D / 64][2] = qv[rt];
+    float amax = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x[4] = {v[h][e].x, v[h][e].y, v[h][e].z, v[h][e].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float f0 = fabsf(bf16_lo(x[k])), f1 = fabsf(bf16_hi(x[k]));
+          odd |= !(f0 <= 3.4028235e38f) || !(f1 <= 3.4028235e38f);
+          amax = fmaxf(amax, fmaxf(f0, f1));
+        }
+      }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint32_t any_odd = __ballot_sync(0xffffffffu, odd);
+    // scale 2^(14 - exponent): the row's maximum lands in [2^14, 2^15); tiny rows
+    // keep the largest scale a float can be divided by
+    const int ex = max(1, min(253, 268 - (int)(__float_as_uint(amax) >> 23)));
+    const float sc = __uint_as_float((uint32_t)ex << 23);
+    qs[rt] = __uint_as_float((uint32_t)(254 - ex) << 23) * a.sm_scale;
+    if (any_odd & (0xfu << (4 * g))) qs[rt] = __uint_as_float(0x7fc00000u);  // infinities and NaN make the row NaN
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x[4] = {v[h][e].x, v[h][e].y, v[h][e].z, v[h][e].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const __half2 f = __floats2half2_rn(bf16_lo(x[k]) * sc, bf16_hi(x[k]) * sc);
+          qf[4 * h + 2 * e + (k >> 1)][RT * (k & 1) + rt] = *reinterpret_cast<const uint32_t*>(&f);
+        }
+      }
+  }
+  float m[RT], l[RT], o[RT][kMT][4];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY;
+    l[rt] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[rt][mt][i] = 0.f;
+  }
+  float R = kMinUnit;  // largest V scale so far: the accumulators' unit is R 2^-15
+  for (int t = t0; t < t1; ++t) {
+    const int si = st.used % kNST;
+    if (t - cur0 == kBatch) {
+      cur = nxt;
+      cur0 = t;
+      look_page(nxt, t + kBatch);
+    }
+    if (t - cur0 == kBatch / 2) look_scale(nxt);
+    const int r0 = (t - cur0) * kGroups;
+    const int mask = (int)((cur.ok >> r0) & ((1u << kGroups) - 1));
+    float ksg[kGroups], vsg[kGroups];
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      ksg[i] = __shfl_sync(0xffffffffu, cur.ks, r0 + i);
+      vsg[i] = __shfl_sync(0xffffffffu, cur.vs, r0 + i);
+    }
+    const int base = t * kTile;
+    const bool part = mask != (1 << kGroups) - 1 || base + kTile > hi_all || base < lo_all;
+    const uint32_t kt = su32(ring + (size_t)si * C::kStage), vt = kt + C::kHalfTile;
+    if (!mbar_wait_landed(full + si, (st.used / kNST) & 1u, status)) { st.alive = false; break; }
+    ++st.used;
+
+    if constexpr (kCareful) {
+      // NaN codes of V in tokens that some rows see and others do not: rows that see one
+      // become NaN there (where the product of "is NaN" and "sees the token" is not
+      // zero), and the tile holds zeros in their place.
+      if (part) {
+#pragma unroll 1
+        for (int gr = 0; gr < kGroups; ++gr) {
+          uint32_t v4[4][D / 32], sees[RT][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 16 * gr + 4 * i + q, pos = base + row;
+            const bool here = pos < w.s.len && pos >= lo_any && (pos >= hi_all || pos < lo_all) && ((mask >> gr) & 1);
+            uint32_t v[D / 32];
+            load_v<D>(v, vt, row, fg);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              const uint32_t nan = here ? e4m3x4_nan(v[k]) : 0u;
+              v[k] &= ~(nan * 0xffu);
+              v4[i][k] = nan * 0x38u;  // (the code of 1)
+            }
+            store_v<D>(v, vt, row, fg);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              const bool see = pos <= pos_r[rt] && (a.window <= 0 || pos > pos_r[rt] - a.window);
+              const uint32_t one = see ? 0x3c00u << (16 * (i & 1)) : 0u;
+              sees[rt][i >> 1] = (i & 1) ? sees[rt][i >> 1] | one : one;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+            e4m3x4_to_f16x4(__byte_perm(v4[0][k], v4[1][k], 0x5140), a0, a1);
+            e4m3x4_to_f16x4(__byte_perm(v4[2][k], v4[3][k], 0x5140), a2, a3);
+            e4m3x4_to_f16x4(__byte_perm(v4[0][k], v4[1][k], 0x7362), b0, b1);
+            e4m3x4_to_f16x4(__byte_perm(v4[2][k], v4[3][k], 0x7362), b2, b3);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(c, a0, a1, a2, a3, sees[rt][0], sees[rt][1]);
+              mma_f16(d, b0, b1, b2, b3, sees[rt][0], sees[rt][1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (c[i] > 0.f) o[rt][2 * k][i] = NAN;
+                if (d[i] > 0.f) o[rt][2 * k + 1][i] = NAN;
+              }
+            }
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (a copy will take the stage)
+        __syncwarp();
+      }
+    }
+
+    // ---- scores: s[rt][2 j + i] is row g, token 16 (j / 2) + 8 (j % 2) + 4 i + q
+    float s[RT][2 * kTile / 8];
+#pragma unroll
+    for (int j = 0; j < kTile / 8; ++j) {
+      const int row = 8 * j + 4 * (g & 1) + (g >> 1);
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        const uint4 kv = lds128(chunk_at<D>(kt, row, 4 * h + q));
+        const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t(&f)[2 * RT] = qf[4 * h + i];
+          uint32_t b0, b1;
+          e4m3x4_to_f16x4(kw[i], b0, b1);
+          mma_f16(c, f[0], RT == 2 ? f[1] : 0u, f[RT], RT == 2 ? f[2 * RT - 1] : 0u, b0, b1);
+        }
+      }
+      const float ks = ksg[j >> 1];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float f = qs[rt] * ks * (MODS ? 1.f : kLog2e);
+        s[rt][2 * j] = c[2 * rt] * f;
+        s[rt][2 * j + 1] = c[2 * rt + 1] * f;
+      }
+    }
+    if (MODS) {
+      const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int k = 0; k < kTile / 4; ++k) {
+          float x = s[rt][k];
+          if (a.softcap > 0.f) x = a.softcap * tanh_of(x * cap_in);
+          const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
+          s[rt][k] = fmaf(slope[rt], (float)(pos - pos_r[rt]), x * kLog2e);
+        }
+    }
+    if (part) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int k = 0; k < kTile / 4; ++k) {
+          const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
+          const bool see = pos <= pos_r[rt] && (a.window <= 0 || pos > pos_r[rt] - a.window) && ((mask >> (k >> 2)) & 1);
+          if (!see) s[rt][k] = -INFINITY;
+        }
+    }
+    // ---- running maximum and sum
+    float Rn = R;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) Rn = fmaxf(Rn, vsg[i]);  // (0 where a group was not read)
+    const float Rq = __fdividef(1.f, Rn);
+    const float rr = Rn == R ? 1.f : __fdividef(R, Rn);
+    float al[RT];
+    bool turn = Rn != R;
+    uint32_t pb[RT][kTile / 8];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float mx = s[rt][0];
+#pragma unroll
+      for (int k = 1; k < kTile / 4; ++k) mx = fmaxf(mx, s[rt][k]);
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[rt], mx);
+      const float ms = mn == -INFINITY ? 0.f : mn;
+      al[rt] = ex2(m[rt] - ms);
+      turn |= mn > m[rt];
+      m[rt] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < kTile / 8; ++j) {
+        const float F = vsg[j >> 1] * Rq * kPScale;
+        const float p0 = ex2(s[rt][2 * j] - ms), p1 = ex2(s[rt][2 * j + 1] - ms);
+        sum += p0 + p1;
+        // masked tokens of a group that was not loaded: vs is 0, p is 0
+        const __half2 h2 = __floats2half2_rn(p0 * F, p1 * F);
+        pb[rt][j] = *reinterpret_cast<const uint32_t*>(&h2);
+      }
+      l[rt] = l[rt] * al[rt] + sum;
+    }
+    if (__any_sync(0xffffffffu, turn)) {
+      R = Rn;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float f = al[rt] * rr;  // of row g; the accumulator's columns are rows 2 q and 2 q + 1
+        const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          o[rt][mt][0] *= f0; o[rt][mt][2] *= f0;
+          o[rt][mt][1] *= f1; o[rt][mt][3] *= f1;
+        }
+      }
+    }
+    // ---- O^T += V^T P^T, 16 tokens at a time
+#pragma unroll
+    for (int gr = 0; gr < kGroups; ++gr) {
+      uint32_t v4[4][D / 32];  // tokens q, 4 + q, 8 + q, 12 + q of the group, this thread's chunk
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * gr + 4 * i + q;
+        load_v<D>(v4[i], vt, row, fg);
+        if (part) {
+          // tokens no row sees may hold anything (an old page's codes, NaN)
+          const int pos = base + row;
+          if (pos >= w.s.len || pos < lo_any || !((mask >> gr) & 1)) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) v4[i][k] = 0;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+        e4m3x4_to_f16x4(__byte_perm(v4[0][k], v4[1][k], 0x5140), a0, a1);
+        e4m3x4_to_f16x4(__byte_perm(v4[2][k], v4[3][k], 0x5140), a2, a3);
+        e4m3x4_to_f16x4(__byte_perm(v4[0][k], v4[1][k], 0x7362), b0, b1);
+        e4m3x4_to_f16x4(__byte_perm(v4[2][k], v4[3][k], 0x7362), b2, b3);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          mma_f16(o[rt][2 * k], a0, a1, a2, a3, pb[rt][2 * gr], pb[rt][2 * gr + 1]);
+          mma_f16(o[rt][2 * k + 1], b0, b1, b2, b3, pb[rt][2 * gr], pb[rt][2 * gr + 1]);
+        }
+      }
+    }
+    __syncwarp();  // the stage has been read
+    if (ti < t1) issue();
+  }
+  if (!st.alive) return;
+
+  // A NaN in V reaches every row of the tile's products (as a NaN times a weight of zero
+  // where a row does not see its token), so one row of each thread shows it.
+  if (kMulti && !kCareful) {
+    bool nan = false;
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) nan |= o[0][mt][0] != o[0][mt][0] || o[0][mt][2] != o[0][mt][2];
+    if (nan) atomicOr(reinterpret_cast<uint32_t*>(smem + C::kNanAt), 1u << warp);
+  }
+
+  // ---- the end of a piece
+  const bool whole = w.u0 == 0 && w.u1 == w.s.units;
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 1);
+    l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 2);
+  }
+  // (R and 2^-15 one after the other: their product may be no normal number)
+  if (whole) {
+    // columns 2 q and 2 q + 1 of the accumulator are rows; this thread has
+    // D / 8 consecutive values of each from fg * D / 8
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = rt * 8 + 2 * q + c;
+        const float L = __shfl_sync(0xffffffffu, l[rt], 8 * q + 4 * c);
+        const float M = __shfl_sync(0xffffffffu, m[rt], 8 * q + 4 * c);
+        if (r < rows) {
+          const float inv = L == 0.f ? 0.f : __fdividef(1.f / kPScale, L);
+          const OutRow o_at(a, w.s.start, w.grp * kRowsC + r, w.head);
+          uint32_t v[kMT];
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt) v[mt] = pack_bf16(o[rt][mt][c] * inv * R, o[rt][mt][2 + c] * inv * R);
+          uint4* dst = reinterpret_cast<uint4*>(o_at.out(a, D) + fg * (D / 8));
+#pragma unroll
+          for (int k = 0; k < kMT / 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          if (g == 0) o_at.lse(a, M, L);
+        }
+      }
+  } else {
+    const int last = w.u0 == 0 ? 1 : 0;  // (a warp's piece that starts an item and does not end it is its last)
+    float* p = C::part_of(smem, warp, last);
+    auto unit = [&](float x) { return x * (1.f / kPScale) * R; };
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int mt = 0; mt < kMT; mt += 2)
+          *reinterpret_cast<float4*>(p + (rt * 8 + 2 * q + c) * D + fg * (D / 8) + 2 * mt) =
+              make_float4(unit(o[rt][mt][c]), unit(o[rt][mt][2 + c]), unit(o[rt][mt + 1][c]), unit(o[rt][mt + 1][2 + c]));
+      if (q == 0) *reinterpret_cast<float2*>(p + kRowsC * D + 2 * (rt * 8 + g)) = make_float2(m[rt], l[rt]);
+    }
+    if (lane == 0) {
+      Piece& rec = recs[2 * warp + last];
+      rec.item0 = w.item0;
+      rec.units = w.s.units;
+      rec.start = w.s.start;
+      rec.row0 = w.grp * kRowsC;
+      rec.rows = rows;
+      rec.head = w.head;
+    }
+  }
+}
+
+// A warp's pieces once more, with care: where V holds a NaN that a mask hides from some
+// rows.  That hardly ever is, so the ordinary loop only notes that it met a NaN, and this
+// stands out of line.  (A prompt of 2048 tokens behind 2048, us: NaN masked in the loop
+// 1500, within the kernel 1170 to 1200, so 1159; none of it 1167.)
 template <int D, int RT, bool MODS>
-__global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel(AttArgs a, const __grid_constant__ AttMaps maps) {
+__device__ __noinline__ void careful_walk(const AttArgs& a, const AttMaps& maps, uint8_t* smem, int b, int b_first, int x,
+                                          int count, int sh, uint32_t done) {
+  using C = AttCfg<D, RT>;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a piece's sums lie where copies go now
+  __syncwarp();
+  Ring st{done, done, true};
+  Walk w;
+  for (bool more = walk_start<D, RT>(w, a, b, Raw(a, b), b_first, x, count, sh); more && st.alive;
+       more = walk_next<D, RT>(w, a, sh))
+    run_piece<D, RT, MODS, true, true>(a, maps, smem, w, sh, st);
+  wait_ring<C>(smem, st, a.status);
+}
+
+template <int D, int RT, bool MODS, bool kMulti>
+__global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1)
+    attention_kernel(const __grid_constant__ AttArgs a, const __grid_constant__ AttMaps maps) {
   using C = AttCfg<D, RT>;
   constexpr int kRowsC = C::kRowsC, kTile = C::kTile, kGroups = C::kGroups, kNST = C::kNST;
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
@@ -307,35 +795,36 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((C::kAlign - (su32(smem_raw) & (C::kAlign - 1))) & (C::kAlign - 1));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t* ring = smem + (size_t)warp * kNST * C::kStage;                      // this warp's
   Piece* recs = reinterpret_cast<Piece*>(smem + C::kRecAt);                     // [warp][first, last]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarsAt) + warp * kNST;
   int* s_last = reinterpret_cast<int*>(smem + C::kMiscAt);                       // [2] last CTA to arrive, by piece
   int* status = a.status;
-  auto part_of = [&](int w, int last) {  // where warp w leaves its first or last piece
-    return reinterpret_cast<float*>(last ? smem + (size_t)w * kNST * C::kStage
-                                         : smem + C::kPartAt + (size_t)w * C::kPartF * 4);
-  };
+  auto part_of = [&](int w, int last) { return C::part_of(smem, w, last); };
 
   if (lane == 0) {
     for (int i = 0; i < kNST; ++i) mbar_init(full + i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     recs[2 * warp].item0 = recs[2 * warp + 1].item0 = -1;
+    if (kMulti && warp == 0) *reinterpret_cast<uint32_t*>(smem + C::kNanAt) = 0;
   }
 
   grid_dep_launch();
   // ---- the shares: every thread adds up a run of sequences, then a scan
   __shared__ long long s_scan[kWarps];
+  int2* s_from = reinterpret_cast<int2*>(s_scan);  // (afterwards) a warp's first sequence and its first unit
   int* s_before = reinterpret_cast<int*>(smem + C::kPartAt);  // [thread]: first unit of its sequences (the pieces come later)
   int* s_units = s_before + kThreads;                          // where it has one sequence: an item's units,
   Raw* s_raw = reinterpret_cast<Raw*>(s_units + kThreads);     // and what was read for it
   const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   const int P = a.page_size;
-  const int box = min(P, kTile);          // token rows of one copy
-  const int nbox = kTile / box, gpb = box >> 4;
+  const int gpb = min(P, kTile) >> 4;     // 16-token groups of one copy
   long long total = 0;
   int sh = 0, G = 0, Xq = 0, Xr = 0, X0 = 0, X1 = 0, wb = 0, wat = 0, wx = 0, wn = 0;
+  auto warp_share = [&](int w) {  // X0 + (X1 - X0) * w / kWarps
+    const int n = X1 - X0;
+    return X0 + n / kWarps * w + n % kWarps * w / kWarps;
+  };
   // Launched while the kernel before may still run.  What it may write is read
   // early all the same, but as a hint: the shares are worked out and the first tiles
   // brought into L2 from it.  After the kernel before is complete the lengths are
@@ -394,10 +883,8 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
 #pragma unroll 1
       for (int step = Xq < kCtaUnits ? 0 : 2; step < 3; ++step) {
         if (step == 2) {
-          const int n = X1 - X0;
-          auto share = [&](int w) { return X0 + n / kWarps * w + n % kWarps * w / kWarps; };  // X0 + n * w / kWarps
-          wx = share(warp);
-          wn = share(warp + 1) - wx;
+          wx = warp_share(warp);
+          wn = warp_share(warp + 1) - wx;
         }
         const int x = step == 0 ? X0 : step == 1 ? X1 : wx;
         if (x >= (int)total) continue;
@@ -456,370 +943,21 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1) attention_kernel
   if ((int)blockIdx.x >= G) return;  // (the whole CTA; nothing is in flight)
   __syncthreads();  // s_before has been read
 
-  const int g = lane >> 2, q = lane & 3;
-  const int fg = D == 128 ? ((g & 1) << 2 | g >> 1) : g;   // this thread's chunk of a V row (16 or 8 values)
-  constexpr int kMT = D / 16;                              // 16-row tiles of V^T
-  uint32_t issued = 0, used = 0;          // tiles copied and consumed so far (ring position and phase)
-  bool alive = true;
-  Walk w;
-  bool more = wn > 0;
-  if (more) more = walk_start<D, RT>(w, a, wb, wr, wat, wx, wn, sh);
-  while (more) {
-    const int rows = min(kRowsC, w.s.n * a.G - w.grp * kRowsC);
-    const int pos0 = w.s.len - w.s.n;  // position of the step's first token
-    // tokens every row sees lie in [lo_all, hi_all), those some row sees in [lo_any, len)
-    const int hi_all = pos0 + 1;
-    const int lo_all = a.window > 0 ? max(0, w.s.len - a.window) : 0;
-    const int lo_any = a.window > 0 ? max(0, pos0 + 1 - a.window) : 0;
-    const int t0 = w.s.tile_at<kTile>(w.u0, sh), t1 = w.s.tile_at<kTile>(w.u1, sh);
-
-    // ---- Q rows on their way before the cache's stream starts
-    uint4 qv[RT][D / 64][2];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = w.grp * kRowsC + rt * 8 + g;
-      const bool live = rt * 8 + g < rows;
-      const int i = live ? r / a.G : 0, hq = w.head * a.G + (live ? r - i * a.G : 0);
-      const uint16_t* qp = reinterpret_cast<const uint16_t*>(a.q) + (long long)(w.s.start + i) * a.q_stride + hq * D;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          qv[rt][h][e] = live ? __ldcg(reinterpret_cast<const uint4*>(qp + 64 * h + 16 * q + 8 * e)) : make_uint4(0, 0, 0, 0);
-    }
-    // ---- pages: lane i looks up 16-token group i of a batch of 32 / kGroups
-    // tiles.  The next batch's page numbers are read as this one begins, its
-    // scales half-way through, so that neither read is waited for.
-    constexpr int kBatch = 32 / kGroups;
-    struct Look { int page; float ks, vs; uint32_t ok; };
-    auto look_page = [&](Look& k, int tb) {
-      const int pos = tb * kTile + 16 * lane;
-      k.page = -2;  // not wanted
-      if (tb + lane / kGroups < t1 && pos < w.s.len && pos + 16 > lo_any)
-        k.page = __ldcg(a.page_table + (size_t)w.b * a.width + pos / P);
-    };
-    auto look_scale = [&](Look& k) {
-      bool ok = k.page >= 0 && k.page < a.num_pages;
-      if (!ok && k.page != -2) atomicExch(status, MOE_ERR_INVALID_ARG);  // its tokens are masked
-      k.ks = k.vs = 0.f;
-      if (ok) {
-        k.ks = __ldcg(a.k_scale + (size_t)k.page * a.kv_heads + w.head);
-        k.vs = __ldcg(a.v_scale + (size_t)k.page * a.kv_heads + w.head);
-      }
-      k.ok = __ballot_sync(0xffffffffu, ok);
-    };
-    Look cur, nxt;
-    look_page(cur, t0);
-    look_scale(cur);
-    int cur0 = t0;  // first tile of cur
-    int ti = t0;    // next tile to copy
-    auto issue = [&]() {
-      const Look& k = ti - cur0 < kBatch ? cur : nxt;
-      const int r = (ti - cur0) % kBatch * kGroups;           // lane of the tile's first group
-      const uint32_t m = (k.ok >> r) & ((1u << kGroups) - 1);
-      const uint32_t bm = (1u << gpb) - 1;
-      const int si = issued % kNST;
-      uint8_t* dst = ring + (size_t)si * C::kStage;
-      const int at = ti * kTile % P;  // first row inside the page: 0 unless a page holds several tiles
-      // a box is copied if any of its groups is wanted
-      int copies = 0;
-      for (int i = 0; i < nbox; ++i) copies += ((m >> (i * gpb)) & bm) != 0;
-      const bool one = elect_one();
-      if (one) mbar_expect_tx(full + si, (uint32_t)(2 * copies * box * D));
-      for (int i = 0; i < nbox; ++i) {
-        const uint32_t want = (m >> (i * gpb)) & bm;
-        if (!want) continue;
-        const int pg = __shfl_sync(0xffffffffu, k.page, r + i * gpb + __ffs(want) - 1) * a.kv_heads + w.head;
-        if (one) {
-          tma_load_3d(dst + i * box * D, &maps.k, 0, at, pg, full + si);
-          tma_load_3d(dst + C::kHalfTile + i * box * D, &maps.v, 0, at, pg, full + si);
-        }
-      }
-      ++issued;
-      ++ti;
-    };
-    nxt = cur;
-    for (int i = 0; i < kNST && ti < t1; ++i) issue();
-    look_page(nxt, t0 + kBatch);
-
-    // ---- Q fragments: rows g of row tile 0 in a0 / a2, of row tile 1 in a1 / a3.  Step
-    // 4 h + i takes columns 64 h + 16 q + 4 i ... + 3 from lane q: a word of the lane's
-    // 16-byte chunk of K.
-    uint32_t qf[D / 16][2 * RT];
-    float qs[RT];      // 1 / (row's scale), times the softmax scale
-    int pos_r[RT];
-    float slope[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int r = w.grp * kRowsC + rt * 8 + g;
-      const bool live = rt * 8 + g < rows;
-      const int i = live ? r / a.G : 0, hq = w.head * a.G + (live ? r - i * a.G : 0);
-      pos_r[rt] = live ? pos0 + i : -1;
-      slope[rt] = 0.f;
-      if (MODS && a.slopes && live) slope[rt] = __ldcg(a.slopes + hq) * kLog2e;
-      const uint4(&v)[D / 64][2] = qv[rt];
-      float amax = 0.f;
-      bool odd = false;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t x[4] = {v[h][e].x, v[h][e].y, v[h][e].z, v[h][e].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float f0 = fabsf(bf16_lo(x[k])), f1 = fabsf(bf16_hi(x[k]));
-            odd |= !(f0 <= 3.4028235e38f) || !(f1 <= 3.4028235e38f);
-            amax = fmaxf(amax, fmaxf(f0, f1));
-          }
-        }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const uint32_t any_odd = __ballot_sync(0xffffffffu, odd);
-      // scale 2^(14 - exponent): the row's maximum lands in [2^14, 2^15); tiny rows
-      // keep the largest scale a float can be divided by
-      const int ex = max(1, min(253, 268 - (int)(__float_as_uint(amax) >> 23)));
-      const float sc = __uint_as_float((uint32_t)ex << 23);
-      qs[rt] = __uint_as_float((uint32_t)(254 - ex) << 23) * a.sm_scale;
-      if (any_odd & (0xfu << (4 * g))) qs[rt] = __uint_as_float(0x7fc00000u);  // infinities and NaN make the row NaN
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t x[4] = {v[h][e].x, v[h][e].y, v[h][e].z, v[h][e].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 f = __floats2half2_rn(bf16_lo(x[k]) * sc, bf16_hi(x[k]) * sc);
-            qf[4 * h + 2 * e + (k >> 1)][RT * (k & 1) + rt] = *reinterpret_cast<const uint32_t*>(&f);
-          }
-        }
-    }
-    float m[RT], l[RT], o[RT][kMT][4];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      m[rt] = -INFINITY;
-      l[rt] = 0.f;
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[rt][mt][i] = 0.f;
-    }
-    float R = kMinUnit;  // largest V scale so far: the accumulators' unit is R 2^-15
-    for (int t = t0; t < t1; ++t) {
-      const int si = used % kNST;
-      if (t - cur0 == kBatch) {
-        cur = nxt;
-        cur0 = t;
-        look_page(nxt, t + kBatch);
-      }
-      if (t - cur0 == kBatch / 2) look_scale(nxt);
-      const int r0 = (t - cur0) * kGroups;
-      const int mask = (int)((cur.ok >> r0) & ((1u << kGroups) - 1));
-      float ksg[kGroups], vsg[kGroups];
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        ksg[i] = __shfl_sync(0xffffffffu, cur.ks, r0 + i);
-        vsg[i] = __shfl_sync(0xffffffffu, cur.vs, r0 + i);
-      }
-      const int base = t * kTile;
-      const bool part = mask != (1 << kGroups) - 1 || base + kTile > hi_all || base < lo_all;
-      const uint32_t kt = su32(ring + (size_t)si * C::kStage), vt = kt + C::kHalfTile;
-      if (!mbar_wait_landed(full + si, (used / kNST) & 1u, status)) { alive = false; break; }
-      ++used;
-
-      // ---- scores: s[rt][2 j + i] is row g, token 16 (j / 2) + 8 (j % 2) + 4 i + q
-      float s[RT][2 * kTile / 8];
-#pragma unroll
-      for (int j = 0; j < kTile / 8; ++j) {
-        const int row = 8 * j + 4 * (g & 1) + (g >> 1);
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          const uint4 kv = lds128(chunk_at<D>(kt, row, 4 * h + q));
-          const uint32_t kw[4] = {kv.x, kv.y, kv.z, kv.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t(&f)[2 * RT] = qf[4 * h + i];
-            uint32_t b0, b1;
-            e4m3x4_to_f16x4(kw[i], b0, b1);
-            mma_f16(c, f[0], RT == 2 ? f[1] : 0u, f[RT], RT == 2 ? f[2 * RT - 1] : 0u, b0, b1);
-          }
-        }
-        const float ks = ksg[j >> 1];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const float f = qs[rt] * ks * (MODS ? 1.f : kLog2e);
-          s[rt][2 * j] = c[2 * rt] * f;
-          s[rt][2 * j + 1] = c[2 * rt + 1] * f;
-        }
-      }
-      if (MODS) {
-        const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int k = 0; k < kTile / 4; ++k) {
-            float x = s[rt][k];
-            if (a.softcap > 0.f) x = a.softcap * tanh_of(x * cap_in);
-            const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
-            s[rt][k] = fmaf(slope[rt], (float)(pos - pos_r[rt]), x * kLog2e);
-          }
-      }
-      if (part) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int k = 0; k < kTile / 4; ++k) {
-            const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
-            const bool see = pos <= pos_r[rt] && (a.window <= 0 || pos > pos_r[rt] - a.window) && ((mask >> (k >> 2)) & 1);
-            if (!see) s[rt][k] = -INFINITY;
-          }
-      }
-      // ---- running maximum and sum
-      float Rn = R;
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) Rn = fmaxf(Rn, vsg[i]);  // (0 where a group was not read)
-      const float Rq = __fdividef(1.f, Rn);
-      const float rr = Rn == R ? 1.f : __fdividef(R, Rn);
-      float al[RT];
-      bool turn = Rn != R;
-      uint32_t pb[RT][kTile / 8];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float mx = s[rt][0];
-#pragma unroll
-        for (int k = 1; k < kTile / 4; ++k) mx = fmaxf(mx, s[rt][k]);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[rt], mx);
-        const float ms = mn == -INFINITY ? 0.f : mn;
-        al[rt] = ex2(m[rt] - ms);
-        turn |= mn > m[rt];
-        m[rt] = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < kTile / 8; ++j) {
-          const float F = vsg[j >> 1] * Rq * kPScale;
-          const float p0 = ex2(s[rt][2 * j] - ms), p1 = ex2(s[rt][2 * j + 1] - ms);
-          sum += p0 + p1;
-          // masked tokens of a group that was not loaded: vs is 0, p is 0
-          const __half2 h2 = __floats2half2_rn(p0 * F, p1 * F);
-          pb[rt][j] = *reinterpret_cast<const uint32_t*>(&h2);
-        }
-        l[rt] = l[rt] * al[rt] + sum;
-      }
-      if (__any_sync(0xffffffffu, turn)) {
-        R = Rn;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const float f = al[rt] * rr;  // of row g; the accumulator's columns are rows 2 q and 2 q + 1
-          const float f0 = __shfl_sync(0xffffffffu, f, 8 * q), f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            o[rt][mt][0] *= f0; o[rt][mt][2] *= f0;
-            o[rt][mt][1] *= f1; o[rt][mt][3] *= f1;
-          }
-        }
-      }
-      // ---- O^T += V^T P^T, 16 tokens at a time
-#pragma unroll
-      for (int gr = 0; gr < kGroups; ++gr) {
-        uint32_t v4[4][D / 32];  // tokens q, 4 + q, 8 + q, 12 + q of the group, this thread's chunk
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 16 * gr + 4 * i + q;
-          if constexpr (D == 128) {
-            const uint4 x = lds128(chunk_at<D>(vt, row, fg));
-            v4[i][0] = x.x; v4[i][1] = x.y; v4[i][2] = x.z; v4[i][3] = x.w;
-          } else {
-            const uint2 x = lds64(chunk_at<D>(vt, row, fg >> 1) + 8 * (fg & 1));
-            v4[i][0] = x.x; v4[i][1] = x.y;
-          }
-          if (part) {
-            // tokens no row sees may hold anything (an old page's codes, NaN)
-            const int pos = base + row;
-            if (pos >= w.s.len || pos < lo_any || !((mask >> gr) & 1)) {
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k) v4[i][k] = 0;
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          e4m3x4_to_f16x4(__byte_perm(v4[0][k], v4[1][k], 0x5140), a0, a1);
-          e4m3x4_to_f16x4(__byte_perm(v4[2][k], v4[3][k], 0x5140), a2, a3);
-          e4m3x4_to_f16x4(__byte_perm(v4[0][k], v4[1][k], 0x7362), b0, b1);
-          e4m3x4_to_f16x4(__byte_perm(v4[2][k], v4[3][k], 0x7362), b2, b3);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            mma_f16(o[rt][2 * k], a0, a1, a2, a3, pb[rt][2 * gr], pb[rt][2 * gr + 1]);
-            mma_f16(o[rt][2 * k + 1], b0, b1, b2, b3, pb[rt][2 * gr], pb[rt][2 * gr + 1]);
-          }
-        }
-      }
-      __syncwarp();  // the stage has been read
-      if (ti < t1) issue();
-    }
-    if (!alive) break;
-
-    // ---- the end of a piece
-    const bool whole = w.u0 == 0 && w.u1 == w.s.units;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 1);
-      l[rt] += __shfl_xor_sync(0xffffffffu, l[rt], 2);
-    }
-    // (R and 2^-15 one after the other: their product may be no normal number)
-    if (whole) {
-      // columns 2 q and 2 q + 1 of the accumulator are rows; this thread has
-      // D / 8 consecutive values of each from fg * D / 8
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int r = rt * 8 + 2 * q + c;
-          const float L = __shfl_sync(0xffffffffu, l[rt], 8 * q + 4 * c);
-          const float M = __shfl_sync(0xffffffffu, m[rt], 8 * q + 4 * c);
-          if (r < rows) {
-            const float inv = L == 0.f ? 0.f : __fdividef(1.f / kPScale, L);
-            const OutRow o_at(a, w.s.start, w.grp * kRowsC + r, w.head);
-            uint32_t v[kMT];
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) v[mt] = pack_bf16(o[rt][mt][c] * inv * R, o[rt][mt][2 + c] * inv * R);
-            uint4* dst = reinterpret_cast<uint4*>(o_at.out(a, D) + fg * (D / 8));
-#pragma unroll
-            for (int k = 0; k < kMT / 4; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-            if (g == 0) o_at.lse(a, M, L);
-          }
-        }
-    } else {
-      const int last = w.u0 == 0 ? 1 : 0;  // (a warp's piece that starts an item and does not end it is its last)
-      float* p = part_of(warp, last);
-      auto unit = [&](float x) { return x * (1.f / kPScale) * R; };
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int mt = 0; mt < kMT; mt += 2)
-            *reinterpret_cast<float4*>(p + (rt * 8 + 2 * q + c) * D + fg * (D / 8) + 2 * mt) =
-                make_float4(unit(o[rt][mt][c]), unit(o[rt][mt][2 + c]), unit(o[rt][mt + 1][c]), unit(o[rt][mt + 1][2 + c]));
-        if (q == 0) *reinterpret_cast<float2*>(p + kRowsC * D + 2 * (rt * 8 + g)) = make_float2(m[rt], l[rt]);
-      }
-      if (lane == 0) {
-        Piece& rec = recs[2 * warp + last];
-        rec.item0 = w.item0;
-        rec.units = w.s.units;
-        rec.start = w.s.start;
-        rec.row0 = w.grp * kRowsC;
-        rec.rows = rows;
-        rec.head = w.head;
-      }
-    }
-    more = walk_next<D, RT>(w, a, sh);
+  Ring st{0, 0, true};
+  if (wn > 0) {
+    // (for careful_walk, instead of registers through the loop)
+    if (kMulti && lane == 0) s_from[warp] = make_int2(wb, wat);
+    Walk w;
+    for (bool more = walk_start<D, RT>(w, a, wb, wr, wat, wx, wn, sh); more && st.alive; more = walk_next<D, RT>(w, a, sh))
+      run_piece<D, RT, MODS, kMulti, false>(a, maps, smem, w, sh, st);
   }
-  // every copy this warp issued lands before the CTA ends
-  for (; used < issued; ++used) mbar_wait_landed(full + used % kNST, (used / kNST) & 1u, status);
+  wait_ring<C>(smem, st, status);
+  __syncwarp();
+  if (kMulti && (*reinterpret_cast<volatile uint32_t*>(smem + C::kNanAt) >> warp & 1) && st.alive) {
+    const int2 from = s_from[warp];
+    const int x = warp_share(warp);
+    careful_walk<D, RT, MODS>(a, maps, smem, from.x, from.y, x, warp_share(warp + 1) - x, sh, st.used);
+  }
   __syncthreads();
 
   // ---- the CTA's pieces: those of one item are added, in order.  Every warp
@@ -971,21 +1109,30 @@ bool map_cache(CUtensorMap* m, const uint8_t* base, int D, int P, long long tile
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int RT, bool MODS>
+template <int D, int RT, bool MODS, bool kMulti>
 cudaError_t launch_cfg(const AttArgs& a, const AttMaps& maps, int ctas, cudaStream_t s) {
   using C = AttCfg<D, RT>;
   static OncePerDevice once;
-  if (const cudaError_t rc = allow_smem(once, attention_kernel<D, RT, MODS>, C::kSmem); rc != cudaSuccess) return rc;
+  constexpr auto kernel = attention_kernel<D, RT, MODS, kMulti>;
+  if (const cudaError_t rc = allow_smem(once, kernel, C::kSmem); rc != cudaSuccess) return rc;
   PdlLaunch L(dim3(ctas), dim3(C::kThreads), C::kSmem, s);
-  return cudaLaunchKernelEx(&L.cfg, attention_kernel<D, RT, MODS>, a, maps);
+  return cudaLaunchKernelEx(&L.cfg, kernel, a, maps);
+}
+
+// Only calls with several new tokens a sequence have rows that see different tokens.  (Single
+// tokens with what those need, us: 9 sequences of 3 to 17 tokens, 96 heads of 64 on 8,
+// 6.8 for 5.9; one of 777 tokens, 56 heads of 128 on 8, 9.1 for 9.0.)
+template <int D, int RT, bool MODS>
+cudaError_t launch_mods(const AttArgs& a, const AttMaps& maps, int ctas, cudaStream_t s) {
+  return a.max_new > 1 ? launch_cfg<D, RT, MODS, true>(a, maps, ctas, s) : launch_cfg<D, RT, MODS, false>(a, maps, ctas, s);
 }
 
 template <int D>
 cudaError_t launch_d(const AttArgs& a, const AttMaps& maps, int ctas, cudaStream_t s) {
   const bool mods = a.softcap > 0.f || a.slopes;
   if (attention_row_tiles(a.G, a.max_new) == 1)
-    return mods ? launch_cfg<D, 1, true>(a, maps, ctas, s) : launch_cfg<D, 1, false>(a, maps, ctas, s);
-  return mods ? launch_cfg<D, 2, true>(a, maps, ctas, s) : launch_cfg<D, 2, false>(a, maps, ctas, s);
+    return mods ? launch_mods<D, 1, true>(a, maps, ctas, s) : launch_mods<D, 1, false>(a, maps, ctas, s);
+  return mods ? launch_mods<D, 2, true>(a, maps, ctas, s) : launch_mods<D, 2, false>(a, maps, ctas, s);
 }
 
 }  // namespace

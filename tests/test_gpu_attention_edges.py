@@ -249,3 +249,31 @@ def test_rows_that_too_many_sequences_count_as_theirs():
     m.decode_attention(q, cache.k, cache.v, cache.k_scale, cache.v_scale, table, start, lens, 1 << 20, out, ws)
     assert m.moe_device_status(ws) == m.MOE_ERR_INVALID_ARG
     assert bool((out == 3.0).all()) and int(ws[4:1024].sum()) == 0
+
+
+# ---------------------------------------------------------------- NaN behind a mask
+@pytest.mark.parametrize("window", [0, 6, 40, 2000])
+@pytest.mark.parametrize("lens,news", [([7, 64, 500, 130, 33], [7, 4, 5, 40, 33]), ([9000, 2500, 40], [5, 3, 2])])
+@pytest.mark.parametrize("D,hk,G,page", [(64, 2, 2, 16), (128, 1, 2, 64), (128, 2, 6, 32), (64, 1, 5, 128)])
+def test_nan_values_reach_only_the_rows_that_see_them(window, lens, news, D, hk, G, page):
+    """A NaN in a token's V or K reaches the rows that see the token, and no other: not
+    those before it, nor those whose window has passed it."""
+    rng = np.random.default_rng(54)
+    b = Batch(rng, lens, news, hk, D, page)
+    for s, (n, new) in enumerate(zip(lens, news)):
+        edges = rng.integers(max(0, n - new - 8), n, 4).tolist()
+        if 0 < window < n - new:
+            edges += rng.integers(n - new - window, n - window + 4, 3).tolist()
+        for i, pos in enumerate(edges):
+            b.cache["v"][b.table[s, pos // page], i % hk, pos % page, rng.integers(0, D, 3)] = (0x7F, 0xFF, 0x7F)
+        pos = n - 2
+        b.cache["k"][b.table[s, pos // page], 0, pos % page, 5] = 0x7F
+    q = bf16_values(rng, (b.total, hk * G, D))
+    ref = orc.attention(q, b.cache, b.table, b.q_start, b.lens, 1 / math.sqrt(D), window=window)[0]
+    assert np.isnan(ref).any() and np.isfinite(ref).any()
+    ws = workspace(m.decode_attention_workspace_size(hk * G, hk, D, b.max_new))
+    got, lse, status = run_attention(b, q, hk * G, ws=ws, window=window)
+    assert status == m.MOE_OK
+    check(b, q, got, lse, 1 / math.sqrt(D), window=window)
+    again = run_attention(b, q, hk * G, ws=ws, window=window)[0]
+    assert np.array_equal(got, again, equal_nan=True)
