@@ -425,7 +425,8 @@ int kv_cache_append(const moe_kv_cache *cache, const void *k, long long k_stride
  *          min(B, total) * kv_heads + total * heads / 8 <= 7 * 10^8
  *   out    bf16 [total, heads, head_dim];  lse fp32 [total, heads] or NULL
  *   slopes fp32 [heads] or NULL
- * Scores, statistics and sums are fp32; the weights are rounded to 11 bits for
+ * Scores, statistics and sums are fp32 (a capped score is within 2^-22 of caps up
+ * to 256, within 2^-20 of itself above); the weights are rounded to 11 bits for
  * their product with V.  V scales of one sequence and head may differ by up to
  * 2^29 before weights lose bits.  An infinity or a NaN in a row of q makes the
  * row NaN; a NaN in a token's k or v reaches the rows that see the token, and no

@@ -132,10 +132,19 @@ MOE_DEV float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh(y / (2 log2 e)) = 1 - 2 / (1 + 2^y): off by about 2^-23, absolutely
+// tanh(y / (2 log2 e)) = 1 - 2 / (1 + 2^y): off by about 2^-23, absolutely, so a capped
+// score by 2^-22 of the cap.  Caps above kFarCap take the other one.
+constexpr float kFarCap = 256.f;
 MOE_DEV float tanh_of(float y) {
   y = y > 80.f ? 80.f : y;  // (2^y stays finite, a NaN stays one)
   return 1.f - __fdividef(2.f, 1.f + ex2(y));
+}
+// the same relatively: below 1/4 the series of tanh z, whose next term, 62/2835 z^9, is 2^-21
+// of it there
+MOE_DEV float tanh_far(float y) {
+  const float z = y * (0.5f * kLn2), z2 = z * z;
+  const float t = z * fmaf(z2, fmaf(z2, fmaf(z2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  return fabsf(z) < 0.25f ? t : tanh_of(y);
 }
 // two E4M3 pairs (the lower and the upper half of w) to two f16 pairs
 MOE_DEV void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -594,13 +603,19 @@ __device__ __forceinline__ void run_piece(const AttArgs& a, const AttMaps& maps,
       }
     }
     if (MODS) {
-      const float cap_in = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+      const float cap_in = a.softcap > 0.f ? fminf(2.f * kLog2e / a.softcap, 3.4028235e38f) : 0.f;
+      if (a.softcap > kFarCap) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int k = 0; k < kTile / 4; ++k) s[rt][k] = a.softcap * tanh_far(s[rt][k] * cap_in);
+      }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int k = 0; k < kTile / 4; ++k) {
           float x = s[rt][k];
-          if (a.softcap > 0.f) x = a.softcap * tanh_of(x * cap_in);
+          if (a.softcap > 0.f && a.softcap <= kFarCap) x = a.softcap * tanh_of(x * cap_in);
           const int pos = base + 8 * (k >> 1) + 4 * (k & 1) + q;
           s[rt][k] = fmaf(slope[rt], (float)(pos - pos_r[rt]), x * kLog2e);
         }

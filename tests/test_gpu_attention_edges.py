@@ -277,3 +277,21 @@ def test_nan_values_reach_only_the_rows_that_see_them(window, lens, news, D, hk,
     check(b, q, got, lse, 1 / math.sqrt(D), window=window)
     again = run_attention(b, q, hk * G, ws=ws, window=window)[0]
     assert np.array_equal(got, again, equal_nan=True)
+
+
+# ---------------------------------------------------------------- caps
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 0.5, 255.0, 257.0, 4096.0, 1e6, 1e20, 3e38])
+@pytest.mark.parametrize("D,hk,G", [(64, 2, 2), (128, 1, 12)])
+def test_caps_of_every_size(cap, D, hk, G):
+    """A cap far above the scores changes nothing, one far below flattens them."""
+    rng = np.random.default_rng(55)
+    b = Batch(rng, [300, 40, 7], [1, 2, 3], hk, D, 32)
+    q = bf16_values(rng, (b.total, hk * G, D), 4.0)
+    q[2] = 0.0  # scores of zero
+    sm = 1 / math.sqrt(D)
+    cap = float(np.float32(cap))
+    got, lse, status = run_attention(b, q, hk * G, softcap=cap)
+    assert status == m.MOE_OK
+    # the tanh is off by 2^-22 of the cap, and above 256 by at most 2^-20 of the score
+    unit = orc.attention(q, b.cache, b.table, b.q_start, b.lens, sm, cap)[3][..., 0]
+    check(b, q, got, lse, sm, score=2.0 ** -22 * cap if cap <= 256 else 2.0 ** -20 * unit, softcap=cap)
