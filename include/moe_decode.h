@@ -378,7 +378,9 @@ int fp8_linear(const void *x, long long x_stride, const uint8_t *w, const float 
  * Values that do not fit (a page outside [0, num_pages), rows outside
  * [0, total], a length above width * page_size) set the status word to
  * MOE_ERR_INVALID_ARG; nothing outside the arrays is read or written.
- * width * page_size <= 2^30, B <= 2^20, total <= 2^24.
+ * width * page_size <= 2^30, B <= 2^20, total <= 2^24.  B == 0 or total == 0 is a
+ * no-op, whatever the arrays' pointers.  Rows that no sequence holds are left as
+ * they are.
  */
 typedef struct moe_kv_cache {
   uint8_t *k;

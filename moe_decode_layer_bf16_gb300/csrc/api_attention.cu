@@ -105,9 +105,10 @@ int check_cache(const moe_kv_cache* c) {
 
 int check_batch(const moe_kv_cache* c, const int32_t* page_table, int width, const int32_t* q_start,
                 const int32_t* lens, int B, int total, int max_new) {
-  if (B < 0 || total < 0 || width < 1 || max_new < 1) return MOE_ERR_INVALID_ARG;
-  if (!page_table || !q_start || !lens) return MOE_ERR_INVALID_ARG;
+  if (B < 0 || total < 0 || width < 0 || max_new < 1) return MOE_ERR_INVALID_ARG;
   if ((long long)width * c->page_size > kMaxLen || B > (1 << 20) || total > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if (B == 0 || total == 0) return MOE_OK;  // a no-op: nothing of the batch is read (arrays of no elements may be null)
+  if (width < 1 || !page_table || !q_start || !lens) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 

@@ -112,3 +112,19 @@ def test_attention_of_more_items_than_can_be_counted_is_refused():
     for ok in ((600000, 600000, 1024, 1024), (1, 1 << 20, 1024, 1024), (1 << 20, 1, 1024, 1024), (4, 93000, 128, 8),
                (1, 1 << 24, 127, 1)):
         assert call(*ok) == m.MOE_ERR_INVALID_ARG, ok
+
+
+def test_batches_without_sequences_or_tokens_are_no_ops():
+    """Arrays of no elements have no address."""
+    L, fake, big = m.lib(), ctypes.c_void_p(0x10000), 1 << 40
+    c = att._Cache(0x10000, 0x10000, 0x10000, 0x10000, 8, 2, 64, 64)
+    for B, total, width in ((0, 0, 0), (0, 0, 4), (2, 0, 4), (2, 0, 0), (0, 3, 4)):
+        assert L.kv_cache_append(c, None, 128, None, 128, None, width, None, None, B, total, 1, fake, big, None) == m.MOE_OK
+        assert L.decode_attention(c, None, 256, 4, None, width, None, None, B, total, 1, 0.1, 0.0, 0, None, None, None, fake,
+                                  big, None) == m.MOE_OK
+    for B, total, width in ((-1, 0, 4), (0, -1, 4), (0, 0, -1)):
+        assert L.kv_cache_append(c, None, 128, None, 128, None, width, None, None, B, total, 1, fake, big,
+                                 None) == m.MOE_ERR_INVALID_ARG
+    for width in (0, 4):  # with tokens, everything is wanted
+        assert L.kv_cache_append(c, fake, 128, fake, 128, None if width else fake, width, fake, fake, 2, 3, 1, fake, big,
+                                 None) == m.MOE_ERR_INVALID_ARG

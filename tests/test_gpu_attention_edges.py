@@ -295,3 +295,24 @@ def test_caps_of_every_size(cap, D, hk, G):
     # the tanh is off by 2^-22 of the cap, and above 256 by at most 2^-20 of the score
     unit = orc.attention(q, b.cache, b.table, b.q_start, b.lens, sm, cap)[3][..., 0]
     check(b, q, got, lse, sm, score=2.0 ** -22 * cap if cap <= 256 else 2.0 ** -20 * unit, softcap=cap)
+
+
+# ---------------------------------------------------------------- batches without tokens
+def test_batches_without_sequences_or_tokens():
+    hk, D, page = 2, 64, 16
+    cache = m.Fp8KvCache(3, hk, D, page)
+    c = (cache.k, cache.v, cache.k_scale, cache.v_scale)
+    ws = workspace(1 << 20)
+
+    def ints(*a):
+        return torch.tensor(a, dtype=torch.int32, device=DEV)
+
+    for B, width in ((0, 4), (0, 0), (2, 4)):
+        table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+        start, lens = ints(*[0] * (B + 1)), ints(*[0] * B)
+        kv = torch.empty((0, hk, D), dtype=torch.bfloat16, device=DEV)
+        m.kv_cache_append(kv, kv, *c, table, start, lens, 1, ws)
+        q = torch.empty((0, 4, D), dtype=torch.bfloat16, device=DEV)
+        m.decode_attention(q, *c, table, start, lens, 1, torch.empty_like(q), ws,
+                           lse=torch.empty((0, 4), device=DEV))
+    assert m.moe_device_status(ws) == m.MOE_OK
