@@ -311,14 +311,14 @@ class AttentionDecode:
         if out is None:
             out = torch.empty((n, self.hidden), dtype=_bf16, device=x.device)
         qkv, mixed = self.qkv[:n], self.mixed[:n]
-        fp8_linear(x, w["qkv"], w["qkv_s"], qkv.view(n, -1), self.workspace, e8m0=self.e8m0)
+        fp8_linear(x, w["qkv"], w["qkv_s"], qkv.flatten(1), self.workspace, e8m0=self.e8m0)
         q, k, v = qkv[:, :h], qkv[:, h:h + hk], qkv[:, h + hk:]
         if self.rotate is not None:
             self.rotate(q, k)
         kv_cache_append(k, v, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, self.max_new, self.workspace)
         decode_attention(q, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, self.max_new, mixed,
                          self.workspace, **self.options)
-        fp8_linear(mixed.view(n, -1), w["o"], w["o_s"], out, self.workspace, e8m0=self.e8m0)
+        fp8_linear(mixed.flatten(1), w["o"], w["o_s"], out, self.workspace, e8m0=self.e8m0)
         return out
 
     def status(self) -> int:

@@ -7,6 +7,7 @@ import os
 import re
 import subprocess
 
+import pytest
 import torch
 
 import moe_decode_layer_bf16_gb300 as m
@@ -128,3 +129,16 @@ def test_batches_without_sequences_or_tokens_are_no_ops():
     for width in (0, 4):  # with tokens, everything is wanted
         assert L.kv_cache_append(c, fake, 128, fake, 128, None if width else fake, width, fake, fake, 2, 3, 1, fake, big,
                                  None) == m.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("n", [0, 1, 2])
+def test_attention_decode_of_a_few_tokens_or_none(monkeypatch, n):
+    shapes = []
+    monkeypatch.setattr(att, "moe_workspace_init", lambda ws: None)
+    monkeypatch.setattr(att, "fp8_linear", lambda x, w, w_s, out, ws, **kw: shapes.append((tuple(x.shape), tuple(out.shape))))
+    for name in ("kv_cache_append", "decode_attention"):
+        monkeypatch.setattr(att, name, lambda *args, **kw: None)
+    layer = m.AttentionDecode(128, 2, 1, 64, dict.fromkeys(("qkv", "qkv_s", "o", "o_s")),
+                              m.Fp8KvCache(2, 1, 64, 16, device="cpu"), max_tokens=2)
+    y = layer(torch.zeros((n, 128), dtype=torch.bfloat16), None, None, None)
+    assert tuple(y.shape) == (n, 128) and shapes == [((n, 128), (n, 256)), ((n, 128), (n, 128))]

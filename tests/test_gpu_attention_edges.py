@@ -316,3 +316,15 @@ def test_batches_without_sequences_or_tokens():
         m.decode_attention(q, *c, table, start, lens, 1, torch.empty_like(q), ws,
                            lse=torch.empty((0, 4), device=DEV))
     assert m.moe_device_status(ws) == m.MOE_OK
+
+
+def test_attention_decode_of_no_tokens():
+    rng = np.random.default_rng(59)
+    hidden, heads, hk, D, page = 256, 4, 2, 64, 16
+    (qkv, qkv_s), (o, o_s) = weights(rng, (heads + 2 * hk) * D, hidden), weights(rng, hidden, heads * D)
+    att = m.AttentionDecode(hidden, heads, hk, D, {"qkv": dev(qkv), "qkv_s": dev(qkv_s), "o": dev(o), "o_s": dev(o_s)},
+                            m.Fp8KvCache(4, hk, D, page), max_tokens=2)
+    table = dev(np.array([[0, 1], [2, 3]], np.int32))
+    x = torch.empty((0, hidden), dtype=torch.bfloat16, device=DEV)
+    y = att(x, table, dev(np.array([0, 0, 0], np.int32)), dev(np.array([3, 0], np.int32)))
+    assert tuple(y.shape) == (0, hidden) and att.status() == m.MOE_OK
