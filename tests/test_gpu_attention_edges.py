@@ -328,3 +328,45 @@ def test_attention_decode_of_no_tokens():
     x = torch.empty((0, hidden), dtype=torch.bfloat16, device=DEV)
     y = att(x, table, dev(np.array([0, 0, 0], np.int32)), dev(np.array([3, 0], np.int32)))
     assert tuple(y.shape) == (0, hidden) and att.status() == m.MOE_OK
+
+
+# ---------------------------------------------------------------- prompts
+@pytest.mark.parametrize("kw", [dict(), dict(window=1), dict(window=50), dict(softcap=20.0, slopes=True, window=97)])
+@pytest.mark.parametrize("lens,news", [([300], [300]), ([500, 90, 40], [129, 64, 40]), ([1300], [47])])
+@pytest.mark.parametrize("D,hk,G,page", [(64, 2, 1, 16), (128, 1, 3, 64), (64, 1, 5, 128), (128, 2, 8, 32)])
+def test_a_prompts_chunk(kw, lens, news, D, hk, G, page):
+    """Many new tokens of a sequence: many groups of rows, with the diagonal across their tiles."""
+    rng = np.random.default_rng(56)
+    b = Batch(rng, lens, news, hk, D, page)
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = np.exp2(-8.0 * np.arange(1, hk * G + 1) / (hk * G)).astype(np.float32)
+    q = bf16_values(rng, (b.total, hk * G, D))
+    sm = 1 / math.sqrt(D)
+    got, lse, status = run_attention(b, q, hk * G, **kw)
+    assert status == m.MOE_OK
+    check(b, q, got, lse, sm, score=2.0 ** -22 * kw.get("softcap", 0.0), **kw)
+
+
+def test_a_prompt_in_chunks_is_the_prompt_at_once():
+    rng = np.random.default_rng(57)
+    hk, G, D, page, n = 2, 4, 128, 64, 700
+    b = Batch(rng, [n], [n], hk, D, page)
+    q = bf16_values(rng, (n, hk * G, D))
+    whole, lse, _ = run_attention(b, q, hk * G)
+    vmax, t = largest_value(b), b.tensors(DEV)
+    done, got, got_lse = 0, [], []
+    for step in (1, 130, 64, 255, 250):
+        part = Batch.__new__(Batch)
+        part.__dict__ = dict(b.__dict__, total=step, news=[step], lens=np.array([done + step], np.int32),
+                             q_start=np.array([0, step], np.int32))
+        o, l, status = run_attention(part, q[done:done + step], hk * G,
+                                     tensors={**t, "lens": dev(part.lens), "q_start": dev(part.q_start)})
+        assert status == m.MOE_OK
+        got.append(o)
+        got_lse.append(l)
+        done += step
+    ref = orc.attention(q, b.cache, b.table, b.q_start, b.lens, 1 / math.sqrt(D))
+    t_out, t_lse = tolerance(ref, D, n, vmax)
+    for o, l in ((whole, lse), (np.concatenate(got), np.concatenate(got_lse))):
+        assert (np.abs(o - ref[0]) <= t_out).all() and (np.abs(l - ref[1]) <= t_lse).all()
