@@ -22,6 +22,7 @@
 namespace {
 
 struct Refused {};
+struct PythonError {};  // the interpreter's error is set
 
 const at::Tensor& tensor(PyObject* o) {
   if (!THPVariable_Check(o)) throw Refused();
@@ -57,6 +58,12 @@ double number(PyObject* o) {
     throw Refused();
   }
   return v;
+}
+
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw PythonError();
+  return v != 0;
 }
 
 // The stream's handle: an integer, or the current stream of the tensors' device,
@@ -97,6 +104,7 @@ PyObject* call(Py_ssize_t got, Py_ssize_t wanted, F&& f) {
     return PyLong_FromLong(f());
   } catch (const Refused&) {
     return PyLong_FromLong(-1);
+  } catch (const PythonError&) {
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {
@@ -118,10 +126,10 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
          dense(out, f32 ? at::kFloat : at::kBFloat16, {M, N}) && M <= INT32_MAX && N <= INT32_MAX && K <= INT32_MAX);
     want(w.get_device() == dev && ws.get_device() == dev && out.get_device() == dev);
     const size_t bytes = room(work, dev);
-    const int e8m0 = PyObject_IsTrue(a[5]);
+    const bool e8m0 = truth(a[5]);
     void* s = stream_of(a[6], dev);
     return fp8_linear(x.data_ptr(), row_stride(x, K), static_cast<const uint8_t*>(w.data_ptr()),
-                      static_cast<const float*>(ws.data_ptr()), (int)M, (int)N, (int)K, e8m0 == 1, out.data_ptr(), f32,
+                      static_cast<const float*>(ws.data_ptr()), (int)M, (int)N, (int)K, e8m0, out.data_ptr(), f32,
                       work.data_ptr(), bytes, s);
   });
 }

@@ -142,3 +142,12 @@ def test_attention_decode_of_a_few_tokens_or_none(monkeypatch, n):
                               m.Fp8KvCache(2, 1, 64, 16, device="cpu"), max_tokens=2)
     y = layer(torch.zeros((n, 128), dtype=torch.bfloat16), None, None, None)
     assert tuple(y.shape) == (n, 128) and shapes == [((n, 128), (n, 256)), ((n, 128), (n, 128))]
+
+
+def test_an_argument_without_a_truth_value_raises_its_own_error():
+    x, w = torch.zeros((1, 128), dtype=torch.bfloat16), torch.zeros((128, 128), dtype=torch.uint8)
+    args = (x, w, torch.zeros((1, 1)), torch.zeros((1, 128)), torch.zeros(1 << 20, dtype=torch.uint8))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        m.fp8_linear(*args, e8m0=torch.zeros(2))
+    with pytest.raises(ValueError, match="CUDA"):  # and what has one is looked at further
+        m.fp8_linear(*args, e8m0=torch.ones(1))
