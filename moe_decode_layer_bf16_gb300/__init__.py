@@ -99,8 +99,8 @@ def lib() -> ctypes.CDLL:
                   "moe_decode_layer_plan", "moe_set_expert_path", "moe_decode_layer_partial", "moe_tp_boundary",
                   "mtp_eh_front_workspace_size", "mtp_eh_front"):
             getattr(L, n).restype = ctypes.c_int
-        from . import attention
-        attention.bind(L)
+        from . import attention_abi
+        attention_abi.bind(L)
         _lib = L
     return _lib
 
@@ -318,6 +318,20 @@ class MoeDecodeLayer:
         return moe_device_status(self.workspace)
 
 
-from .attention import (AttentionDecode, Fp8KvCache, decode_attention, decode_attention_workspace_size, fp8_block_gemm,  # noqa: E402
-                        fp8_block_gemm_workspace_size, fp8_linear, fp8_linear_workspace_size, fp8_quant_rows,
-                        kv_cache_append, kv_cache_workspace_size)
+# The attention module's names, imported when they are first asked for: it needs torch at
+# once, building and loading the library does not.
+_ATTENTION = ("AttentionDecode", "Fp8KvCache", "decode_attention", "decode_attention_workspace_size", "fp8_block_gemm",
+              "fp8_block_gemm_workspace_size", "fp8_linear", "fp8_linear_workspace_size", "fp8_quant_rows",
+              "kv_cache_append", "kv_cache_workspace_size")
+
+
+def __getattr__(name):
+    if name not in _ATTENTION:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    from . import attention
+    globals().update({n: getattr(attention, n) for n in _ATTENTION})
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_ATTENTION})

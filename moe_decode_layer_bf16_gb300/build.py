@@ -1,6 +1,7 @@
 """Build libmoe_decode.so in-tree for sm_103a (nvcc, one object per source,
-compiled in parallel, then linked), and beside it _calls.so, the extension module
-through which Python makes the attention operators' calls.
+compiled in parallel, then linked), and beside it, where torch is installed,
+_calls.so, the extension module through which Python makes the attention
+operators' calls.  The library itself needs nvcc alone.
 Usage: python -m moe_decode_layer_bf16_gb300.build"""
 
 from __future__ import annotations
@@ -36,9 +37,11 @@ def _newer(target: str, deps) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
-def _torch_root() -> str:
-    import importlib.util  # (where torch is, without importing it)
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_root():
+    """Where torch is, without importing it; None if it is not installed."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
 def calls_command(source: str, obj: str):
@@ -56,13 +59,15 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     headers.append(os.path.join(PKG, "..", "include", "moe_decode.h"))
     cc = nvcc()
     extra = list(extra_flags or [])
+    torch_root = _torch_root()
 
     def compile_one(src):
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+        python = src.endswith(".cpp")
         if _newer(o, [s, *headers]) and not extra:
             return o
-        cmd = calls_command(s, o) if src.endswith(".cpp") else [cc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o]
+        cmd = calls_command(s, o) if python else [cc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -80,12 +85,15 @@ def build(verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        *objs, calls = ex.map(compile_one, [*SOURCES, "calls.cpp"])
-    link(LIB, objs, [cc, *ARCH, "-shared", "-o", LIB, *objs])
-    libs = os.path.join(_torch_root(), "lib")
-    link(CALLS, [calls, LIB],
-         [os.environ.get("CXX", "g++"), "-shared", "-o", CALLS, calls, "-L" + libs, "-ltorch_python", "-ltorch",
-          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libmoe_decode.so", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs])
+        calls = ex.submit(compile_one, "calls.cpp") if torch_root else None
+        objs = list(ex.map(compile_one, SOURCES))
+        link(LIB, objs, [cc, *ARCH, "-shared", "-o", LIB, *objs])
+    if calls:
+        obj, libs = calls.result(), os.path.join(torch_root, "lib")
+        link(CALLS, [obj, LIB],
+             [os.environ.get("CXX", "g++"), "-shared", "-o", CALLS, obj, "-L" + libs, "-ltorch_python", "-ltorch",
+              "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libmoe_decode.so", "-Wl,-rpath,$ORIGIN",
+              "-Wl,-rpath," + libs])
     return LIB
 
 
