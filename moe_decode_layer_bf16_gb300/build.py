@@ -30,6 +30,13 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _read(path: str):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
+
+
 def _newer(target: str, deps) -> bool:
     if not os.path.exists(target):
         return False
@@ -42,6 +49,12 @@ def _torch_root():
     import importlib.util
     spec = importlib.util.find_spec("torch")
     return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _calls_key() -> str:
+    """What the extension module is compiled against, beside its sources."""
+    root = _torch_root()
+    return f"torch in {root}:\n{_read(os.path.join(root, 'version.py'))}\nPython {sys.version}\n"
 
 
 def calls_command(source: str, obj: str):
@@ -59,13 +72,14 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     headers.append(os.path.join(PKG, "..", "include", "moe_decode.h"))
     cc = nvcc()
     extra = list(extra_flags or [])
+    key_file = os.path.join(BUILD, "calls.key")
     torch_root = _torch_root()
 
     def compile_one(src):
         s = os.path.join(CSRC, src)
         o = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
         python = src.endswith(".cpp")
-        if _newer(o, [s, *headers]) and not extra:
+        if _newer(o, [s, *headers]) and not extra and (not python or _read(key_file) == _calls_key()):
             return o
         cmd = calls_command(s, o) if python else [cc, *ARCH, *FLAGS, *extra, "-c", s, "-o", o]
         if verbose:
@@ -75,6 +89,9 @@ def build(verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {src}:\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, flush=True)
+        if python:
+            with open(key_file, "w") as f:
+                f.write(_calls_key())
         return o
 
     def link(target, objs, cmd):

@@ -62,6 +62,19 @@ def test_the_library_where_the_extension_does_not_compile(made):
     assert "libmoe_decode.so" in made.names and os.path.exists(b.LIB)
 
 
+def test_another_torch_another_extension(made, monkeypatch):
+    made()
+    key = b._calls_key()
+    monkeypatch.setattr(b, "_calls_key", lambda: key + "newer")
+    assert made() == ["_calls.so", "calls.o"]
+    assert made() == []
+
+
+def test_the_key_names_torch_and_python():
+    import torch
+    assert torch.__version__ in b._calls_key() and sys.version in b._calls_key()
+
+
 def test_package_and_library_without_torch():
     """Importing the package, its build and the loaded library take no torch."""
     code = ("import sys; sys.modules['torch'] = None\n"
