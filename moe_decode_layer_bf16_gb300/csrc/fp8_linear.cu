@@ -168,9 +168,10 @@ struct Cfg {
   // token 23.1 us, first cell 4.7 us after the start).  XQ: all (holding the
   // others back until the first rows of x are here: 18.4 -> 19.1 us)
   static constexpr int kAhead = XQ ? kNST : std::min(kNST, 4);
-  // weight tiles brought into L2 before the kernel before is complete (one token, us:
-  // 6 16.8, 12 16.6, 20 16.0, 32 16.6)
-  static constexpr int kPrefetch = 20;
+  // weight tiles brought into L2 before the kernel before is complete (one token, 7168 ->
+  // 9216, and 8 tokens, 7168 -> 7168, us in a graph: 6 14.4 14.5, 12 14.6 14.5, 20 14.6
+  // 14.7, 32 15.5 15.3; other sizes alike)
+  static constexpr int kPrefetch = 6;
   static constexpr int kTST = NT <= 128 ? 4 : 2;              // accumulator buffers in tensor memory
   static constexpr int kTCols = NT * kTST;                    // 64 .. 512, a power of two
   static constexpr int kHalf = NT / 2;                        // columns of an epilogue warp
