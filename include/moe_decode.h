@@ -362,7 +362,8 @@ int fp8_linear(const void *x, long long x_stride, const uint8_t *w, const float 
  * A paged key/value cache in FP8.  A block is a page of one key/value head:
  * page_size tokens whose codes share one fp32 scale (value = code * scale).
  *   k, v              fp8 [num_pages, kv_heads, page_size, head_dim]
- *   k_scale, v_scale  fp32 [num_pages, kv_heads]
+ *   k_scale, v_scale  fp32 [num_pages, kv_heads], finite and at most 2^126 (as the
+ *                     append writes them)
  * page_size 16, 32, 64 or 128; head_dim 64 or 128; kv_heads <= 1024; k and v
  * 16-byte aligned.  Nothing needs to be initialised: what a block held before
  * its first slot is written does not matter.

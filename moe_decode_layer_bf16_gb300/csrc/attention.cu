@@ -11,9 +11,9 @@
 // the head, far below the tensor cores' balance, so the cache stream from HBM
 // is the floor.  One pass with the running maximum and sum of the softmax.
 // Measured: 61 sequences of 300 to 16384 tokens, 526 MB, 87.9 us, 6.0 TB/s (0.88 of the
-// copy rate); one of 131001 tokens 51.2 us, 5.2 TB/s; about 2 us until the lengths, the
+// copy rate); one of 131001 tokens 51.9 us, 5.2 TB/s; about 2 us until the lengths, the
 // page numbers and the first tile are there, and 4 until the pieces are joined, are
-// what short caches cost (777 tokens 9.4 us).
+// what short caches cost (777 tokens 9.3 us).
 //
 // Work split.  The unit is a tile of 32 tokens of one item (sequence, kv head,
 // group of up to 8 RT rows); an item counts kItemCost tiles more for its start and
@@ -66,8 +66,8 @@ namespace {
 // sequences of 300 to 16384 tokens, us: 1 100.7, 2 87.9, 3 88.2, 4 89.2).
 constexpr int kItemCost = 2;
 // Items of so many tiles at most are not cut: a tile takes a warp 1.3 us, joining pieces
-// 5 us (80 drawn cases, geometric mean: 0 13.1 us, 1 11.2, 2 11.0, 4 11.0, 8 11.5; 3
-// sequences of 2 tokens, 96 heads on 8: 14.1 us cut, 7.4 whole).
+// 5 us (80 attention cases that perf/operators.py draws from random.Random(7), geometric
+// mean in a graph: 0 10.99 us, 1 9.95, 2 9.88, 4 9.93, 8 10.50).
 constexpr int kWholeTiles = 2;
 // Where tiles as units come to more than 31 bits (a prompt of 93000 tokens, 128 heads on 8),
 // a unit is 2^5 of them, or 2^10, ...: one unit more or less a warp is nothing there.
@@ -802,10 +802,12 @@ __global__ void __launch_bounds__((AttCfg<D, RT>::kThreads), 1)
   constexpr int kRowsC = C::kRowsC, kTile = C::kTile, kGroups = C::kGroups, kNST = C::kNST;
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   // Items of up to so many units (and more than kWholeTiles tiles) stay within a CTA where
-  // a CTA's share is smaller than that: no joining through memory (80 drawn cases,
-  // geometric mean: 0 10.8 us, kWarps 10.9, 2 kWarps 10.5, 3 kWarps 10.7; 19 sequences
-  // of 374 to 496 tokens, windowed, 14.1 us for 10.8; the items of 4 x 3 rows of 52 to
-  // 1514 tokens, which then wait for their longest, 13.0 for 14.6).
+  // a CTA's share is smaller than that: no joining through memory.  Graph, us, 0 / kWarps /
+  // 2 kWarps / 3 kWarps: 19 sequences of 374 to 496 tokens, window 321, 16 heads on one,
+  // 12.4 / 12.2 / 10.0 / 10.0; 7 x 3 rows of 200 to 400 tokens, 96 heads on 8, 15.7 / 15.7
+  // / 12.6 / 12.6; 4 x 3 of 52 to 1514 tokens, 16 heads of 64 on 4, which then wait for
+  // their longest, 11.4 / 11.8 / 11.7 / 11.7; the 80 drawn cases above 9.87 / 9.90 / 9.88
+  // / 9.85.
   constexpr int kCtaUnits = 2 * kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((C::kAlign - (su32(smem_raw) & (C::kAlign - 1))) & (C::kAlign - 1));

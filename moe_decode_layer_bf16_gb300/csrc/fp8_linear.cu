@@ -5,9 +5,9 @@
 // every sum in fp32, rounded once at the end.  The weight format is the one of
 // the expert layers, so the attention projections around them use it too.
 //
-// What bounds it.  One token of 7168 -> 9216 is 66 MB of weights: 14.5 us, 4.6 TB/s (0.67
+// What bounds it.  One token of 7168 -> 9216 is 66 MB of weights: 14.4 us, 4.6 TB/s (0.68
 // of the copy rate; start and exchange of sums are about 5 us of it).  4096 tokens are
-// 541 GFLOP: 219 us in a graph, 2470 TFLOP/s, of which the quantisation takes 15 and
+// 541 GFLOP: 221 us back to back, 2450 TFLOP/s, of which the quantisation takes 15 and
 // the MMAs alone 160; between MMAs of a cell the accumulator buffer goes to the epilogue
 // and back, and with two buffers of 256 columns (all of tensor memory) that round trip
 // shows.

@@ -13,7 +13,9 @@
 // atomics and no order.  The block's new rows are read once into registers (their
 // place does not depend on the page, so that read does not wait for the page's
 // number), their maximum reduced over the CTA, then converted and stored.  Bound
-// by latency for a token each and by DRAM for prompt chunks.
+// by latency for a token each (64 sequences 4.9 us in a graph), and for prompt chunks by
+// that chain of steps, of which a CTA has one block's under way at a time (4 x 2048
+// tokens 13.0 us, 3.8 TB/s of the copy's 6.8).
 #include "common.cuh"
 #include "kernels.h"
 #include "step_rows.h"
