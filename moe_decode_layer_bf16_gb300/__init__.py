@@ -335,3 +335,6 @@ def __getattr__(name):
 
 def __dir__():
     return sorted({*globals(), *_ATTENTION})
+
+
+__all__ = [n for n in __dir__() if not n.startswith("_")]

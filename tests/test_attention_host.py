@@ -13,6 +13,14 @@ import torch
 import moe_decode_layer_bf16_gb300 as m
 from moe_decode_layer_bf16_gb300 import attention as att
 
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    if not os.path.exists(m.LIB_PATH):
+        from moe_decode_layer_bf16_gb300 import build
+        build.build()
+
+
 CSRC = os.path.join(os.path.dirname(m.__file__), "csrc")
 
 
