@@ -329,8 +329,7 @@ def __getattr__(name):
     if name not in _ATTENTION:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     from . import attention
-    globals().update({n: getattr(attention, n) for n in _ATTENTION})
-    return globals()[name]
+    return globals().setdefault(name, getattr(attention, name))
 
 
 def __dir__():
