@@ -326,10 +326,11 @@ _ATTENTION = ("AttentionDecode", "Fp8KvCache", "decode_attention", "decode_atten
 
 
 def __getattr__(name):
-    if name not in _ATTENTION:
+    if name not in ("attention", *_ATTENTION):
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import attention
-    return globals().setdefault(name, getattr(attention, name))
+    import importlib
+    attention = importlib.import_module(".attention", __name__)
+    return attention if name == "attention" else globals().setdefault(name, getattr(attention, name))
 
 
 def __dir__():

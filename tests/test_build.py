@@ -95,6 +95,9 @@ def test_names_of_the_attention_module():
         assert getattr(m, name) is getattr(attention, name)
     with pytest.raises(AttributeError, match="no_such_name"):
         m.no_such_name
+    code = "import moe_decode_layer_bf16_gb300 as m; assert m.attention.fp8_linear is m.fp8_linear"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(m.__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
     star = {}
     exec("from moe_decode_layer_bf16_gb300 import *", star)
     assert {*m._ATTENTION, "MoeDecodeLayer", "moe_decode_layer", "MOE_OK"} <= set(star)
