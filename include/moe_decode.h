@@ -442,6 +442,114 @@ int decode_attention(const moe_kv_cache *cache, const void *q, long long q_strid
                      int max_new, float sm_scale, float softcap, int window, const float *slopes, void *out, float *lse,
                      void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A prompt's way through the attention sublayer: the layer boundary with FP8
+ * output, pages of the cache given to the step's tokens and taken back, and
+ * attention of whole prompts over themselves.  No counterpart on the source
+ * pages; formats, batches and workspaces are those of the calls above.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * rmsnorm_residual whose output is what fp8_block_gemm reads:
+ *   r' = x + residual (fp32; x NULL: the residual);  residual_out = bf16(r');
+ *   y = residual_out * rsqrt(mean(residual_out^2) + eps) * gain   (fp32);
+ *   codes, scales = the quantisation of fp8_quant_rows, of y unrounded;
+ *   out = bf16(y), where out is not NULL.
+ *   x, residual   bf16 [M, H], rows x_stride / residual_stride elements apart
+ *                 (>= H, % 8 == 0)
+ *   gain          bf16 [H]
+ *   residual_out  bf16 [M, H]; may be the residual itself where that is dense
+ *   codes         fp8 [M, H];  scales fp32 [ceil(H / 128), M rounded up to a
+ *                 multiple of 4] (columns from M on are not written)
+ * H % 16 == 0, H <= 16384, M <= 2^20; every pointer 16-byte aligned; apart from
+ * residual_out no output may overlap an input.  M == 0 is a no-op.  One kernel;
+ * a row's result does not depend on the other rows, but for the last bits of
+ * its mean on whether there are few or many (fp32 sums in another order).
+ */
+int rmsnorm_residual_fp8(const void *x, long long x_stride, const void *residual, long long residual_stride,
+                         const void *gain, int M, int H, float eps, int e8m0, uint8_t *codes, float *scales, void *out,
+                         void *residual_out, void *stream);
+
+/*
+ * Pages of the cache on the GPU.  The free pages are a stack: the first
+ * free_state[0] entries of free_pages, the last of them on top.  Sequence b
+ * holds lens[b] tokens in its first ceil(lens[b] / page_size) table entries.
+ *
+ * kv_pages_extend makes room for a step's new_tokens[b] >= 0 tokens of each
+ * sequence and describes the step's rows:
+ *   need_b = ceil((lens[b] + new_b) / page_size) - ceil(lens[b] / page_size);
+ *   a sequence is served if it needs no page or the needs up to and with it, of
+ *   all sequences before it, are at most free_state[0]; n_b = new_b if it is, else
+ *   0 (its table, length and rows are then as if it had asked for nothing);
+ *   the pages go from the top of the stack down to the served sequences in
+ *   turn, to each sequence's table entries in turn;
+ *   lens_out[b] = lens[b] + n_b;  q_start[b] = sum of n before b (B + 1 values);
+ *   row q_start[b] + i:  positions = lens[b] + i, slots = page * page_size +
+ *   position % page_size with the position's page; rows from q_start[B] to
+ *   `rows`: -1;
+ *   free_out[0] = pages left;  free_out[1] = pages that were asked for and not
+ *   given (0: everyone was served).
+ *
+ * kv_pages_release takes back the pages of the sequences with done[b] != 0:
+ * they are pushed sequence by sequence, entry by entry; lens_out[b] = 0 for
+ * these and lens[b] for the others, free_out = {free_state[0] + pages, 0}.
+ * Table entries stay as they are.  A page that several sequences hold may be
+ * released by the last of them only.
+ *
+ *   page_table  int32 [B, width];  lens, lens_out, new_tokens int32 [B]; done one byte [B]
+ *   free_pages  int32 [capacity];  free_state, free_out int32 [2]
+ *   q_start     int32 [B + 1];  positions int32 [rows];  slots int64 [rows]
+ *   workspace   kv_cache_workspace_size
+ * lens_out may be lens, and free_out free_state (a step in place); no other
+ * arrays may overlap.  page_size 16, 32, 64 or 128; width * page_size <= 2^30;
+ * B <= 2^20; rows <= 2^24.  B == 0 only fills rows and the state.
+ * Values that do not fit set the status word to MOE_ERR_INVALID_ARG: a sequence
+ * with a negative length or more tokens than its table has room for is left as
+ * it is, as is one whose rows (counted over all that is asked for) pass `rows`;
+ * a page outside [0, num_pages) is handed on, with slots of -1; a state outside
+ * [0, capacity] counts as an empty stack and is left as it is; pages that do not
+ * fit on the stack are not released, none of the call's.  One kernel each.
+ */
+int kv_pages_extend(int32_t *page_table, int width, const int32_t *lens, const int32_t *new_tokens, int B,
+                    const int32_t *free_pages, int capacity, const int32_t *free_state, int page_size, int num_pages,
+                    int32_t *q_start, int32_t *lens_out, int32_t *free_out, int32_t *positions, int64_t *slots, int rows,
+                    void *ws, size_t ws_bytes, void *stream);
+int kv_pages_release(const int32_t *page_table, int width, const int32_t *lens, const uint8_t *done, int B,
+                     int32_t *free_pages, int capacity, const int32_t *free_state, int page_size, int num_pages,
+                     int32_t *lens_out, int32_t *free_out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of whole prompts over themselves, from the projection's bf16 keys
+ * and values (decode_attention serves tokens whose sequence holds more than the
+ * step's).  Rows [q_start[b], q_start[b + 1]) of `total` are prompt b; for its
+ * row i and query head h with kv head h / (heads / kv_heads):
+ *   s_j = sm_scale * q_i . k_j;  if softcap > 0: s_j = softcap * tanh(s_j / softcap);
+ *   if slopes: s_j += slopes[h] * (j - i)
+ *   over the prompt's rows j <= i and, if window > 0, j > i - window:
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j);  lse = log sum_j exp(s_j).
+ *   q     bf16 [total, heads, head_dim], k, v bf16 [total, kv_heads, head_dim],
+ *         rows q_stride / k_stride / v_stride elements apart (% 8 == 0; slices of
+ *         a fused projection do), 16-byte aligned
+ *   out   bf16 [total, heads, head_dim];  lse fp32 [total, heads] or NULL
+ *   slopes fp32 [heads] or NULL
+ * head_dim 64 or 128; heads % kv_heads == 0, heads <= 4096, kv_heads <= 1024;
+ * B <= 2^20, total <= 2^24, total * heads < 2^31.  B == 0 or total == 0 is a no-op.
+ * Rows that no prompt holds are left as they are.  A prompt whose rows do not lie
+ * in [0, total) is left out and sets the status word to MOE_ERR_INVALID_ARG.
+ * Scores, statistics and sums are fp32 (caps as decode_attention's); the weights
+ * are rounded to bf16 for their product with V.  An infinity or a NaN in a row of
+ * q makes the row NaN; a NaN in a row's k or v reaches the rows that see it,
+ * and no other; what rows outside the prompts hold does not matter.
+ * One kernel; results do not depend on the order in which CTAs finish.
+ */
+int prompt_attention_workspace_size(size_t *bytes);
+int prompt_attention(const void *q, long long q_stride, const void *k, long long k_stride, const void *v,
+                     long long v_stride, int heads, int kv_heads, int head_dim, const int32_t *q_start, int B, int total,
+                     float sm_scale, float softcap, int window, const float *slopes, void *out, float *lse, void *ws,
+                     size_t ws_bytes, void *stream);
+
 /* Expert kernels (moe_decode_layer_plan, moe_set_expert_path). */
 enum moe_expert_path {
   MOE_PATH_AUTO = 0,      /* the library's choice by layer kind and token count */

@@ -13,7 +13,10 @@ plus MoeDecodeLayer, a holder of one layer's weights and workspace, and, from
 the attention module,
   fp8_quant_rows, fp8_block_gemm, fp8_linear, kv_cache_append, decode_attention
 (with their *_workspace_size), and AttentionDecode, the attention sublayer over
-an Fp8KvCache.
+an Fp8KvCache; from the prompt module
+  rmsnorm_residual_fp8, kv_pages_extend, kv_pages_release, prompt_attention
+(with its *_workspace_size), KvPages, the pages of a batch, and AttentionPrompt,
+the attention sublayer of whole prompts.
 """
 
 from __future__ import annotations
@@ -318,23 +321,26 @@ class MoeDecodeLayer:
         return moe_device_status(self.workspace)
 
 
-# The attention module's names, imported when they are first asked for: it needs torch at
-# once, building and loading the library does not.
+# The names of the attention and prompt modules, imported when they are first asked for:
+# these need torch at once, building and loading the library does not.
 _ATTENTION = ("AttentionDecode", "Fp8KvCache", "decode_attention", "decode_attention_workspace_size", "fp8_block_gemm",
               "fp8_block_gemm_workspace_size", "fp8_linear", "fp8_linear_workspace_size", "fp8_quant_rows",
               "kv_cache_append", "kv_cache_workspace_size")
+_PROMPT = ("AttentionPrompt", "KvPages", "kv_pages_extend", "kv_pages_release", "prompt_attention",
+           "prompt_attention_workspace_size", "rmsnorm_residual_fp8")
 
 
 def __getattr__(name):
-    if name not in ("attention", *_ATTENTION):
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    import importlib
-    attention = importlib.import_module(".attention", __name__)
-    return attention if name == "attention" else globals().setdefault(name, getattr(attention, name))
+    for module, names in (("attention", _ATTENTION), ("prompt", _PROMPT)):
+        if name == module or name in names:
+            import importlib
+            found = importlib.import_module("." + module, __name__)
+            return found if name == module else globals().setdefault(name, getattr(found, name))
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def __dir__():
-    return sorted({*globals(), *_ATTENTION})
+    return sorted({*globals(), *_ATTENTION, *_PROMPT})
 
 
 __all__ = [n for n in __dir__() if not n.startswith("_")]

@@ -18,7 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_decode.so")
 CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["api.cu", "gemv.cu", "experts.cu", "experts_tc.cu", "rmsnorm.cu", "mtp.cu",
-           "api_attention.cu", "fp8_linear.cu", "kv_append.cu", "attention.cu"]
+           "api_attention.cu", "fp8_linear.cu", "kv_append.cu", "attention.cu",
+           "api_prompt.cu", "rmsnorm_fp8.cu", "kv_pages.cu", "prompt_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--threads", "1"]
 

@@ -8,6 +8,7 @@
 
 #include "../../include/moe_decode.h"
 #include "kernels.h"
+#include "op_workspace.h"
 
 namespace moe {
 
@@ -16,26 +17,6 @@ namespace {
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // No sequence is longer, so no window is wider (and its differences fit in 32 bits).
 constexpr int kMaxLen = 1 << 30;
-bool al16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-// Start of every workspace of these operators: the status word, then the
-// tickets of split work.  Both are left as they were found, whatever the
-// operator, so one workspace serves them all in stream order.
-constexpr size_t kHdrBytes = 256;
-constexpr size_t kTicketBytes = ((size_t)std::max(kLinMaxCtas, kAttMaxCtas) * sizeof(int) + 255) / 256 * 256;
-constexpr size_t kDataAt = kHdrBytes + kTicketBytes;
-
-struct Ws {
-  int* status;
-  int* tickets;
-  uint8_t* data;
-  explicit Ws(void* ws) {
-    uint8_t* p = reinterpret_cast<uint8_t*>(ws);
-    status = reinterpret_cast<int*>(p) + kHdrStatus;
-    tickets = reinterpret_cast<int*>(p + kHdrBytes);
-    data = p + kDataAt;
-  }
-};
 
 int check_linear(int M, int N, int K) {
   if (M < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;

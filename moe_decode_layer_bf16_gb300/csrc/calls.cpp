@@ -208,9 +208,147 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+int32_t* ints(const at::Tensor& t, at::IntArrayRef shape, int dev) {
+  want(dense(t, at::kInt, shape) && t.get_device() == dev);
+  return static_cast<int32_t*>(t.data_ptr());
+}
+
+// Rows of [M, n] bf16 values, dense but for the step from row to row.
+int64_t bf16_rows(const at::Tensor& t, int64_t M, int64_t n, int dev) {
+  want(t.scalar_type() == at::kBFloat16 && t.dim() == 2 && t.size(0) == M && t.size(1) == n && (n == 1 || t.stride(1) == 1) &&
+       t.get_device() == dev);
+  return row_stride(t, n);
+}
+
+// residual, gain, codes, scales, residual_out, eps, x, out, e8m0, stream
+PyObject* norm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&]() -> int {
+    const at::Tensor &res = tensor(a[0]), &gain = tensor(a[1]), &codes = tensor(a[2]), &scales = tensor(a[3]),
+                     &res_out = tensor(a[4]);
+    want(res.dim() == 2);
+    const int64_t M = res.size(0), H = res.size(1);
+    const int dev = res.get_device();
+    want(M <= INT32_MAX && H <= INT32_MAX);
+    const int64_t ldr = bf16_rows(res, M, H, dev);
+    want(dense(gain, at::kBFloat16, {H}) && gain.get_device() == dev);
+    want(is_codes(codes) && codes.is_contiguous() && codes.dim() == 2 && codes.size(0) == M && codes.size(1) == H &&
+         codes.get_device() == dev);
+    want(dense(scales, at::kFloat, {(H + 127) / 128, (M + 3) / 4 * 4}) && scales.get_device() == dev);
+    want(dense(res_out, at::kBFloat16, {M, H}) && res_out.get_device() == dev);
+    const double eps = number(a[5]);
+    const void* x = nullptr;
+    int64_t ldx = 0;
+    if (a[6] != Py_None) {
+      const at::Tensor& t = tensor(a[6]);
+      ldx = bf16_rows(t, M, H, dev);
+      x = t.data_ptr();
+    }
+    void* out = nullptr;
+    if (a[7] != Py_None) {
+      const at::Tensor& t = tensor(a[7]);
+      want(dense(t, at::kBFloat16, {M, H}) && t.get_device() == dev);
+      out = t.data_ptr();
+    }
+    const bool e8m0 = truth(a[8]);
+    void* s = stream_of(a[9], dev);
+    return rmsnorm_residual_fp8(x, ldx, res.data_ptr(), ldr, gain.data_ptr(), (int)M, (int)H, (float)eps, e8m0,
+                                static_cast<uint8_t*>(codes.data_ptr()), static_cast<float*>(scales.data_ptr()), out,
+                                res_out.data_ptr(), s);
+  });
+}
+
+struct Pages {
+  int32_t *table, *lens, *stack, *state;
+  int width, B, capacity, page, pages, dev;
+};
+
+// page_table, lens, (new or done), free_pages, free_state, page_size, num_pages
+Pages pages(PyObject* const* a) {
+  const at::Tensor &table = tensor(a[0]), &lens = tensor(a[1]), &stack = tensor(a[3]);
+  const int dev = table.get_device();
+  want(table.dim() == 2 && stack.dim() == 1);
+  const int64_t B = table.size(0), width = table.size(1), capacity = stack.size(0);
+  want(B <= INT32_MAX && width <= INT32_MAX && capacity <= INT32_MAX);
+  return {ints(table, {B, width}, dev), ints(lens, {B}, dev), ints(stack, {capacity}, dev), ints(tensor(a[4]), {2}, dev),
+          (int)width, (int)B, (int)capacity, (int)integer(a[5]), (int)integer(a[6]), dev};
+}
+
+// page_table, lens, new, free_pages, free_state, page_size, num_pages, q_start, lens_out, free_out, positions, slots,
+// workspace, stream
+PyObject* extend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 14, [&]() -> int {
+    const Pages p = pages(a);
+    const int32_t* fresh = ints(tensor(a[2]), {p.B}, p.dev);
+    int32_t *start = ints(tensor(a[7]), {(int64_t)p.B + 1}, p.dev), *lens_out = ints(tensor(a[8]), {p.B}, p.dev),
+            *free_out = ints(tensor(a[9]), {2}, p.dev);
+    const at::Tensor &pos = tensor(a[10]), &slots = tensor(a[11]);
+    want(pos.dim() == 1 && pos.size(0) <= INT32_MAX && dense(slots, at::kLong, {pos.size(0)}) && slots.get_device() == p.dev);
+    int32_t* positions = ints(pos, {pos.size(0)}, p.dev);
+    const at::Tensor& work = tensor(a[12]);
+    const size_t bytes = room(work, p.dev);
+    void* s = stream_of(a[13], p.dev);
+    return kv_pages_extend(p.table, p.width, p.lens, fresh, p.B, p.stack, p.capacity, p.state, p.page, p.pages, start, lens_out,
+                           free_out, positions, static_cast<int64_t*>(slots.data_ptr()), (int)pos.size(0), work.data_ptr(),
+                           bytes, s);
+  });
+}
+
+// page_table, lens, done, free_pages, free_state, page_size, num_pages, lens_out, free_out, workspace, stream
+PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 11, [&]() -> int {
+    const Pages p = pages(a);
+    const at::Tensor &done = tensor(a[2]), &work = tensor(a[9]);
+    want((done.scalar_type() == at::kBool || done.scalar_type() == at::kByte) && done.dim() == 1 && done.size(0) == p.B &&
+         done.is_contiguous() && done.get_device() == p.dev);
+    int32_t *lens_out = ints(tensor(a[7]), {p.B}, p.dev), *free_out = ints(tensor(a[8]), {2}, p.dev);
+    const size_t bytes = room(work, p.dev);
+    void* s = stream_of(a[10], p.dev);
+    return kv_pages_release(p.table, p.width, p.lens, static_cast<const uint8_t*>(done.data_ptr()), p.B, p.stack, p.capacity,
+                            p.state, p.page, p.pages, lens_out, free_out, work.data_ptr(), bytes, s);
+  });
+}
+
+// q, k, v, q_start, out, workspace, lse, sm_scale, softcap, window, slopes, stream
+PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 12, [&]() -> int {
+    const at::Tensor &q = tensor(a[0]), &k = tensor(a[1]), &v = tensor(a[2]), &start = tensor(a[3]), &out = tensor(a[4]),
+                     &work = tensor(a[5]);
+    const int dev = q.get_device();
+    want(q.dim() == 3 && k.dim() == 3 && start.dim() == 1 && start.size(0) >= 1);
+    const int64_t total = q.size(0), heads = q.size(1), d = q.size(2), hk = k.size(1), B = start.size(0) - 1;
+    want(dense_rows(q, d) && dense_rows(k, d) && dense_rows(v, d) && k.size(0) == total && v.sizes() == k.sizes() &&
+         k.get_device() == dev && v.get_device() == dev);
+    want(total <= INT32_MAX && heads <= INT32_MAX && hk <= INT32_MAX && d <= INT32_MAX && B <= INT32_MAX);
+    const int32_t* starts = ints(start, {B + 1}, dev);
+    want(dense(out, at::kBFloat16, q.sizes()) && out.get_device() == dev);
+    float *lse = nullptr, *slopes = nullptr;
+    if (a[6] != Py_None) {
+      const at::Tensor& t = tensor(a[6]);
+      want(dense(t, at::kFloat, {total, heads}) && t.get_device() == dev);
+      lse = static_cast<float*>(t.data_ptr());
+    }
+    if (a[10] != Py_None) {
+      const at::Tensor& t = tensor(a[10]);
+      want(dense(t, at::kFloat, {heads}) && t.get_device() == dev);
+      slopes = static_cast<float*>(t.data_ptr());
+    }
+    const double scale = a[7] == Py_None ? 1.0 / std::sqrt((double)d) : number(a[7]), cap = number(a[8]);
+    const int window = (int)integer(a[9]);
+    const size_t bytes = room(work, dev);
+    void* s = stream_of(a[11], dev);
+    return prompt_attention(q.data_ptr(), row_stride(q, heads * d), k.data_ptr(), row_stride(k, hk * d), v.data_ptr(),
+                            row_stride(v, hk * d), (int)heads, (int)hk, (int)d, starts, (int)B, (int)total, (float)scale,
+                            (float)cap, window, slopes, out.data_ptr(), lse, work.data_ptr(), bytes, s);
+  });
+}
+
 PyMethodDef methods[] = {{"fp8_linear", (PyCFunction)(void (*)(void))linear, METH_FASTCALL, nullptr},
                          {"kv_cache_append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, nullptr},
                          {"decode_attention", (PyCFunction)(void (*)(void))attention, METH_FASTCALL, nullptr},
+                         {"rmsnorm_residual_fp8", (PyCFunction)(void (*)(void))norm_fp8, METH_FASTCALL, nullptr},
+                         {"kv_pages_extend", (PyCFunction)(void (*)(void))extend, METH_FASTCALL, nullptr},
+                         {"kv_pages_release", (PyCFunction)(void (*)(void))release, METH_FASTCALL, nullptr},
+                         {"prompt_attention", (PyCFunction)(void (*)(void))prompt, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -289,6 +289,58 @@ int attention_row_tiles(int G, int max_new);
 size_t attention_partial_bytes(int D, int G, int max_new);
 cudaError_t launch_attention(const AttArgs& a, int sms, cudaStream_t s);
 
+// Residual addition and RMSNorm with FP8 output (rmsnorm_fp8.cu).
+struct NormFp8Args {
+  const void* x;  // bf16 [M, H] or null, row strides in elements
+  const void* residual;
+  const void* gain;
+  long long ldx, ldr;
+  void* residual_out;  // bf16 [M, H]; may be the residual
+  void* out;           // bf16 [M, H] or null
+  uint8_t* codes;      // [M, H]
+  float* scales;       // [groups][mp]
+  int M, H, mp, e8m0;
+  float eps;
+};
+cudaError_t launch_rmsnorm_fp8(const NormFp8Args& a, int sms, cudaStream_t s);
+
+// Pages of the cache given to a step's tokens and taken back (kv_pages.cu).
+struct PagesArgs {
+  int32_t* page_table;       // [B][width]
+  const int32_t* lens;       // [B]
+  const int32_t* fresh;      // extend: new tokens [B]
+  const uint8_t* done;       // release: [B]
+  int32_t* free_pages;       // [capacity], read by extend, written by release
+  const int32_t* free_state; // {pages on the stack, ...}
+  int32_t* q_start;          // extend: [B + 1]
+  int32_t* lens_out;         // [B]
+  int32_t* free_out;         // {pages on the stack, pages that were missing}
+  int32_t* positions;        // extend: [rows]
+  int64_t* slots;            // extend: [rows]
+  int width, shift, num_pages, capacity, B, rows;  // shift: log2 of the page's tokens
+  int* status;
+};
+cudaError_t launch_kv_pages_extend(const PagesArgs& a, cudaStream_t s);
+cudaError_t launch_kv_pages_release(const PagesArgs& a, cudaStream_t s);
+
+// Causal attention over packed prompts (prompt_attention.cu).
+struct PromptArgs {
+  const void* q;  // bf16 [total][G * kv_heads][D], token strides in elements
+  const void* k;  // bf16 [total][kv_heads][D]
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const int32_t* q_start;  // [B + 1]
+  const float* slopes;     // [G * kv_heads] or null
+  void* out;
+  float* lse;
+  int kv_heads, G, D, B, total;
+  int window;  // tokens a row sees at most, 0 = all
+  float sm_scale, softcap;
+  int* status;
+  int* tickets;
+};
+cudaError_t launch_prompt_attention(const PromptArgs& a, int sms, cudaStream_t s);
+
 // Lets launches of `kernel` on the current device take `bytes` of dynamic shared memory.
 template <class K>
 cudaError_t allow_smem(OncePerDevice& once, K kernel, size_t bytes) {
