@@ -535,7 +535,7 @@ int kv_pages_release(const int32_t *page_table, int width, const int32_t *lens, 
  *   out   bf16 [total, heads, head_dim];  lse fp32 [total, heads] or NULL
  *   slopes fp32 [heads] or NULL
  * head_dim 64 or 128; heads % kv_heads == 0, heads <= 4096, kv_heads <= 1024;
- * B <= 2^20, total <= 2^24, total * heads < 2^31.  B == 0 or total == 0 is a no-op.
+ * B <= 2^20, total <= 2^24, total * heads < 2^31 - 1024.  B == 0 or total == 0 is a no-op.
  * Rows that no prompt holds are left as they are.  A prompt whose rows do not lie
  * in [0, total) is left out and sets the status word to MOE_ERR_INVALID_ARG.
  * Scores, statistics and sums are fp32 (caps as decode_attention's); the weights

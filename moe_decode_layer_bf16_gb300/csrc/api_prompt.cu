@@ -111,7 +111,7 @@ int prompt_attention(const void* q, long long q_stride, const void* k, long long
   if (B < 0 || total < 0 || heads < 1 || kv_heads < 1 || head_dim < 1) return MOE_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return MOE_ERR_UNSUPPORTED;
   if (heads % kv_heads || heads > 4096 || kv_heads > 1024) return MOE_ERR_UNSUPPORTED;
-  if (B > (1 << 20) || total > (1 << 24) || (long long)total * heads > INT_MAX) return MOE_ERR_UNSUPPORTED;
+  if (B > (1 << 20) || total > (1 << 24) || (long long)total * heads > INT_MAX - 1024) return MOE_ERR_UNSUPPORTED;
   if (!std::isfinite(sm_scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0) return MOE_ERR_INVALID_ARG;
   if (B == 0 || total == 0) return MOE_OK;
   int rc;

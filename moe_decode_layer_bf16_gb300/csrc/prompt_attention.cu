@@ -1,74 +1,638 @@
-// Causal attention of packed prompts over themselves, grouped heads, bf16:
-//   s_j = sm_scale q . k_j (capped, biased by distance), j <= i, j > i - window;
+// Causal attention of packed prompts over themselves, grouped heads, bf16: for row i of
+// a prompt and query head h, over its rows j <= i (and j > i - window),
+//   s_j = sm_scale q . k_j (capped, biased by distance);
 //   out = sum_j exp(s_j) v_j / sum_j exp(s_j);  lse = log sum_j exp(s_j).
 //
-// A warp for each row and head, one pass over its keys with the running maximum and sum.
+// What bounds it: the two products, 4 D flops for each visible pair of a row and a key,
+// on the tensor cores; beside them an exponential for each pair.
+//
+// Rows.  The query heads of a key/value head see the same keys, so their rows are packed
+// token by token: row r of a prompt and kv head is token r / G, head r % G.  An item is
+// 256 packed rows of one prompt and kv head, as two tiles of 128, each with its own
+// range of key tiles (128 keys).  Packing wastes nothing whatever the group is and keeps
+// the masked part of a tile small: 128 rows are 128 / G tokens.
+//
+// One CTA an SM takes items from a counter, a prompt's last (longest) ones first.  Twelve
+// warps: two softmax warpgroups, a tile each; one warp issues the MMAs, one copies keys
+// and values (TMA, a ring of tiles) and hands out the items, two load the queries and
+// look through the values of tiles that not every row sees.  For each key tile
+//   S = Q K^T into tensor memory (tcgen05, fp32), a thread reads its row of S,
+//   p = 2^(s c - m c) in bf16 over S's first columns,
+//   O += P V (P from tensor memory).
+// While one tile's softmax runs, the tensor cores work on the other tile.  The running
+// maximum m is moved, and O and the sum rescaled, only when a row's grows by more than
+// 2^8: until then the weights are up to 2^8, with the same relative precision.
+//
+// What a masked position holds must not matter, but 0 x NaN is NaN: values of tiles
+// that some row does not see in full (the diagonal, a window's edge, a prompt's end) are
+// looked through before their product, infinities and NaN replaced by zeros, and put
+// back at the end into the rows that see them.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "async.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "step_rows.h"
-#include "../../include/moe_decode.h"
+#include "tcgen05.cuh"
+#include "tmap.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kKeys = 128;    // keys of a tile
+constexpr int kRows = 128;    // packed rows of a tile
+constexpr int kBox = 128 * kKeys;  // bytes of 64 columns of 128 rows
+constexpr int kSlots = 4;     // items handed out ahead
+constexpr int kLooks = 4;     // tiles of values in the ring at most
+constexpr int kThreads = 384;
+constexpr int kMma = 8, kCopy = 9, kHelp = 10;  // warps
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that is let pass
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) prompt_attention_kernel(PromptArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int h = blockIdx.y, heads = a.G * a.kv_heads, hk = h / a.G;
-  grid_dep_launch();
-  grid_dep_wait();
-  const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (row >= a.total) return;
-  int start = -1;
-  for (int b = 0; b < a.B; ++b) {
-    const int s = a.q_start[b], e = a.q_start[b + 1];
-    if (!step_rows_ok(s, e, a.total)) {
-      if (lane == 0) atomicExch(a.status, MOE_ERR_INVALID_ARG);
-      continue;
+struct Cfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBoxes * kBox;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kRing = 2 * kTileBytes;  // behind the two query tiles
+  static constexpr int kBars = kRing + kStages * kTileBytes;
+  static constexpr int kSmem = kBars + 1024 + 512;  // (aligned by hand)
+};
+static_assert(Cfg<128>::kStages <= 2 * kLooks && Cfg<64>::kStages <= 2 * kLooks, "barriers of values looked through");
+static_assert(Cfg<128>::kSmem <= 232448 && Cfg<64>::kSmem <= 232448, "shared memory of a CTA");
+
+struct Item {
+  int start, n, row0, head;  // the prompt's first row and length, the item's first packed row, kv head; n = 0: the end
+};
+
+struct Bars {
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t item_full[kSlots], item_empty[kSlots], v_done[kSlots], v_ok[kLooks];
+  Item item[kSlots];
+  int bad[kSlots];  // the item met infinities or NaN among values that it looked through
+  uint32_t tmem;
+};
+static_assert(sizeof(Bars) <= 512, "room behind the ring");
+
+// The key tiles of a tile of packed rows, and which of them some row does not see in full.
+struct Range {
+  int lo, hi;          // none: lo > hi
+  int tok_lo, tok_hi;  // tokens of the tile's rows
+  MOE_DEV bool has(int j) const { return j >= lo && j <= hi; }
+  MOE_DEV bool edge(int j, int window) const {
+    return kKeys * j + kKeys - 1 > tok_lo || (window > 0 && kKeys * j <= tok_hi - window);
+  }
+};
+MOE_DEV Range range_of(const Item& it, int t, int G, int window) {
+  Range r;
+  const int r0 = it.row0 + t * kRows, last = it.n * G - 1;
+  if (r0 > last) {
+    r.lo = 1;
+    r.hi = 0;
+    r.tok_lo = r.tok_hi = 0;
+    return r;
+  }
+  r.tok_lo = r0 / G;
+  r.tok_hi = min(r0 + kRows - 1, last) / G;
+  r.lo = window > 0 ? max(0, r.tok_lo - window + 1) / kKeys : 0;
+  r.hi = r.tok_hi / kKeys;
+  return r;
+}
+struct Pair {
+  Range t[2];
+  int lo, hi;
+  MOE_DEV Pair(const Item& it, int G, int window) {
+    t[0] = range_of(it, 0, G, window);
+    t[1] = range_of(it, 1, G, window);
+    lo = t[0].lo;
+    hi = max(t[0].hi, t[1].hi);
+  }
+  MOE_DEV bool edge(int j, int window) const {
+    return (t[0].has(j) && t[0].edge(j, window)) || (t[1].has(j) && t[1].edge(j, window));
+  }
+};
+
+// Instruction descriptor of kind::f16: fp32 accumulator, A and B bf16, A K-major; B
+// K-major or, for the values, N-major.
+MOE_DEV constexpr uint32_t bf16_desc(int n, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kRows >> 4) << 24);
+}
+// Shared-memory descriptor of an N-major tile in TMA's 128-byte swizzled layout: 64
+// columns of N a box, boxes kBox apart (leading dimension), groups of 8 rows of K 1024
+// bytes apart (stride dimension).
+MOE_DEV uint64_t n_major_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
+}
+MOE_DEV void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, int accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+MOE_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+MOE_DEV void tc_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+MOE_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (x, y) = (x, y) * c + d, two at a time
+MOE_DEV void fma2(float& x, float& y, float c, float d) {
+  asm("{\n .reg .b64 a, b, e;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 e, {%3, %3};\n"
+      " fma.rn.f32x2 a, a, b, e;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(c), "f"(d));
+}
+MOE_DEV void add2(float& x, float& y, float c, float d) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(c), "f"(d));
+}
+
+// tanh(z) = 1 - 2 / (1 + e^(2 z)), off by about 2^-23 absolutely; for caps above kFarCap
+// and z below 1/4 the series, whose next term, 62/2835 z^9, is 2^-21 of it there.
+constexpr float kFarCap = 256.f;
+MOE_DEV float tanh_of(float z) {
+  const float y = z * (2.f * kLog2e);
+  return 1.f - __fdividef(2.f, 1.f + ex2(y > 80.f ? 80.f : y));  // (2^y stays finite, a NaN stays one)
+}
+MOE_DEV float tanh_far(float z) {
+  const float z2 = z * z;
+  const float t = z * fmaf(z2, fmaf(z2, fmaf(z2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+  return fabsf(z) < 0.25f ? t : tanh_of(z);
+}
+
+// Whether one of two bf16 values is infinite or NaN, as bits 15 and 31.
+MOE_DEV uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+MOE_DEV uint32_t finite_or_zero(uint32_t w) {
+  const uint32_t b = not_finite(w);
+  return w & ~((b >> 15) * 0xffffu);
+}
+
+// The rows that see one of the prompt's infinities or NaN that were replaced: o (32
+// columns from c0) gets them back.
+template <int D>
+__device__ __noinline__ void put_back(const PromptArgs& p, Item it, int t, int tok, int c0, float* o) {
+  const Pair pr(it, p.G, p.window);
+  const Range r = pr.t[t];
+  for (int j = r.lo; j <= r.hi; ++j) {
+    if (!pr.edge(j, p.window)) continue;
+    const int k0 = max(kKeys * j, p.window > 0 ? tok - p.window + 1 : 0), k1 = min(kKeys * j + kKeys - 1, tok);
+    for (int k = k0; k <= k1; ++k) {
+      const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.v) +
+                                                      (long long)(it.start + k) * p.v_stride + (size_t)it.head * D + c0);
+      for (int c = 0; c < 4; ++c) {
+        const uint4 x = __ldcg(v + c);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int e = 0; e < 4; ++e) {
+          if (not_finite(w[e]) & 0x8000u) o[8 * c + 2 * e] += bf16_lo(w[e]);
+          if (not_finite(w[e]) >> 31) o[8 * c + 2 * e + 1] += bf16_hi(w[e]);
+        }
+      }
     }
-    if (s <= row && row < e) start = s;
   }
-  if (start < 0) return;
-  const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + row * a.q_stride + (size_t)h * D;
-  float qf[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    qf[i] = __bfloat162float(q[lane + 32 * i]);
-    acc[i] = 0.f;
+}
+
+// kMods: scores are capped or biased (or the scale is not positive).
+template <int D, bool kMods>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
+  Bars& b = *reinterpret_cast<Bars*>(smem + C::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* status = p.status;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(b.kv_full + i, 1);
+      mbar_init(b.kv_empty + i, 3);  // the MMAs that read it, two helpers
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(b.q_full + t, 1);
+      mbar_init(b.q_empty + t, 1);
+      mbar_init(b.s_full + t, 1);
+      mbar_init(b.p_full + t, 4);
+      mbar_init(b.o_full + t, 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(b.item_full + i, 1);
+      mbar_init(b.item_empty + i, 11);  // eight softmax warps, the MMA warp, two helpers
+      mbar_init(b.v_done + i, 2);
+    }
+    for (int i = 0; i < kLooks; ++i) mbar_init(b.v_ok + i, 2);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const int first = a.window > 0 ? max(start, row - a.window + 1) : start;
-  const float slope = a.slopes ? a.slopes[h] : 0.f;
-  for (int j = first; j <= row; ++j) {
-    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(a.k) + j * a.k_stride + (size_t)hk * D;
-    const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(a.v) + j * a.v_stride + (size_t)hk * D;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s += qf[i] * __bfloat162float(k[lane + 32 * i]);
-    s = warp_sum(s) * a.sm_scale;
-    if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-    if (a.slopes) s += slope * (float)(j - row);
-    const float top = fmaxf(m, s), keep = expf(m - top), p = expf(s - top);
-    m = top;
-    l = l * keep + p;
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = acc[i] * keep + p * __bfloat162float(v[lane + 32 * i]);
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&b.tmem)), "r"(512) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + ((size_t)row * heads + h) * D;
+  grid_dep_launch();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = b.tmem;  // S (and P) of tile t at 128 t, O at 256 + 128 t
+  grid_dep_wait();
+  const int G = p.G, window = p.window;
+
+  // The k-th item of this CTA: every role but the copying warp, which makes them.
+  auto item = [&](int k, Item* it) {
+    if (!mbar_wait_landed(b.item_full + k % kSlots, (k / kSlots) & 1, status)) return false;
+    *it = b.item[k % kSlots];
+    return it->n > 0;
+  };
+  auto item_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b.item_empty + k % kSlots);
+  };
+
+  if (warp < kMma) {
+    // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = warp >> 2;
+    const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + quad + 128 * t, to = tmem + quad + 256 + 128 * t;
+    const float c = kMods ? kLog2e : p.sm_scale * kLog2e;
+    const int heads = G * p.kv_heads;
+    uint32_t steps = 0, dones = 0;
+    Item it;
+    for (int k = 0; item(k, &it); ++k) {
+      const Pair pr(it, G, window);
+      const Range rg = pr.t[t];
+      if (rg.lo > rg.hi) {
+        item_done(k);
+        continue;
+      }
+      const int row = it.row0 + t * kRows + 32 * (warp & 3) + lane;
+      const bool live = row < it.n * G;
+      const int tok = min(row / G, it.n - 1), head = it.head * G + (live ? row - row / G * G : 0);
+      const float slope = kMods && p.slopes ? p.slopes[head] : 0.f;
+      float m = -INFINITY, mc = 0.f, l0 = 0.f, l1 = 0.f;  // maximum in use, times c; two halves of the sum
+      bool alive = true;
+      for (int j = rg.lo; j <= rg.hi; ++j, ++steps) {
+        if (!mbar_wait_landed(b.s_full + t, steps & 1, status)) { alive = false; break; }
+        tc_fence_after();
+        float s[kKeys];
 #pragma unroll
-  for (int i = 0; i < E; ++i) out[lane + 32 * i] = __float2bfloat16(acc[i] / l);
-  if (a.lse && lane == 0) a.lse[(size_t)row * heads + h] = m + logf(l);
+        for (int i = 0; i < kKeys; i += 32) tc_ld32(ts + i, s + i);
+        tc_wait_ld();
+        if constexpr (kMods) {
+          const float gap0 = (float)(kKeys * j - tok);
+          const float cap = p.softcap, cap_in = cap > 0.f ? p.sm_scale / cap : 0.f;
+          if (cap > kFarCap) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) s[i] = cap * tanh_far(s[i] * cap_in);
+          } else if (cap > 0.f) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) s[i] = cap * tanh_of(s[i] * cap_in);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) s[i] *= p.sm_scale;
+          }
+          if (p.slopes) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) s[i] = fmaf(slope, gap0 + (float)i, s[i]);
+          }
+        }
+        if (rg.edge(j, window)) {
+          const int last = tok - kKeys * j, first = window > 0 ? last - window + 1 : 0;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) s[i] = i <= last && i >= first ? s[i] : -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < kKeys; i += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[i + e]);
+        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (__any_sync(0xffffffffu, (mt - m) * c > kGrow)) {
+          const float mn = fmaxf(m, mt), mcn = mn == -INFINITY ? 0.f : mn * c;
+          const float f = m == -INFINITY ? 0.f : ex2(mc - mcn);
+          l0 *= f;
+          l1 *= f;
+          if (j > rg.lo) {  // (this tile's products so far were complete before S was)
+#pragma unroll
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              tc_ld16(to + i, o);
+              tc_wait_ld();
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+              tc_st16(to + i, w);
+            }
+          }
+          m = mn;
+          mc = mcn;
+        }
+#pragma unroll
+        for (int i = 0; i < kKeys; i += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x = s[i + e], y = s[i + e + 1];
+            fma2(x, y, c, -mc);
+            x = ex2(x);
+            y = ex2(y);
+            add2(l0, l1, x, y);
+            w[e / 2] = pack_bf16(x, y);
+          }
+          tc_st16(ts + i / 2, w);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.p_full + t);
+      }
+      if (!alive) break;
+      // ---------------------------------------------------------------- the rows' results
+      if (!mbar_wait_landed(b.o_full + t, dones & 1, status)) break;
+      ++dones;
+      tc_fence_after();
+      if (!mbar_wait_landed(b.v_done + k % kSlots, (k / kSlots) & 1, status)) break;
+      const bool bad = b.bad[k % kSlots] != 0;
+      const float l = l0 + l1, inv = 1.f / l;
+      const size_t at = (size_t)(it.start + tok) * heads + head;
+      uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at * D);
+#pragma unroll
+      for (int i = 0; i < D; i += 32) {
+        float o[32];
+        tc_ld32(to + i, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        if (bad && live) put_back<D>(p, it, t, tok, i, o);
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            out[(i + e) / 8] = make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
+                                          pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
+        }
+      }
+      if (p.lse && live) p.lse[at] = (mc + log2f(l)) * kLn2;
+      tc_fence_before();
+      item_done(k);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kMma) {
+      // ================================================================ MMA
+      if (elect_one()) {
+        uint32_t ring = 0, edges = 0, pq[2] = {0, 0}, pp[2] = {0, 0};
+        bool alive = true;
+        const uint32_t sq = su32(smem), sring = su32(smem + C::kRing);
+        auto stage = [&](uint32_t n) { return sring + n % C::kStages * C::kTileBytes; };
+        auto landed = [&](uint32_t n) { return mbar_wait_landed(b.kv_full + n % C::kStages, n / C::kStages & 1, status); };
+        Item it;
+        for (int k = 0; alive && item(k, &it); ++k) {
+          const Pair pr(it, G, window);
+          for (int j = pr.lo; alive && j <= pr.hi + 1; ++j) {
+            const uint32_t nk = ring + 2 * (j - pr.lo), nv = nk - 1;  // ring places of this step's keys and of the last one's values
+            if (j > pr.lo) {
+              if (!landed(nv)) { alive = false; break; }
+              if (pr.edge(j - 1, window)) {
+                if (!mbar_wait_landed(b.v_ok + edges % kLooks, edges / kLooks & 1, status)) { alive = false; break; }
+                ++edges;
+              }
+            }
+            if (j <= pr.hi && !landed(nk)) { alive = false; break; }
+            for (int t = 0; t < 2; ++t) {
+              const Range& r = pr.t[t];
+              if (j > pr.lo && r.has(j - 1)) {
+                if (!mbar_wait_landed(b.p_full + t, pp[t]++ & 1, status)) { alive = false; break; }
+                tc_fence_after();
+                const uint64_t dv = n_major_desc(stage(nv));
+                for (int s = 0; s < kKeys / 16; ++s)
+                  mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * s, dv + (uint64_t)(s * (2048 >> 4)), bf16_desc(D, true),
+                         j - 1 > r.lo || s > 0);
+                if (j - 1 == r.hi) tc_commit(b.o_full + t);
+              }
+              if (j <= pr.hi && r.has(j)) {
+                if (j == r.lo) {
+                  if (!mbar_wait_landed(b.q_full + t, pq[t]++ & 1, status)) { alive = false; break; }
+                  tc_fence_after();
+                }
+                const uint64_t dq = smem_desc(sq + t * C::kTileBytes), dk = smem_desc(stage(nk));
+                for (int s = 0; s < D / 16; ++s) {
+                  const uint64_t step = (uint64_t)((s / 4 * kBox + s % 4 * 32) >> 4);
+                  mma_ss(tmem + 128 * t, dq + step, dk + step, bf16_desc(kKeys, false), s > 0);
+                }
+                tc_commit(b.s_full + t);
+                if (j == r.hi) tc_commit(b.q_empty + t);
+              }
+            }
+            if (!alive) break;
+            if (j > pr.lo) tc_commit(b.kv_empty + nv % C::kStages);
+            if (j <= pr.hi) tc_commit(b.kv_empty + nk % C::kStages);
+          }
+          ring += 2 * (pr.hi - pr.lo + 1);
+          if (alive) mbar_arrive(b.item_empty + k % kSlots);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kCopy) {
+      // ================================================================ items, keys and values
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      uint32_t ring = 0;
+      bool alive = true;
+      // a window of 32 prompts, a lane each: items before it, and in it up to and with each lane
+      int b0 = -32, before = 0, upto = 0, start = 0, n = 0;
+      int next = blockIdx.x;
+      for (int k = 0; alive; ++k) {
+        int ahead = 0;
+        if (lane == 0) ahead = atomicAdd(p.tickets, 1);
+        while (b0 < p.B && next >= before + __shfl_sync(0xffffffffu, upto, 31)) {
+          before += __shfl_sync(0xffffffffu, upto, 31);
+          b0 += 32;
+          start = n = 0;
+          if (b0 + lane < p.B) {
+            start = p.q_start[b0 + lane];
+            const int stop = p.q_start[b0 + lane + 1];
+            if (step_rows_ok(start, stop, p.total)) n = stop - start;
+            else if (blockIdx.x == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
+          }
+          upto = (n * G + 2 * kRows - 1) / (2 * kRows) * p.kv_heads;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+          }
+        }
+        const bool end = b0 >= p.B;
+        Item it{0, 0, 0, 0};
+        if (!end) {
+          const int at = next - before;
+          const int who = __popc(__ballot_sync(0xffffffffu, upto <= at));
+          it.start = __shfl_sync(0xffffffffu, start, who);
+          it.n = __shfl_sync(0xffffffffu, n, who);
+          const int prior = __shfl_sync(0xffffffffu, upto, who > 0 ? who - 1 : 0);
+          const int idx = at - (who > 0 ? prior : 0);
+          const int blocks = (it.n * G + 2 * kRows - 1) / (2 * kRows);
+          it.row0 = (blocks - 1 - idx / p.kv_heads) * 2 * kRows;
+          it.head = idx % p.kv_heads;
+        }
+        if (!mbar_wait_landed(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status)) break;
+        if (lane == 0) {
+          b.item[k % kSlots] = it;
+          b.bad[k % kSlots] = 0;
+          mbar_arrive(b.item_full + k % kSlots);
+        }
+        __syncwarp();
+        if (end) break;
+        const Pair pr(it, G, window);
+        if (elect_one()) {
+          for (int j = pr.lo; j <= pr.hi; ++j) {
+            for (int kv = 0; kv < 2; ++kv, ++ring) {
+              const uint32_t st = ring % C::kStages;
+              if (!mbar_wait_landed(b.kv_empty + st, (ring / C::kStages & 1) ^ 1, status)) { alive = false; break; }
+              mbar_expect_tx(b.kv_full + st, C::kTileBytes);
+              for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_3d(smem + C::kRing + st * C::kTileBytes + x * kBox, kv ? &vmap : &kmap, 64 * x, it.head,
+                            it.start + kKeys * j, b.kv_full + st);
+            }
+            if (!alive) break;
+          }
+          if (!alive)  // nothing may still be on its way when the CTA leaves
+            for (uint32_t r = ring > C::kStages ? ring - C::kStages : 0; r < ring; ++r)
+              mbar_wait_landed(b.kv_full + r % C::kStages, r / C::kStages & 1, status);
+        }
+        ring = __shfl_sync(0xffffffffu, __reduce_max_sync(0xffffffffu, ring), 0);
+        alive = __all_sync(0xffffffffu, alive);
+        next = (int)gridDim.x + __shfl_sync(0xffffffffu, ahead, 0);
+      }
+      // the last CTA leaves the counters as it found them
+      if (lane == 0 && atom_add_acq_rel(p.tickets + 1, 1) == (int)gridDim.x - 1) p.tickets[0] = p.tickets[1] = 0;
+    } else {
+      // ================================================================ queries; values that not every row sees
+      const int t = warp - kHelp;
+      constexpr int kChunks = D / 8;  // 16-byte pieces of a row
+      uint32_t ring = 0, fills = 0, edges = 0;
+      bool alive = true;
+      Item it;
+      for (int k = 0; alive && item(k, &it); ++k) {
+        const Pair pr(it, G, window);
+        const Range& r = pr.t[t];
+        if (r.lo <= r.hi) {
+          if (!mbar_wait_landed(b.q_empty + t, (fills & 1) ^ 1, status)) break;
+          ++fills;
+          const int rows = it.n * G, ch = lane % kChunks;
+          int row = it.row0 + t * kRows + lane / kChunks;
+          int tok = row / G, g = row - tok * G;
+          const uint32_t to = su32(smem) + t * C::kTileBytes + ch / 8 * kBox;
+          for (int i = lane / kChunks; i < kRows; i += 32 / kChunks, row += 32 / kChunks) {
+            const bool in = row < rows;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (long long)(it.start + (in ? tok : 0)) * p.q_stride +
+                                  (size_t)(it.head * G + (in ? g : 0)) * D + ch * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 128 + ((ch % 8 ^ (i & 7)) << 4)), "l"(src),
+                         "r"(in ? 16 : 0)
+                         : "memory");
+            for (g += 32 / kChunks; g >= G; g -= G) ++tok;
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b.q_full + t);
+        }
+        // every tile of the ring is waited for and given back in turn: a wait that skips one
+        // could not tell its phase from the last but one
+        for (int i = 0; alive && i < 2 * (pr.hi - pr.lo + 1); ++i, ++ring) {
+          const uint32_t st = ring % C::kStages;
+          if (!mbar_wait_landed(b.kv_full + st, ring / C::kStages & 1, status)) { alive = false; break; }
+          if (!(i & 1) || !pr.edge(pr.lo + i / 2, window)) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b.kv_empty + st);
+            continue;
+          }
+          // this warp's half of the tile (in any order: the swizzle stays within it)
+          uint4* half = reinterpret_cast<uint4*>(smem + C::kRing + st * C::kTileBytes + t * (C::kTileBytes / 2)) + lane;
+          uint32_t any = 0;
+#pragma unroll 8
+          for (int x = 0; x < C::kTileBytes / 2 / 512; ++x) {
+            const uint4 w = half[32 * x];
+            any |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
+          }
+          if (__any_sync(0xffffffffu, any != 0)) {
+            for (int x = 0; x < C::kTileBytes / 2 / 512; ++x) {
+              const uint4 w = half[32 * x];
+              half[32 * x] = make_uint4(finite_or_zero(w.x), finite_or_zero(w.y), finite_or_zero(w.z), finite_or_zero(w.w));
+            }
+            b.bad[k % kSlots] = 1;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(b.v_ok + edges % kLooks);
+            mbar_arrive(b.kv_empty + st);
+          }
+          ++edges;
+        }
+        __syncwarp();
+        if (alive && lane == 0) mbar_arrive(b.v_done + k % kSlots);
+        if (alive) item_done(k);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Rows of a [total][kv_heads][D] array, `stride` elements apart, in boxes of 64 columns
+// of one head and 128 rows; rows past the end read as zeros.
+bool map_rows(CUtensorMap* m, const void* base, int D, int heads, int total, long long stride) {
+  if (!encode_fn()) return false;
+  const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)total};
+  const cuuint64_t step[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, kKeys}, es[3] = {1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dim, step, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kMods>
+cudaError_t launch_as(const PromptArgs& a, int sms, cudaStream_t s) {
+  static OncePerDevice once;
+  if (const cudaError_t rc = allow_smem(once, prompt_attention_kernel<D, kMods>, Cfg<D>::kSmem); rc != cudaSuccess) return rc;
+  CUtensorMap kmap, vmap;
+  if (!map_rows(&kmap, a.k, D, a.kv_heads, a.total, a.k_stride) || !map_rows(&vmap, a.v, D, a.kv_heads, a.total, a.v_stride))
+    return cudaErrorUnknown;
+  // items at most: a started one for each prompt and head beside the full ones
+  const long long items = ((long long)a.total * a.G / (2 * kRows) + std::min(a.B, a.total)) * a.kv_heads;
+  PdlLaunch L(dim3((unsigned)std::min<long long>(items, sms)), dim3(kThreads), Cfg<D>::kSmem, s);
+  return cudaLaunchKernelEx(&L.cfg, prompt_attention_kernel<D, kMods>, a, kmap, vmap);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptArgs& a, int sms, cudaStream_t s) {
-  PdlLaunch L(dim3((a.total + kThreads / 32 - 1) / (kThreads / 32), a.G * a.kv_heads), dim3(kThreads), 0, s);
-  if (a.D == 64) return cudaLaunchKernelEx(&L.cfg, prompt_attention_kernel<64>, a);
-  return cudaLaunchKernelEx(&L.cfg, prompt_attention_kernel<128>, a);
+  const float c = a.sm_scale * kLog2e;
+  const bool mods = a.softcap > 0.f || a.slopes || !(c > 1e-30f && c < 1e30f);
+  if (a.D == 64) return mods ? launch_as<64, true>(a, sms, s) : launch_as<64, false>(a, sms, s);
+  return mods ? launch_as<128, true>(a, sms, s) : launch_as<128, false>(a, sms, s);
 }
 
 }  // namespace moe
