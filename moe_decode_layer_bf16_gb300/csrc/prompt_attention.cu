@@ -59,24 +59,10 @@ struct Cfg {
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kRing = 2 * kTileBytes;  // behind the two query tiles
   static constexpr int kBars = kRing + kStages * kTileBytes;
-  static constexpr int kSmem = kBars + 1024 + 512;  // (aligned by hand)
+  static constexpr int kSmem = kBars + 1024 + 768;  // (aligned by hand)
 };
 static_assert(Cfg<128>::kStages <= 2 * kLooks && Cfg<64>::kStages <= 2 * kLooks, "barriers of values looked through");
 static_assert(Cfg<128>::kSmem <= 232448 && Cfg<64>::kSmem <= 232448, "shared memory of a CTA");
-
-struct Item {
-  int start, n, row0, head;  // the prompt's first row and length, the item's first packed row, kv head; n = 0: the end
-};
-
-struct Bars {
-  uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
-  uint64_t item_full[kSlots], item_empty[kSlots], v_done[kSlots], v_ok[kLooks];
-  Item item[kSlots];
-  int bad[kSlots];  // the item met infinities or NaN among values that it looked through
-  uint32_t tmem;
-};
-static_assert(sizeof(Bars) <= 512, "room behind the ring");
 
 // The key tiles of a tile of packed rows, and which of them some row does not see in full.
 struct Range {
@@ -87,34 +73,35 @@ struct Range {
     return kKeys * j + kKeys - 1 > tok_lo || (window > 0 && kKeys * j <= tok_hi - window);
   }
 };
-MOE_DEV Range range_of(const Item& it, int t, int G, int window) {
-  Range r;
-  const int r0 = it.row0 + t * kRows, last = it.n * G - 1;
-  if (r0 > last) {
-    r.lo = 1;
-    r.hi = 0;
-    r.tok_lo = r.tok_hi = 0;
-    return r;
+struct Item {
+  int start, n, row0, head;  // the prompt's first row and length, the item's first packed row, kv head; n = 0: the end
+  Range t[2];
+  MOE_DEV int lo() const { return t[0].lo; }
+  MOE_DEV int hi() const { return max(t[0].hi, t[1].hi); }
+  MOE_DEV bool edge(int j, int window) const {
+    return (t[0].has(j) && t[0].edge(j, window)) || (t[1].has(j) && t[1].edge(j, window));
   }
+};
+MOE_DEV Range range_of(int n, int r0, int G, int window) {
+  Range r{1, 0, 0, 0};
+  const int last = n * G - 1;
+  if (r0 > last) return r;
   r.tok_lo = r0 / G;
   r.tok_hi = min(r0 + kRows - 1, last) / G;
   r.lo = window > 0 ? max(0, r.tok_lo - window + 1) / kKeys : 0;
   r.hi = r.tok_hi / kKeys;
   return r;
 }
-struct Pair {
-  Range t[2];
-  int lo, hi;
-  MOE_DEV Pair(const Item& it, int G, int window) {
-    t[0] = range_of(it, 0, G, window);
-    t[1] = range_of(it, 1, G, window);
-    lo = t[0].lo;
-    hi = max(t[0].hi, t[1].hi);
-  }
-  MOE_DEV bool edge(int j, int window) const {
-    return (t[0].has(j) && t[0].edge(j, window)) || (t[1].has(j) && t[1].edge(j, window));
-  }
+
+struct Bars {
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t item_full[kSlots], item_empty[kSlots], v_done[kSlots], v_ok[kLooks];
+  Item item[kSlots];
+  int bad[kSlots];  // the item met infinities or NaN among values that it looked through
+  uint32_t tmem;
 };
+static_assert(sizeof(Bars) <= 768, "room behind the ring");
 
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B bf16, A K-major; B
 // K-major or, for the values, N-major.
@@ -148,6 +135,13 @@ MOE_DEV void tc_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 16 bf16 values, rounded, to 32 bytes of memory
+MOE_DEV void store16(void* to, const float* f) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(pack_bf16(f[0], f[1])),
+               "r"(pack_bf16(f[2], f[3])), "r"(pack_bf16(f[4], f[5])), "r"(pack_bf16(f[6], f[7])), "r"(pack_bf16(f[8], f[9])),
+               "r"(pack_bf16(f[10], f[11])), "r"(pack_bf16(f[12], f[13])), "r"(pack_bf16(f[14], f[15]))
+               : "memory");
+}
 MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 MOE_DEV float ex2(float x) {
@@ -162,23 +156,41 @@ MOE_DEV void fma2(float& x, float& y, float c, float d) {
       : "+f"(x), "+f"(y)
       : "f"(c), "f"(d));
 }
+// (x, y) = (x, y) * (u, v) + d
+MOE_DEV void fma2(float& x, float& y, float u, float v, float d) {
+  asm("{\n .reg .b64 a, b, e;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 e, {%4, %4};\n"
+      " fma.rn.f32x2 a, a, b, e;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v), "f"(d));
+}
+MOE_DEV void mul2(float& x, float& y, float u, float v) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v));
+}
 MOE_DEV void add2(float& x, float& y, float c, float d) {
   asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
       : "+f"(x), "+f"(y)
       : "f"(c), "f"(d));
 }
 
-// tanh(z) = 1 - 2 / (1 + e^(2 z)), off by about 2^-23 absolutely; for caps above kFarCap
-// and z below 1/4 the series, whose next term, 62/2835 z^9, is 2^-21 of it there.
-constexpr float kFarCap = 256.f;
-MOE_DEV float tanh_of(float z) {
+// tanh z for |z| < kNear: z times a polynomial in z^2, the interpolation of tanh(z) / z at
+// Chebyshev's nodes of z^2 < kNear^2, off by 4e-9 of it; two at a time.
+constexpr float kNear = 0.625f;
+MOE_DEV void tanh_near2(float& x, float& y) {
+  float u = x, v = y, f = -0.005657135f, g = -0.005657135f;
+  mul2(u, v, x, y);
+  fma2(f, g, u, v, 0.020588191f);
+  fma2(f, g, u, v, -0.05372011f);
+  fma2(f, g, u, v, 0.13331114f);
+  fma2(f, g, u, v, -0.33333260f);
+  fma2(f, g, u, v, 1.f);
+  mul2(x, y, f, g);
+}
+// tanh z = 1 - 2 / (1 + e^(2 z)): off by 2^-21 of it from kNear on
+MOE_DEV float tanh_far(float z) {
   const float y = z * (2.f * kLog2e);
   return 1.f - __fdividef(2.f, 1.f + ex2(y > 80.f ? 80.f : y));  // (2^y stays finite, a NaN stays one)
-}
-MOE_DEV float tanh_far(float z) {
-  const float z2 = z * z;
-  const float t = z * fmaf(z2, fmaf(z2, fmaf(z2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
-  return fabsf(z) < 0.25f ? t : tanh_of(z);
 }
 
 // Whether one of two bf16 values is infinite or NaN, as bits 15 and 31.
@@ -192,10 +204,9 @@ MOE_DEV uint32_t finite_or_zero(uint32_t w) {
 // columns from c0) gets them back.
 template <int D>
 __device__ __noinline__ void put_back(const PromptArgs& p, Item it, int t, int tok, int c0, float* o) {
-  const Pair pr(it, p.G, p.window);
-  const Range r = pr.t[t];
+  const Range r = it.t[t];
   for (int j = r.lo; j <= r.hi; ++j) {
-    if (!pr.edge(j, p.window)) continue;
+    if (!it.edge(j, p.window)) continue;
     const int k0 = max(kKeys * j, p.window > 0 ? tok - p.window + 1 : 0), k1 = min(kKeys * j + kKeys - 1, tok);
     for (int k = k0; k <= k1; ++k) {
       const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.v) +
@@ -271,13 +282,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2;
     const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + quad + 128 * t, to = tmem + quad + 256 + 128 * t;
-    const float c = kMods ? kLog2e : p.sm_scale * kLog2e;
+    const float c = kMods ? 1.f : p.sm_scale * kLog2e;
     const int heads = G * p.kv_heads;
     uint32_t steps = 0, dones = 0;
     Item it;
     for (int k = 0; item(k, &it); ++k) {
-      const Pair pr(it, G, window);
-      const Range rg = pr.t[t];
+      const Range rg = it.t[t];
       if (rg.lo > rg.hi) {
         item_done(k);
         continue;
@@ -285,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = it.row0 + t * kRows + 32 * (warp & 3) + lane;
       const bool live = row < it.n * G;
       const int tok = min(row / G, it.n - 1), head = it.head * G + (live ? row - row / G * G : 0);
-      const float slope = kMods && p.slopes ? p.slopes[head] : 0.f;
+      const float slope = kMods && p.slopes ? p.slopes[head] * kLog2e : 0.f;
       float m = -INFINITY, mc = 0.f, l0 = 0.f, l1 = 0.f;  // maximum in use, times c; two halves of the sum
       bool alive = true;
       for (int j = rg.lo; j <= rg.hi; ++j, ++steps) {
@@ -295,22 +305,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kKeys; i += 32) tc_ld32(ts + i, s + i);
         tc_wait_ld();
-        if constexpr (kMods) {
-          const float gap0 = (float)(kKeys * j - tok);
-          const float cap = p.softcap, cap_in = cap > 0.f ? p.sm_scale / cap : 0.f;
-          if (cap > kFarCap) {
+        if constexpr (kMods) {  // the scores, times log2 e
+          const float cap = p.softcap;
+          if (cap > 0.f) {
+            const float in = p.sm_scale / cap, out = cap * kLog2e;
+            float far = 0.f;
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] = cap * tanh_far(s[i] * cap_in);
-          } else if (cap > 0.f) {
+            for (int i = 0; i < kKeys; i += 2) {
+              mul2(s[i], s[i + 1], in, in);
+              far = fmaxf(far, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
+            }
+            if (__any_sync(0xffffffffu, far >= kNear)) {
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] = cap * tanh_of(s[i] * cap_in);
+              for (int i = 0; i < kKeys; i += 2) {
+                const float x = tanh_far(s[i]), y = tanh_far(s[i + 1]);
+                const bool fx = !(fabsf(s[i]) < kNear), fy = !(fabsf(s[i + 1]) < kNear);
+                tanh_near2(s[i], s[i + 1]);
+                s[i] = fx ? x : s[i];
+                s[i + 1] = fy ? y : s[i + 1];
+                mul2(s[i], s[i + 1], out, out);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < kKeys; i += 2) {
+                tanh_near2(s[i], s[i + 1]);
+                mul2(s[i], s[i + 1], out, out);
+              }
+            }
           } else {
+            const float scale = p.sm_scale * kLog2e;
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] *= p.sm_scale;
+            for (int i = 0; i < kKeys; i += 2) mul2(s[i], s[i + 1], scale, scale);
           }
           if (p.slopes) {
+            const float gap = (float)(kKeys * j - tok);
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] = fmaf(slope, gap0 + (float)i, s[i]);
+            for (int i = 0; i < kKeys; i += 2) {
+              float x = (float)i, y = (float)(i + 1);
+              add2(x, y, gap, gap);  // (exact)
+              mul2(x, y, slope, slope);
+              add2(s[i], s[i + 1], x, y);
+            }
           }
         }
         if (rg.edge(j, window)) {
@@ -372,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool bad = b.bad[k % kSlots] != 0;
       const float l = l0 + l1, inv = 1.f / l;
       const size_t at = (size_t)(it.start + tok) * heads + head;
-      uint4* out = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at * D);
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at * D;
 #pragma unroll
       for (int i = 0; i < D; i += 32) {
         float o[32];
@@ -382,10 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 32; ++e) o[e] *= inv;
         if (bad && live) put_back<D>(p, it, t, tok, i, o);
         if (live) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            out[(i + e) / 8] = make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]),
-                                          pack_bf16(o[e + 4], o[e + 5]), pack_bf16(o[e + 6], o[e + 7]));
+          store16(out + i, o);
+          store16(out + i + 16, o + 16);
         }
       }
       if (p.lse && live) p.lse[at] = (mc + log2f(l)) * kLn2;
@@ -404,20 +437,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto landed = [&](uint32_t n) { return mbar_wait_landed(b.kv_full + n % C::kStages, n / C::kStages & 1, status); };
         Item it;
         for (int k = 0; alive && item(k, &it); ++k) {
-          const Pair pr(it, G, window);
-          for (int j = pr.lo; alive && j <= pr.hi + 1; ++j) {
-            const uint32_t nk = ring + 2 * (j - pr.lo), nv = nk - 1;  // ring places of this step's keys and of the last one's values
-            if (j > pr.lo) {
+          const int lo = it.lo(), hi = it.hi();
+          for (int j = lo; alive && j <= hi + 1; ++j) {
+            const uint32_t nk = ring + 2 * (j - lo), nv = nk - 1;  // ring places of this step's keys and of the last one's values
+            if (j > lo) {
               if (!landed(nv)) { alive = false; break; }
-              if (pr.edge(j - 1, window)) {
+              if (it.edge(j - 1, window)) {
                 if (!mbar_wait_landed(b.v_ok + edges % kLooks, edges / kLooks & 1, status)) { alive = false; break; }
                 ++edges;
               }
             }
-            if (j <= pr.hi && !landed(nk)) { alive = false; break; }
+            if (j <= hi && !landed(nk)) { alive = false; break; }
             for (int t = 0; t < 2; ++t) {
-              const Range& r = pr.t[t];
-              if (j > pr.lo && r.has(j - 1)) {
+              const Range& r = it.t[t];
+              if (j > lo && r.has(j - 1)) {
                 if (!mbar_wait_landed(b.p_full + t, pp[t]++ & 1, status)) { alive = false; break; }
                 tc_fence_after();
                 const uint64_t dv = n_major_desc(stage(nv));
@@ -426,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          j - 1 > r.lo || s > 0);
                 if (j - 1 == r.hi) tc_commit(b.o_full + t);
               }
-              if (j <= pr.hi && r.has(j)) {
+              if (j <= hi && r.has(j)) {
                 if (j == r.lo) {
                   if (!mbar_wait_landed(b.q_full + t, pq[t]++ & 1, status)) { alive = false; break; }
                   tc_fence_after();
@@ -441,10 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (!alive) break;
-            if (j > pr.lo) tc_commit(b.kv_empty + nv % C::kStages);
-            if (j <= pr.hi) tc_commit(b.kv_empty + nk % C::kStages);
+            if (j > lo) tc_commit(b.kv_empty + nv % C::kStages);
+            if (j <= hi) tc_commit(b.kv_empty + nk % C::kStages);
           }
-          ring += 2 * (pr.hi - pr.lo + 1);
+          ring += 2 * (hi - lo + 1);
           if (alive) mbar_arrive(b.item_empty + k % kSlots);
         }
       }
@@ -478,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const bool end = b0 >= p.B;
-        Item it{0, 0, 0, 0};
+        Item it{};
         if (!end) {
           const int at = next - before;
           const int who = __popc(__ballot_sync(0xffffffffu, upto <= at));
@@ -489,6 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int blocks = (it.n * G + 2 * kRows - 1) / (2 * kRows);
           it.row0 = (blocks - 1 - idx / p.kv_heads) * 2 * kRows;
           it.head = idx % p.kv_heads;
+          it.t[0] = range_of(it.n, it.row0, G, window);
+          it.t[1] = range_of(it.n, it.row0 + kRows, G, window);
         }
         if (!mbar_wait_landed(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status)) break;
         if (lane == 0) {
@@ -498,9 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (end) break;
-        const Pair pr(it, G, window);
         if (elect_one()) {
-          for (int j = pr.lo; j <= pr.hi; ++j) {
+          for (int j = it.lo(); j <= it.hi(); ++j) {
             for (int kv = 0; kv < 2; ++kv, ++ring) {
               const uint32_t st = ring % C::kStages;
               if (!mbar_wait_landed(b.kv_empty + st, (ring / C::kStages & 1) ^ 1, status)) { alive = false; break; }
@@ -529,23 +563,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       Item it;
       for (int k = 0; alive && item(k, &it); ++k) {
-        const Pair pr(it, G, window);
-        const Range& r = pr.t[t];
-        if (r.lo <= r.hi) {
+        if (it.t[t].lo <= it.t[t].hi) {
           if (!mbar_wait_landed(b.q_empty + t, (fills & 1) ^ 1, status)) break;
           ++fills;
-          const int rows = it.n * G, ch = lane % kChunks;
-          int row = it.row0 + t * kRows + lane / kChunks;
-          int tok = row / G, g = row - tok * G;
-          const uint32_t to = su32(smem) + t * C::kTileBytes + ch / 8 * kBox;
-          for (int i = lane / kChunks; i < kRows; i += 32 / kChunks, row += 32 / kChunks) {
-            const bool in = row < rows;
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (long long)(it.start + (in ? tok : 0)) * p.q_stride +
-                                  (size_t)(it.head * G + (in ? g : 0)) * D + ch * 8;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 128 + ((ch % 8 ^ (i & 7)) << 4)), "l"(src),
-                         "r"(in ? 16 : 0)
+          // a pass of the warp is kStep rows; a row's step to the next pass is some tokens and heads
+          constexpr int kStep = 32 / kChunks;
+          const int ch = lane % kChunks, r0 = lane / kChunks, row = it.row0 + t * kRows + r0;
+          const int left = it.n * G - it.row0 - t * kRows;  // rows of the tile (it may be over)
+          const int tok = row / G, toks = kStep / G, more = kStep - toks * G;
+          int g = row - tok * G;
+          const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (long long)(it.start + tok) * p.q_stride +
+                                (size_t)(it.head * G + g) * D + ch * 8;
+          const long long step = toks * p.q_stride + more * D, wrap = p.q_stride - G * D;
+          const uint32_t to = su32(smem) + t * C::kTileBytes + ch / 8 * kBox + r0 * 128;
+#pragma unroll 8
+          for (int i = 0; i < kRows; i += kStep) {
+            const bool in = r0 + i < left;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 128 + ((ch % 8 ^ ((r0 + i) & 7)) << 4)),
+                         "l"(in ? src : reinterpret_cast<const uint16_t*>(p.q)), "r"(in ? 16 : 0)
                          : "memory");
-            for (g += 32 / kChunks; g >= G; g -= G) ++tok;
+            src += step;
+            g += more;
+            if (g >= G) {
+              g -= G;
+              src += wrap;
+            }
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -554,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every tile of the ring is waited for and given back in turn: a wait that skips one
         // could not tell its phase from the last but one
-        for (int i = 0; alive && i < 2 * (pr.hi - pr.lo + 1); ++i, ++ring) {
+        for (int i = 0; alive && i < 2 * (it.hi() - it.lo() + 1); ++i, ++ring) {
           const uint32_t st = ring % C::kStages;
           if (!mbar_wait_landed(b.kv_full + st, ring / C::kStages & 1, status)) { alive = false; break; }
-          if (!(i & 1) || !pr.edge(pr.lo + i / 2, window)) {
+          if (!(i & 1) || !it.edge(it.lo() + i / 2, window)) {
             __syncwarp();
             if (lane == 0) mbar_arrive(b.kv_empty + st);
             continue;
@@ -628,7 +670,10 @@ cudaError_t launch_as(const PromptArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_prompt_attention(const PromptArgs& args, int sms, cudaStream_t s) {
+  PromptArgs a = args;
+  // (a cap's inverse, and the cap times log2 e, stay finite; no score comes near either end)
+  if (a.softcap > 0.f) a.softcap = std::min(std::max(a.softcap, 0x1p-100f), 0x1p100f);
   const float c = a.sm_scale * kLog2e;
   const bool mods = a.softcap > 0.f || a.slopes || !(c > 1e-30f && c < 1e30f);
   if (a.D == 64) return mods ? launch_as<64, true>(a, sms, s) : launch_as<64, false>(a, sms, s);
