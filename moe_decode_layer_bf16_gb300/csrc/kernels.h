@@ -338,6 +338,7 @@ struct PromptArgs {
   float sm_scale, softcap;
   int* status;
   int* tickets;
+  int rows;  // packed rows of a tile (the launch's)
 };
 cudaError_t launch_prompt_attention(const PromptArgs& a, int sms, cudaStream_t s);
 

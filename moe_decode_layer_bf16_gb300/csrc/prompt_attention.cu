@@ -30,6 +30,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "async.cuh"
 #include "common.cuh"
@@ -42,13 +43,30 @@ namespace moe {
 
 namespace {
 
+// mbar_wait_landed for waits that are often long: the thread sleeps up to a millisecond at a
+// time, where one that asks again and again takes its scheduler's slots from the softmax (a
+// serving mix 189 -> 177 us).
+MOE_DEV bool wait(uint64_t* bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  do {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(su32(bar)), "r"(parity), "r"(1000000u) : "memory");
+    if (ok) return true;
+  } while (globaltimer_ns() - t0 < kWaitNs);
+  atomicExch(status, MOE_ERR_DEVICE_TIMEOUT);
+  return false;
+}
+
 constexpr int kKeys = 128;    // keys of a tile
 constexpr int kRows = 128;    // packed rows of a tile
 constexpr int kBox = 128 * kKeys;  // bytes of 64 columns of 128 rows
 constexpr int kSlots = 4;     // items handed out ahead
 constexpr int kLooks = 4;     // tiles of values in the ring at most
 constexpr int kThreads = 384;
-constexpr int kMma = 8, kCopy = 9, kHelp = 10;  // warps
+constexpr int kMma = 8, kCopy = 9, kHelp = 10;  // warps (the softmax's are the first eight)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that is let pass
 
@@ -82,22 +100,32 @@ struct Item {
     return (t[0].has(j) && t[0].edge(j, window)) || (t[1].has(j) && t[1].edge(j, window));
   }
 };
-MOE_DEV Range range_of(int n, int r0, int G, int window) {
+MOE_DEV Range range_of(int n, int r0, int rows, int G, int window) {
   Range r{1, 0, 0, 0};
   const int last = n * G - 1;
   if (r0 > last) return r;
   r.tok_lo = r0 / G;
-  r.tok_hi = min(r0 + kRows - 1, last) / G;
+  r.tok_hi = min(r0 + rows - 1, last) / G;
   r.lo = window > 0 ? max(0, r.tok_lo - window + 1) / kKeys : 0;
   r.hi = r.tok_hi / kKeys;
   return r;
 }
 
+// What the MMA warp does with a key tile: a word beside its place in the ring, for tile t:
+enum Command : uint32_t {
+  kHas = 1,       // << t: the tile takes part
+  kFirst = 4,     // << t: it is its first
+  kLast = 16,     // << t: and its last
+  kEdge = 64,     // the values are looked through before they are used
+  kEnd = 128      // no more items
+};
+
 struct Bars {
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
   uint64_t item_full[kSlots], item_empty[kSlots], v_done[kSlots], v_ok[kLooks];
   Item item[kSlots];
+  uint32_t cmd[8];
   int bad[kSlots];  // the item met infinities or NaN among values that it looked through
   uint32_t tmem;
 };
@@ -193,6 +221,51 @@ MOE_DEV float tanh_far(float z) {
   return 1.f - __fdividef(2.f, 1.f + ex2(y > 80.f ? 80.f : y));  // (2^y stays finite, a NaN stays one)
 }
 
+// A row's scores capped and biased, times log2 e; gap: the first one's key minus the row.
+template <int N>
+MOE_DEV void modified(const PromptArgs& p, float* s, float slope, float gap) {
+  const float cap = p.softcap;
+  if (cap > 0.f) {
+    const float in = p.sm_scale / cap, out = cap * kLog2e;
+    float far = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      mul2(s[i], s[i + 1], in, in);
+      far = fmaxf(far, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
+    }
+    if (__any_sync(0xffffffffu, far >= kNear)) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float x = tanh_far(s[i]), y = tanh_far(s[i + 1]);
+        const bool fx = !(fabsf(s[i]) < kNear), fy = !(fabsf(s[i + 1]) < kNear);
+        tanh_near2(s[i], s[i + 1]);
+        s[i] = fx ? x : s[i];
+        s[i + 1] = fy ? y : s[i + 1];
+        mul2(s[i], s[i + 1], out, out);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        tanh_near2(s[i], s[i + 1]);
+        mul2(s[i], s[i + 1], out, out);
+      }
+    }
+  } else {
+    const float scale = p.sm_scale * kLog2e;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) mul2(s[i], s[i + 1], scale, scale);
+  }
+  if (p.slopes) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      float x = (float)i, y = (float)(i + 1);
+      add2(x, y, gap, gap);  // (exact)
+      mul2(x, y, slope, slope);
+      add2(s[i], s[i + 1], x, y);
+    }
+  }
+}
+
 // Whether one of two bf16 values is infinite or NaN, as bits 15 and 31.
 MOE_DEV uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 MOE_DEV uint32_t finite_or_zero(uint32_t w) {
@@ -200,24 +273,20 @@ MOE_DEV uint32_t finite_or_zero(uint32_t w) {
   return w & ~((b >> 15) * 0xffffu);
 }
 
-// The rows that see one of the prompt's infinities or NaN that were replaced: o (32
-// columns from c0) gets them back.
+// A row that sees one of the prompt's infinities or NaN that were replaced gets them back.
 template <int D>
-__device__ __noinline__ void put_back(const PromptArgs& p, Item it, int t, int tok, int c0, float* o) {
-  const Range r = it.t[t];
+__device__ __noinline__ void put_back(const PromptArgs& p, const Item& it, int t, int tok, __nv_bfloat16* out) {
+  const Range& r = it.t[t];
   for (int j = r.lo; j <= r.hi; ++j) {
     if (!it.edge(j, p.window)) continue;
     const int k0 = max(kKeys * j, p.window > 0 ? tok - p.window + 1 : 0), k1 = min(kKeys * j + kKeys - 1, tok);
     for (int k = k0; k <= k1; ++k) {
-      const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.v) +
-                                                      (long long)(it.start + k) * p.v_stride + (size_t)it.head * D + c0);
-      for (int c = 0; c < 4; ++c) {
-        const uint4 x = __ldcg(v + c);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        for (int e = 0; e < 4; ++e) {
-          if (not_finite(w[e]) & 0x8000u) o[8 * c + 2 * e] += bf16_lo(w[e]);
-          if (not_finite(w[e]) >> 31) o[8 * c + 2 * e + 1] += bf16_hi(w[e]);
-        }
+      const uint32_t* v = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(p.v) +
+                                                            (long long)(it.start + k) * p.v_stride + (size_t)it.head * D);
+      for (int c = 0; c < D / 2; ++c) {
+        const uint32_t w = __ldcg(v + c), b = not_finite(w);
+        if (b & 0x8000u) out[2 * c] = __float2bfloat16(__bfloat162float(out[2 * c]) + bf16_lo(w));
+        if (b >> 31) out[2 * c + 1] = __float2bfloat16(__bfloat162float(out[2 * c + 1]) + bf16_hi(w));
       }
     }
   }
@@ -226,7 +295,8 @@ __device__ __noinline__ void put_back(const PromptArgs& p, Item it, int t, int t
 // kMods: scores are capped or biased (or the scale is not positive).
 template <int D, bool kMods>
 __global__ void __launch_bounds__(kThreads, 1)
-    prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                            const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
@@ -242,12 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(b.q_full + t, 1);
       mbar_init(b.q_empty + t, 1);
       mbar_init(b.s_full + t, 1);
-      mbar_init(b.p_full + t, 4);
+      mbar_init(b.p_full[t], 4);
+      mbar_init(b.p_full[t] + 1, 4);
       mbar_init(b.o_full + t, 1);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(b.item_full + i, 1);
-      mbar_init(b.item_empty + i, 11);  // eight softmax warps, the MMA warp, two helpers
+      mbar_init(b.item_empty + i, 10);  // eight softmax warps, two helpers
       mbar_init(b.v_done + i, 2);
     }
     for (int i = 0; i < kLooks; ++i) mbar_init(b.v_ok + i, 2);
@@ -261,13 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = b.tmem;  // S (and P) of tile t at 128 t, O at 256 + 128 t
+  // All of tensor memory is this CTA's, so it starts at 0: S (and P) of tile t at 128 t, O at 256 + 128 t.
+  constexpr uint32_t tmem = 0;
   grid_dep_wait();
   const int G = p.G, window = p.window;
 
   // The k-th item of this CTA: every role but the copying warp, which makes them.
   auto item = [&](int k, Item* it) {
-    if (!mbar_wait_landed(b.item_full + k % kSlots, (k / kSlots) & 1, status)) return false;
+    if (!wait(b.item_full + k % kSlots, (k / kSlots) & 1, status)) return false;
     *it = b.item[k % kSlots];
     return it->n > 0;
   };
@@ -284,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + quad + 128 * t, to = tmem + quad + 256 + 128 * t;
     const float c = kMods ? 1.f : p.sm_scale * kLog2e;
     const int heads = G * p.kv_heads;
-    uint32_t steps = 0, dones = 0;
+    uint32_t steps = 0, items = 0;
     Item it;
     for (int k = 0; item(k, &it); ++k) {
       const Range rg = it.t[t];
@@ -292,119 +364,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         item_done(k);
         continue;
       }
-      const int row = it.row0 + t * kRows + 32 * (warp & 3) + lane;
-      const bool live = row < it.n * G;
+      const int r = 32 * (warp & 3) + lane, row = it.row0 + t * p.rows + r;
+      const bool live = r < p.rows && row < it.n * G;
       const int tok = min(row / G, it.n - 1), head = it.head * G + (live ? row - row / G * G : 0);
       const float slope = kMods && p.slopes ? p.slopes[head] * kLog2e : 0.f;
       float m = -INFINITY, mc = 0.f, l0 = 0.f, l1 = 0.f;  // maximum in use, times c; two halves of the sum
       bool alive = true;
+      // a tile's maximum is mt: the maximum in use follows where some row's grows by much
+      auto grow = [&](float mt, bool some) {
+        if (!__any_sync(0xffffffffu, (mt - m) * c > kGrow)) return;
+        const float mn = fmaxf(m, mt), mcn = mn == -INFINITY ? 0.f : mn * c;
+        const float f = m == -INFINITY ? 0.f : ex2(mc - mcn);
+        l0 *= f;
+        l1 *= f;
+        if (some) {  // (this tile's products so far were complete before S was)
+#pragma unroll
+          for (int i = 0; i < D; i += 16) {
+            float o[16];
+            tc_ld16(to + i, o);
+            tc_wait_ld();
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+            tc_st16(to + i, w);
+          }
+        }
+        m = mn;
+        mc = mcn;
+      };
+      // 32 scores' weights to tensor memory
+      auto weights = [&](const float* s, uint32_t at) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x = s[e], y = s[e + 1];
+          fma2(x, y, c, -mc);
+          x = ex2(x);
+          y = ex2(y);
+          add2(l0, l1, x, y);
+          w[e / 2] = pack_bf16(x, y);
+        }
+        tc_st16(at, w);
+      };
       for (int j = rg.lo; j <= rg.hi; ++j, ++steps) {
-        if (!mbar_wait_landed(b.s_full + t, steps & 1, status)) { alive = false; break; }
+        if (!wait(b.s_full + t, steps & 1, status)) { alive = false; break; }
         tc_fence_after();
         float s[kKeys];
 #pragma unroll
         for (int i = 0; i < kKeys; i += 32) tc_ld32(ts + i, s + i);
         tc_wait_ld();
-        if constexpr (kMods) {  // the scores, times log2 e
-          const float cap = p.softcap;
-          if (cap > 0.f) {
-            const float in = p.sm_scale / cap, out = cap * kLog2e;
-            float far = 0.f;
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 2) {
-              mul2(s[i], s[i + 1], in, in);
-              far = fmaxf(far, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
-            }
-            if (__any_sync(0xffffffffu, far >= kNear)) {
-#pragma unroll
-              for (int i = 0; i < kKeys; i += 2) {
-                const float x = tanh_far(s[i]), y = tanh_far(s[i + 1]);
-                const bool fx = !(fabsf(s[i]) < kNear), fy = !(fabsf(s[i + 1]) < kNear);
-                tanh_near2(s[i], s[i + 1]);
-                s[i] = fx ? x : s[i];
-                s[i + 1] = fy ? y : s[i + 1];
-                mul2(s[i], s[i + 1], out, out);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kKeys; i += 2) {
-                tanh_near2(s[i], s[i + 1]);
-                mul2(s[i], s[i + 1], out, out);
-              }
-            }
-          } else {
-            const float scale = p.sm_scale * kLog2e;
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 2) mul2(s[i], s[i + 1], scale, scale);
-          }
-          if (p.slopes) {
-            const float gap = (float)(kKeys * j - tok);
-#pragma unroll
-            for (int i = 0; i < kKeys; i += 2) {
-              float x = (float)i, y = (float)(i + 1);
-              add2(x, y, gap, gap);  // (exact)
-              mul2(x, y, slope, slope);
-              add2(s[i], s[i + 1], x, y);
-            }
-          }
-        }
+        if constexpr (kMods) modified<kKeys>(p, s, slope, (float)(kKeys * j - tok));
         if (rg.edge(j, window)) {
-          const int last = tok - kKeys * j, first = window > 0 ? last - window + 1 : 0;
+          const int last = tok - kKeys * j;
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) s[i] = i <= last && i >= first ? s[i] : -INFINITY;
+          for (int i = 0; i < kKeys; ++i) s[i] = i <= last ? s[i] : -INFINITY;
+          if (window > 0 && last >= window) {
+            const int first = last - window + 1;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) s[i] = i >= first ? s[i] : -INFINITY;
+          }
         }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < kKeys; i += 4)
+        for (int i = 4; i < kKeys; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
+        grow(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), j > rg.lo);
+        // the weights, in two halves: the products of the first run while the second is made
 #pragma unroll
-          for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], s[i + e]);
-        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (__any_sync(0xffffffffu, (mt - m) * c > kGrow)) {
-          const float mn = fmaxf(m, mt), mcn = mn == -INFINITY ? 0.f : mn * c;
-          const float f = m == -INFINITY ? 0.f : ex2(mc - mcn);
-          l0 *= f;
-          l1 *= f;
-          if (j > rg.lo) {  // (this tile's products so far were complete before S was)
-#pragma unroll
-            for (int i = 0; i < D; i += 16) {
-              float o[16];
-              tc_ld16(to + i, o);
-              tc_wait_ld();
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-              tc_st16(to + i, w);
-            }
-          }
-          m = mn;
-          mc = mcn;
+        for (int h = 0; h < 2; ++h) {
+          weights(s + 64 * h, ts + 32 * h);
+          weights(s + 64 * h + 32, ts + 32 * h + 16);
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b.p_full[t] + h);
         }
-#pragma unroll
-        for (int i = 0; i < kKeys; i += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float x = s[i + e], y = s[i + e + 1];
-            fma2(x, y, c, -mc);
-            x = ex2(x);
-            y = ex2(y);
-            add2(l0, l1, x, y);
-            w[e / 2] = pack_bf16(x, y);
-          }
-          tc_st16(ts + i / 2, w);
-        }
-        tc_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b.p_full + t);
       }
       if (!alive) break;
       // ---------------------------------------------------------------- the rows' results
-      if (!mbar_wait_landed(b.o_full + t, dones & 1, status)) break;
-      ++dones;
+      if (!wait(b.o_full + t, items++ & 1, status)) break;
       tc_fence_after();
-      if (!mbar_wait_landed(b.v_done + k % kSlots, (k / kSlots) & 1, status)) break;
-      const bool bad = b.bad[k % kSlots] != 0;
       const float l = l0 + l1, inv = 1.f / l;
       const size_t at = (size_t)(it.start + tok) * heads + head;
       uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at * D;
@@ -415,14 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] *= inv;
-        if (bad && live) put_back<D>(p, it, t, tok, i, o);
         if (live) {
           store16(out + i, o);
           store16(out + i + 16, o + 16);
         }
       }
-      if (p.lse && live) p.lse[at] = (mc + log2f(l)) * kLn2;
       tc_fence_before();
+      if (p.lse && live) p.lse[at] = (mc + log2f(l)) * kLn2;
+      if (!wait(b.v_done + k % kSlots, (k / kSlots) & 1, status)) break;
+      if (b.bad[k % kSlots] && live) put_back<D>(p, b.item[k % kSlots], t, tok, reinterpret_cast<__nv_bfloat16*>(out));
       item_done(k);
     }
   } else {
@@ -430,55 +469,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMma) {
       // ================================================================ MMA
       if (elect_one()) {
-        uint32_t ring = 0, edges = 0, pq[2] = {0, 0}, pp[2] = {0, 0};
-        bool alive = true;
+        // What the MMAs take is made of constants and of counters that only this thread moves,
+        // so that it stays in uniform registers.
+        uint32_t edges = 0, pq = 0, pp = 0;  // phases of the two tiles' barriers, a bit each
         const uint32_t sq = su32(smem), sring = su32(smem + C::kRing);
-        auto stage = [&](uint32_t n) { return sring + n % C::kStages * C::kTileBytes; };
-        auto landed = [&](uint32_t n) { return mbar_wait_landed(b.kv_full + n % C::kStages, n / C::kStages & 1, status); };
-        Item it;
-        for (int k = 0; alive && item(k, &it); ++k) {
-          const int lo = it.lo(), hi = it.hi();
-          for (int j = lo; alive && j <= hi + 1; ++j) {
-            const uint32_t nk = ring + 2 * (j - lo), nv = nk - 1;  // ring places of this step's keys and of the last one's values
-            if (j > lo) {
-              if (!landed(nv)) { alive = false; break; }
-              if (it.edge(j - 1, window)) {
-                if (!mbar_wait_landed(b.v_ok + edges % kLooks, edges / kLooks & 1, status)) { alive = false; break; }
-                ++edges;
-              }
+        struct Place {
+          uint32_t st = 0, ph = 0;
+          MOE_DEV void next() {
+            if (++st == C::kStages) {
+              st = 0;
+              ph ^= 1;
             }
-            if (j <= hi && !landed(nk)) { alive = false; break; }
-            for (int t = 0; t < 2; ++t) {
-              const Range& r = it.t[t];
-              if (j > lo && r.has(j - 1)) {
-                if (!mbar_wait_landed(b.p_full + t, pp[t]++ & 1, status)) { alive = false; break; }
-                tc_fence_after();
-                const uint64_t dv = n_major_desc(stage(nv));
-                for (int s = 0; s < kKeys / 16; ++s)
-                  mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * s, dv + (uint64_t)(s * (2048 >> 4)), bf16_desc(D, true),
-                         j - 1 > r.lo || s > 0);
-                if (j - 1 == r.hi) tc_commit(b.o_full + t);
-              }
-              if (j <= hi && r.has(j)) {
-                if (j == r.lo) {
-                  if (!mbar_wait_landed(b.q_full + t, pq[t]++ & 1, status)) { alive = false; break; }
-                  tc_fence_after();
-                }
-                const uint64_t dq = smem_desc(sq + t * C::kTileBytes), dk = smem_desc(stage(nk));
-                for (int s = 0; s < D / 16; ++s) {
-                  const uint64_t step = (uint64_t)((s / 4 * kBox + s % 4 * 32) >> 4);
-                  mma_ss(tmem + 128 * t, dq + step, dk + step, bf16_desc(kKeys, false), s > 0);
-                }
-                tc_commit(b.s_full + t);
-                if (j == r.hi) tc_commit(b.q_empty + t);
-              }
-            }
-            if (!alive) break;
-            if (j > lo) tc_commit(b.kv_empty + nv % C::kStages);
-            if (j <= hi) tc_commit(b.kv_empty + nk % C::kStages);
           }
-          ring += 2 * (hi - lo + 1);
-          if (alive) mbar_arrive(b.item_empty + k % kSlots);
+        };
+        auto landed = [&](const Place& n) { return wait(b.kv_full + n.st, n.ph, status); };
+        // O += P V of tile t; V in ring place n
+        auto product = [&](auto tc, const Place& n, uint32_t cmd) {
+          constexpr int t = decltype(tc)::value;
+          const uint64_t dv = n_major_desc(sring + n.st * C::kTileBytes);
+          constexpr uint32_t d = 256 + 128 * t, a = 128 * t, idesc = bf16_desc(D, true);
+          const uint32_t ph = pp >> t & 1;
+          pp ^= 1u << t;
+          if (!wait(b.p_full[t], ph, status)) return false;
+          tc_fence_after();
+          mma_ts(d, a, dv, idesc, cmd & (kFirst << t) ? 0 : 1);
+#pragma unroll
+          for (int s = 1; s < kKeys / 32; ++s) mma_ts(d, a + 8 * s, dv + (uint64_t)(s * (2048 >> 4)), idesc, 1);
+          if (!wait(b.p_full[t] + 1, ph, status)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int s = kKeys / 32; s < kKeys / 16; ++s) mma_ts(d, a + 8 * s, dv + (uint64_t)(s * (2048 >> 4)), idesc, 1);
+          if (cmd & (kLast << t)) tc_commit(b.o_full + t);
+          return true;
+        };
+        // S = Q K^T of tile t; K in ring place n
+        auto scores = [&](auto tc, const Place& n, uint32_t cmd) {
+          constexpr int t = decltype(tc)::value;
+          if (cmd & (kFirst << t)) {
+            if (!wait(b.q_full + t, pq >> t & 1, status)) return false;
+            pq ^= 1u << t;
+            tc_fence_after();
+          }
+          const uint64_t dq = smem_desc(sq + t * C::kTileBytes), dk = smem_desc(sring + n.st * C::kTileBytes);
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint64_t at = (uint64_t)((s / 4 * kBox + s % 4 * 32) >> 4);
+            mma_ss(128 * t, dq + at, dk + at, bf16_desc(kKeys, false), s > 0);
+          }
+          tc_commit(b.s_full + t);
+          if (cmd & (kLast << t)) tc_commit(b.q_empty + t);
+          return true;
+        };
+        using T0 = std::integral_constant<int, 0>;
+        using T1 = std::integral_constant<int, 1>;
+        // A step is a key tile of an item: its scores, with the products of the step before
+        // (whose item may be another one).
+        uint32_t cmd = 0, old = 0;
+        Place key, val;
+        while (true) {
+          bool early = false;
+          if (old) {
+            if (!landed(val)) break;
+            if (old & kEdge) {
+              if (!wait(b.v_ok + edges % kLooks, edges / kLooks & 1, status)) break;
+              ++edges;
+            }
+            if ((old & kHas) && !product(T0(), val, old)) break;
+            // tile 0's scores come between the products where their data are there
+            if (mbar_try_wait(b.kv_full + key.st, key.ph)) {
+              cmd = b.cmd[key.st];
+              early = (cmd & kHas) && (!(cmd & kFirst) || mbar_try_wait(b.q_full, pq & 1));
+              if (early && !scores(T0(), key, cmd)) break;
+            }
+            if ((old & (kHas << 1)) && !product(T1(), val, old)) break;
+            tc_commit(b.kv_empty + val.st);
+          }
+          if (!landed(key)) break;
+          cmd = b.cmd[key.st];
+          if (cmd & kEnd) break;
+          if ((cmd & kHas) && !early && !scores(T0(), key, cmd)) break;
+          if ((cmd & (kHas << 1)) && !scores(T1(), key, cmd)) break;
+          tc_commit(b.kv_empty + key.st);
+          old = cmd;
+          val = key;
+          val.next();
+          key = val;
+          key.next();
         }
       }
       __syncwarp();
@@ -503,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (step_rows_ok(start, stop, p.total)) n = stop - start;
             else if (blockIdx.x == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
           }
-          upto = (n * G + 2 * kRows - 1) / (2 * kRows) * p.kv_heads;
+          upto = (n * G + 2 * p.rows - 1) / (2 * p.rows) * p.kv_heads;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -519,25 +595,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.n = __shfl_sync(0xffffffffu, n, who);
           const int prior = __shfl_sync(0xffffffffu, upto, who > 0 ? who - 1 : 0);
           const int idx = at - (who > 0 ? prior : 0);
-          const int blocks = (it.n * G + 2 * kRows - 1) / (2 * kRows);
-          it.row0 = (blocks - 1 - idx / p.kv_heads) * 2 * kRows;
+          const int blocks = (it.n * G + 2 * p.rows - 1) / (2 * p.rows);
+          it.row0 = (blocks - 1 - idx / p.kv_heads) * 2 * p.rows;
           it.head = idx % p.kv_heads;
-          it.t[0] = range_of(it.n, it.row0, G, window);
-          it.t[1] = range_of(it.n, it.row0 + kRows, G, window);
+          it.t[0] = range_of(it.n, it.row0, p.rows, G, window);
+          it.t[1] = range_of(it.n, it.row0 + p.rows, p.rows, G, window);
         }
-        if (!mbar_wait_landed(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status)) break;
+        if (!wait(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status)) break;
         if (lane == 0) {
           b.item[k % kSlots] = it;
           b.bad[k % kSlots] = 0;
           mbar_arrive(b.item_full + k % kSlots);
         }
         __syncwarp();
-        if (end) break;
         if (elect_one()) {
-          for (int j = it.lo(); j <= it.hi(); ++j) {
+          auto command = [&](int j) {
+            uint32_t c = it.edge(j, window) ? kEdge : 0;
+            for (int t = 0; t < 2; ++t)
+              if (it.t[t].has(j))
+                c |= (kHas | (j == it.t[t].lo ? kFirst : 0) | (j == it.t[t].hi ? kLast : 0)) << t;
+            return c;
+          };
+          if (end) {
+            const uint32_t st = ring % C::kStages;
+            if (wait(b.kv_empty + st, (ring / C::kStages & 1) ^ 1, status)) {
+              b.cmd[st] = kEnd;
+              mbar_arrive(b.kv_full + st);
+            }
+          }
+          for (int j = it.lo(); !end && j <= it.hi(); ++j) {
             for (int kv = 0; kv < 2; ++kv, ++ring) {
               const uint32_t st = ring % C::kStages;
-              if (!mbar_wait_landed(b.kv_empty + st, (ring / C::kStages & 1) ^ 1, status)) { alive = false; break; }
+              if (!wait(b.kv_empty + st, (ring / C::kStages & 1) ^ 1, status)) { alive = false; break; }
+              if (!kv) b.cmd[st] = command(j);
               mbar_expect_tx(b.kv_full + st, C::kTileBytes);
               for (int x = 0; x < C::kBoxes; ++x)
                 tma_load_3d(smem + C::kRing + st * C::kTileBytes + x * kBox, kv ? &vmap : &kmap, 64 * x, it.head,
@@ -547,8 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!alive)  // nothing may still be on its way when the CTA leaves
             for (uint32_t r = ring > C::kStages ? ring - C::kStages : 0; r < ring; ++r)
-              mbar_wait_landed(b.kv_full + r % C::kStages, r / C::kStages & 1, status);
+              wait(b.kv_full + r % C::kStages, r / C::kStages & 1, status);
         }
+        if (end) break;
         ring = __shfl_sync(0xffffffffu, __reduce_max_sync(0xffffffffu, ring), 0);
         alive = __all_sync(0xffffffffu, alive);
         next = (int)gridDim.x + __shfl_sync(0xffffffffu, ahead, 0);
@@ -558,47 +649,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ================================================================ queries; values that not every row sees
       const int t = warp - kHelp;
+      asm volatile("fence.proxy.async.global;" ::: "memory");
       constexpr int kChunks = D / 8;  // 16-byte pieces of a row
       uint32_t ring = 0, fills = 0, edges = 0;
       bool alive = true;
       Item it;
       for (int k = 0; alive && item(k, &it); ++k) {
         if (it.t[t].lo <= it.t[t].hi) {
-          if (!mbar_wait_landed(b.q_empty + t, (fills & 1) ^ 1, status)) break;
+          if (!wait(b.q_empty + t, (fills & 1) ^ 1, status)) break;
           ++fills;
-          // a pass of the warp is kStep rows; a row's step to the next pass is some tokens and heads
-          constexpr int kStep = 32 / kChunks;
-          const int ch = lane % kChunks, r0 = lane / kChunks, row = it.row0 + t * kRows + r0;
-          const int left = it.n * G - it.row0 - t * kRows;  // rows of the tile (it may be over)
-          const int tok = row / G, toks = kStep / G, more = kStep - toks * G;
-          int g = row - tok * G;
-          const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (long long)(it.start + tok) * p.q_stride +
-                                (size_t)(it.head * G + g) * D + ch * 8;
-          const long long step = toks * p.q_stride + more * D, wrap = p.q_stride - G * D;
-          const uint32_t to = su32(smem) + t * C::kTileBytes + ch / 8 * kBox + r0 * 128;
-#pragma unroll 8
-          for (int i = 0; i < kRows; i += kStep) {
-            const bool in = r0 + i < left;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 128 + ((ch % 8 ^ ((r0 + i) & 7)) << 4)),
-                         "l"(in ? src : reinterpret_cast<const uint16_t*>(p.q)), "r"(in ? 16 : 0)
-                         : "memory");
-            src += step;
-            g += more;
-            if (g >= G) {
-              g -= G;
-              src += wrap;
+          if (p.rows % G == 0) {
+            // whole tokens: one copy for 64 columns
+            if (elect_one()) {
+              mbar_expect_tx(b.q_full + t, p.rows * D * 2);
+              for (int x = 0; x < C::kBoxes; ++x)
+                tma_load_4d(smem + t * C::kTileBytes + x * kBox, &qmap, 64 * x, 0, it.head, it.start + it.t[t].tok_lo, b.q_full + t);
             }
+            __syncwarp();
+          } else {
+            // a pass of the warp is kStep rows; a row's step to the next pass is some tokens and heads
+            constexpr int kStep = 32 / kChunks;
+            const int ch = lane % kChunks, r0 = lane / kChunks, row = it.row0 + t * p.rows + r0;
+            const int left = it.n * G - it.row0 - t * p.rows;  // rows of the tile (it may be over)
+            const int tok = row / G, toks = kStep / G, more = kStep - toks * G;
+            int g = row - tok * G;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (long long)(it.start + tok) * p.q_stride +
+                                  (size_t)(it.head * G + g) * D + ch * 8;
+            const long long step = toks * p.q_stride + more * D, wrap = p.q_stride - G * D;
+            const uint32_t to = su32(smem) + t * C::kTileBytes + ch / 8 * kBox + r0 * 128;
+#pragma unroll 8
+            for (int i = 0; i < kRows; i += kStep) {
+              const bool in = r0 + i < left;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 128 + ((ch % 8 ^ ((r0 + i) & 7)) << 4)),
+                           "l"(in ? src : reinterpret_cast<const uint16_t*>(p.q)), "r"(in ? 16 : 0)
+                           : "memory");
+              src += step;
+              g += more;
+              if (g >= G) {
+                g -= G;
+                src += wrap;
+              }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b.q_full + t);
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b.q_full + t);
         }
         // every tile of the ring is waited for and given back in turn: a wait that skips one
         // could not tell its phase from the last but one
         for (int i = 0; alive && i < 2 * (it.hi() - it.lo() + 1); ++i, ++ring) {
           const uint32_t st = ring % C::kStages;
-          if (!mbar_wait_landed(b.kv_full + st, ring / C::kStages & 1, status)) { alive = false; break; }
+          if (!wait(b.kv_full + st, ring / C::kStages & 1, status)) { alive = false; break; }
           if (!(i & 1) || !it.edge(it.lo() + i / 2, window)) {
             __syncwarp();
             if (lane == 0) mbar_arrive(b.kv_empty + st);
@@ -632,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (alive) item_done(k);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (fills > 0) wait(b.q_full + t, (fills - 1) & 1, status);  // (nothing on its way when the CTA leaves)
     }
   }
   __syncwarp();
@@ -655,23 +758,38 @@ bool map_rows(CUtensorMap* m, const void* base, int D, int heads, int total, lon
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as [total][kv_heads][G][D], in boxes of 64 columns, the G heads of a kv head
+// and a tile's tokens.
+bool map_queries(CUtensorMap* m, const PromptArgs& a, int D) {
+  const cuuint64_t dim[4] = {(cuuint64_t)D, (cuuint64_t)a.G, (cuuint64_t)a.kv_heads, (cuuint64_t)a.total};
+  const cuuint64_t step[3] = {(cuuint64_t)D * 2, (cuuint64_t)a.G * D * 2, (cuuint64_t)a.q_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)a.G, 1, (cuuint32_t)(a.rows / a.G)}, es[4] = {1, 1, 1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), dim, step, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool kMods>
 cudaError_t launch_as(const PromptArgs& a, int sms, cudaStream_t s) {
   static OncePerDevice once;
   if (const cudaError_t rc = allow_smem(once, prompt_attention_kernel<D, kMods>, Cfg<D>::kSmem); rc != cudaSuccess) return rc;
-  CUtensorMap kmap, vmap;
+  CUtensorMap qmap{}, kmap, vmap;
   if (!map_rows(&kmap, a.k, D, a.kv_heads, a.total, a.k_stride) || !map_rows(&vmap, a.v, D, a.kv_heads, a.total, a.v_stride))
     return cudaErrorUnknown;
+  if (a.rows % a.G == 0 && !map_queries(&qmap, a, D)) return cudaErrorUnknown;
   // items at most: a started one for each prompt and head beside the full ones
-  const long long items = ((long long)a.total * a.G / (2 * kRows) + std::min(a.B, a.total)) * a.kv_heads;
+  const long long items = ((long long)a.total * a.G / (2 * a.rows) + std::min(a.B, a.total)) * a.kv_heads;
   PdlLaunch L(dim3((unsigned)std::min<long long>(items, sms)), dim3(kThreads), Cfg<D>::kSmem, s);
-  return cudaLaunchKernelEx(&L.cfg, prompt_attention_kernel<D, kMods>, a, kmap, vmap);
+  return cudaLaunchKernelEx(&L.cfg, prompt_attention_kernel<D, kMods>, a, qmap, kmap, vmap);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attention(const PromptArgs& args, int sms, cudaStream_t s) {
   PromptArgs a = args;
+  // A tile's rows: whole tokens, which one copy brings, where that fills it to 7 / 8; else 128.
+  const int whole = kRows / a.G * a.G;
+  a.rows = 8 * whole >= 7 * kRows ? whole : kRows;
   // (a cap's inverse, and the cap times log2 e, stay finite; no score comes near either end)
   if (a.softcap > 0.f) a.softcap = std::min(std::max(a.softcap, 0x1p-100f), 0x1p100f);
   const float c = a.sm_scale * kLog2e;
