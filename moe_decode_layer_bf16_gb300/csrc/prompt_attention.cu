@@ -12,7 +12,7 @@
 // range of key tiles (128 keys).  Packing wastes nothing whatever the group is and keeps
 // the masked part of a tile small: 128 rows are 128 / G tokens.
 //
-// One CTA an SM takes items from a counter, a prompt's last (longest) ones first.  Twelve
+// One CTA an SM takes items from a counter, the longest first (of 32 prompts at a time).  Twelve
 // warps: two softmax warpgroups, a tile each; one warp issues the MMAs, one copies keys
 // and values (TMA, a ring of tiles) and hands out the items, two load the queries and
 // look through the values of tiles that not every row sees.  For each key tile
@@ -55,6 +55,7 @@ MOE_DEV bool wait(uint64_t* bar, uint32_t parity, int* status) {
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
         : "=r"(ok) : "r"(su32(bar)), "r"(parity), "r"(1000000u) : "memory");
     if (ok) return true;
+    if (*(volatile int*)status == MOE_ERR_DEVICE_TIMEOUT) return false;
   } while (globaltimer_ns() - t0 < kWaitNs);
   atomicExch(status, MOE_ERR_DEVICE_TIMEOUT);
   return false;
@@ -65,8 +66,8 @@ constexpr int kRows = 128;    // packed rows of a tile
 constexpr int kBox = 128 * kKeys;  // bytes of 64 columns of 128 rows
 constexpr int kSlots = 4;     // items handed out ahead
 constexpr int kLooks = 4;     // tiles of values in the ring at most
-constexpr int kThreads = 384;
-constexpr int kMma = 8, kCopy = 9, kHelp = 10;  // warps (the softmax's are the first eight)
+constexpr int kThreads = 640;
+constexpr int kMma = 16, kCopy = 17, kHelp = 18;  // warps (the softmax's are the first eight)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that is let pass
 
@@ -74,10 +75,11 @@ template <int D>
 struct Cfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBoxes * kBox;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kRing = 2 * kTileBytes;  // behind the two query tiles
   static constexpr int kBars = kRing + kStages * kTileBytes;
-  static constexpr int kSmem = kBars + 1024 + 768;  // (aligned by hand)
+  static constexpr int kPairs = kBars + 768;        // a value of each softmax thread
+  static constexpr int kSmem = kPairs + 2048;
 };
 static_assert(Cfg<128>::kStages <= 2 * kLooks && Cfg<64>::kStages <= 2 * kLooks, "barriers of values looked through");
 static_assert(Cfg<128>::kSmem <= 232448 && Cfg<64>::kSmem <= 232448, "shared memory of a CTA");
@@ -177,6 +179,11 @@ MOE_DEV float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+MOE_DEV float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
 // (x, y) = (x, y) * c + d, two at a time
 MOE_DEV void fma2(float& x, float& y, float c, float d) {
   asm("{\n .reg .b64 a, b, e;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n mov.b64 e, {%3, %3};\n"
@@ -273,17 +280,18 @@ MOE_DEV uint32_t finite_or_zero(uint32_t w) {
   return w & ~((b >> 15) * 0xffffu);
 }
 
-// A row that sees one of the prompt's infinities or NaN that were replaced gets them back.
+// A row that sees one of the prompt's infinities or NaN that were replaced gets them back:
+// in its half of the columns, from c0.
 template <int D>
-__device__ __noinline__ void put_back(const PromptArgs& p, const Item& it, int t, int tok, __nv_bfloat16* out) {
+__device__ __noinline__ void put_back(const PromptArgs& p, const Item& it, int t, int tok, int c0, __nv_bfloat16* out) {
   const Range& r = it.t[t];
   for (int j = r.lo; j <= r.hi; ++j) {
     if (!it.edge(j, p.window)) continue;
     const int k0 = max(kKeys * j, p.window > 0 ? tok - p.window + 1 : 0), k1 = min(kKeys * j + kKeys - 1, tok);
     for (int k = k0; k <= k1; ++k) {
       const uint32_t* v = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(p.v) +
-                                                            (long long)(it.start + k) * p.v_stride + (size_t)it.head * D);
-      for (int c = 0; c < D / 2; ++c) {
+                                                            (long long)(it.start + k) * p.v_stride + (size_t)it.head * D + c0);
+      for (int c = 0; c < D / 4; ++c) {
         const uint32_t w = __ldcg(v + c), b = not_finite(w);
         if (b & 0x8000u) out[2 * c] = __float2bfloat16(__bfloat162float(out[2 * c]) + bf16_lo(w));
         if (b >> 31) out[2 * c + 1] = __float2bfloat16(__bfloat162float(out[2 * c + 1]) + bf16_hi(w));
@@ -298,11 +306,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     prompt_attention_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (su32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) uint8_t smem[];
   Bars& b = *reinterpret_cast<Bars*>(smem + C::kBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* status = p.status;
+  if (su32(smem) & 1023u) {  // (the tiles' swizzle wants it; no other memory of the CTA lies before)
+    if (tid == 0) atomicExch(status, MOE_ERR_CUDA);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(b.kv_full + i, 1);
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(b.item_full + i, 1);
-      mbar_init(b.item_empty + i, 10);  // eight softmax warps, two helpers
+      mbar_init(b.item_empty + i, 18);  // sixteen softmax warps, two helpers
       mbar_init(b.v_done + i, 2);
     }
     for (int i = 0; i < kLooks; ++i) mbar_init(b.v_ok + i, 2);
@@ -350,122 +361,136 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kMma) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    const int t = warp >> 2;
-    const uint32_t quad = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + quad + 128 * t, to = tmem + quad + 256 + 128 * t;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // Tile t's warp for rows 32 q .. 32 q + 31 and half h of the columns.  The two warps of
+    // the same rows agree on what is theirs together: at a barrier of their own.
+    const int q = warp & 3, t = warp >> 2 & 1, h = warp >> 3, pair = 1 + 4 * t + q;
+    const uint32_t quad = (uint32_t)(32 * q) << 16;
+    const uint32_t ts = tmem + quad + 128 * t, to = tmem + quad + 256 + 128 * t + D / 2 * h;
+    float* mine = reinterpret_cast<float*>(smem + C::kPairs) + 256 * t + 128 * h + 32 * q + lane;
+    const float* theirs = mine + (h ? -128 : 128);
+    auto either = [&](bool x) {  // of the rows' two warps
+      int y;
+      asm volatile(
+          "{\n .reg .pred p, r;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred r, %2, 64, p;\n selp.s32 %0, 1, 0, r;\n}"
+          : "=r"(y) : "r"((int)x), "r"(pair) : "memory");
+      return y != 0;
+    };
     const float c = kMods ? 1.f : p.sm_scale * kLog2e;
     const int heads = G * p.kv_heads;
     uint32_t steps = 0, items = 0;
     Item it;
-    for (int k = 0; item(k, &it); ++k) {
+    // (A wait that fails leaves the status set, and every later wait gives up at once: a pair's
+    // warps go through the same barriers to the item's end either way.)
+    for (int k = 0;; ++k) {
+      const bool more = item(k, &it);
+      if (either(!more)) break;
       const Range rg = it.t[t];
       if (rg.lo > rg.hi) {
         item_done(k);
         continue;
       }
-      const int r = 32 * (warp & 3) + lane, row = it.row0 + t * p.rows + r;
+      const int r = 32 * q + lane, row = it.row0 + t * p.rows + r;
       const bool live = r < p.rows && row < it.n * G;
       const int tok = min(row / G, it.n - 1), head = it.head * G + (live ? row - row / G * G : 0);
       const float slope = kMods && p.slopes ? p.slopes[head] * kLog2e : 0.f;
-      float m = -INFINITY, mc = 0.f, l0 = 0.f, l1 = 0.f;  // maximum in use, times c; two halves of the sum
-      bool alive = true;
-      // a tile's maximum is mt: the maximum in use follows where some row's grows by much
-      auto grow = [&](float mt, bool some) {
-        if (!__any_sync(0xffffffffu, (mt - m) * c > kGrow)) return;
-        const float mn = fmaxf(m, mt), mcn = mn == -INFINITY ? 0.f : mn * c;
-        const float f = m == -INFINITY ? 0.f : ex2(mc - mcn);
-        l0 *= f;
-        l1 *= f;
-        if (some) {  // (this tile's products so far were complete before S was)
-#pragma unroll
-          for (int i = 0; i < D; i += 16) {
-            float o[16];
-            tc_ld16(to + i, o);
-            tc_wait_ld();
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-            tc_st16(to + i, w);
-          }
-        }
-        m = mn;
-        mc = mcn;
-      };
-      // 32 scores' weights to tensor memory
-      auto weights = [&](const float* s, uint32_t at) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float x = s[e], y = s[e + 1];
-          fma2(x, y, c, -mc);
-          x = ex2(x);
-          y = ex2(y);
-          add2(l0, l1, x, y);
-          w[e / 2] = pack_bf16(x, y);
-        }
-        tc_st16(at, w);
-      };
+      float m = -INFINITY, mc = 0.f, l0 = 0.f, l1 = 0.f;  // maximum in use, times c; two parts of the half's sum
       for (int j = rg.lo; j <= rg.hi; ++j, ++steps) {
-        if (!wait(b.s_full + t, steps & 1, status)) { alive = false; break; }
+        wait(b.s_full + t, steps & 1, status);
         tc_fence_after();
-        float s[kKeys];
-#pragma unroll
-        for (int i = 0; i < kKeys; i += 32) tc_ld32(ts + i, s + i);
+        float s[kKeys / 2];
+        tc_ld32(ts + 64 * h, s);
+        tc_ld32(ts + 64 * h + 32, s + 32);
         tc_wait_ld();
-        if constexpr (kMods) modified<kKeys>(p, s, slope, (float)(kKeys * j - tok));
+        if constexpr (kMods) modified<kKeys / 2>(p, s, slope, (float)(kKeys * j + 64 * h - tok));
         if (rg.edge(j, window)) {
-          const int last = tok - kKeys * j;
+          const int last = tok - kKeys * j - 64 * h, first = window > 0 ? last - window + 1 : -kKeys;
+          // bits of the columns that the row sees
+          const uint64_t upto = last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1;
+          const uint64_t seen = first <= 0 ? upto : first > 63 ? 0ull : upto & (~0ull << first);
+          const uint32_t w0 = (uint32_t)seen, w1 = (uint32_t)(seen >> 32);
 #pragma unroll
-          for (int i = 0; i < kKeys; ++i) s[i] = i <= last ? s[i] : -INFINITY;
-          if (window > 0 && last >= window) {
-            const int first = last - window + 1;
-#pragma unroll
-            for (int i = 0; i < kKeys; ++i) s[i] = i >= first ? s[i] : -INFINITY;
+          for (int i = 0; i < 32; ++i) {
+            s[i] = w0 & (1u << i) ? s[i] : -INFINITY;
+            s[i + 32] = w1 & (1u << i) ? s[i + 32] : -INFINITY;
           }
         }
-        float top[4] = {s[0], s[1], s[2], s[3]};
+        float top[4];
 #pragma unroll
-        for (int i = 4; i < kKeys; ++i) top[i & 3] = fmaxf(top[i & 3], s[i]);
-        grow(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), j > rg.lo);
-        // the weights, in two halves: the products of the first run while the second is made
+        for (int i = 0; i < 4; ++i) top[i] = max3(s[3 * i], s[3 * i + 1], s[3 * i + 2]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          weights(s + 64 * h, ts + 32 * h);
-          weights(s + 64 * h + 32, ts + 32 * h + 16);
-          tc_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b.p_full[t] + h);
+        for (int i = 12; i + 1 < kKeys / 2; i += 2) top[i / 2 & 3] = max3(top[i / 2 & 3], s[i], s[i + 1]);
+        const float mt = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        // Where a row's maximum grows by much, the maximum in use follows.  (Past this barrier
+        // both warps have read their scores, and weights may take the scores' place.)
+        if (either((mt - m) * c > kGrow)) {
+          *mine = mt;
+          either(false);
+          const float mn = max3(m, mt, *theirs), mcn = mn == -INFINITY ? 0.f : mn * c;
+          const float f = m == -INFINITY ? 0.f : ex2(mc - mcn);
+          l0 *= f;
+          l1 *= f;
+          if (j > rg.lo) {  // (this tile's products so far were complete before S was)
+#pragma unroll 1
+            for (int i = 0; i < D / 2; i += 16) {  // (rare: unrolled, its registers would be missed elsewhere)
+              float o[16];
+              tc_ld16(to + i, o);
+              tc_wait_ld();
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+              tc_st16(to + i, w);
+            }
+          }
+          m = mn;
+          mc = mcn;
         }
-      }
-      if (!alive) break;
-      // ---------------------------------------------------------------- the rows' results
-      if (!wait(b.o_full + t, items++ & 1, status)) break;
-      tc_fence_after();
-      const float l = l0 + l1, inv = 1.f / l;
-      const size_t at = (size_t)(it.start + tok) * heads + head;
-      uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at * D;
 #pragma unroll
-      for (int i = 0; i < D; i += 32) {
-        float o[32];
-        tc_ld32(to + i, o);
+        for (int i = 0; i < kKeys / 2; i += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x = s[i + e], y = s[i + e + 1];
+            fma2(x, y, c, -mc);
+            x = ex2(x);
+            y = ex2(y);
+            add2(l0, l1, x, y);
+            w[e / 2] = pack_bf16(x, y);
+          }
+          tc_st16(ts + 32 * h + i / 2, w);
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.p_full[t] + h);
+      }
+      // ---------------------------------------------------------------- the rows' results
+      either(false);
+      *mine = l0 + l1;
+      either(false);
+      const float l = h ? *theirs + *mine : *mine + *theirs, inv = 1.f / l;
+      wait(b.o_full + t, items++ & 1, status);
+      tc_fence_after();
+      const size_t at = (size_t)(it.start + tok) * heads + head;
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + at * D + D / 2 * h;
+#pragma unroll
+      for (int i = 0; i < D / 2; i += 16) {
+        float o[16];
+        tc_ld16(to + i, o);
         tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= inv;
-        if (live) {
-          store16(out + i, o);
-          store16(out + i + 16, o + 16);
-        }
+        for (int e = 0; e < 16; ++e) o[e] *= inv;
+        if (live) store16(out + i, o);
       }
       tc_fence_before();
-      if (p.lse && live) p.lse[at] = (mc + log2f(l)) * kLn2;
-      if (!wait(b.v_done + k % kSlots, (k / kSlots) & 1, status)) break;
-      if (b.bad[k % kSlots] && live) put_back<D>(p, b.item[k % kSlots], t, tok, reinterpret_cast<__nv_bfloat16*>(out));
+      if (p.lse && live && h == 0) p.lse[at] = (mc + log2f(l)) * kLn2;
+      wait(b.v_done + k % kSlots, (k / kSlots) & 1, status);
+      if (b.bad[k % kSlots] && live)
+        put_back<D>(p, b.item[k % kSlots], t, tok, D / 2 * h, reinterpret_cast<__nv_bfloat16*>(out));
       item_done(k);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kMma) {
       // ================================================================ MMA
       if (elect_one()) {
@@ -563,14 +588,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("fence.proxy.async.global;" ::: "memory");
       uint32_t ring = 0;
       bool alive = true;
-      // a window of 32 prompts, a lane each: items before it, and in it up to and with each lane
-      int b0 = -32, before = 0, upto = 0, start = 0, n = 0;
+      // A run of 32 prompts at a time, a lane each.  Their items come by level, the longest first:
+      // at level L the L-th block of rows of each prompt that has one.
+      int b0 = -32, before = 0, level = 0, start = 0, n = 0, blocks = 0;  // before: items before this level
       int next = blockIdx.x;
       for (int k = 0; alive; ++k) {
         int ahead = 0;
         if (lane == 0) ahead = atomicAdd(p.tickets, 1);
-        while (b0 < p.B && next >= before + __shfl_sync(0xffffffffu, upto, 31)) {
-          before += __shfl_sync(0xffffffffu, upto, 31);
+        uint32_t who = 0;  // the prompts that have a block at this level
+        while (b0 < p.B) {
+          who = __ballot_sync(0xffffffffu, level > 0 && blocks >= level);
+          const int each = __popc(who) * p.kv_heads;
+          if (each > 0) {
+            // the levels down to the next shorter prompt's have as many items each
+            const int below = __reduce_max_sync(0xffffffffu, blocks < level ? blocks : 0);
+            const int down = min((next - before) / each, level - below);
+            before += down * each;
+            level -= down;
+            if (level > below) break;
+            continue;
+          }
           b0 += 32;
           start = n = 0;
           if (b0 + lane < p.B) {
@@ -579,25 +616,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (step_rows_ok(start, stop, p.total)) n = stop - start;
             else if (blockIdx.x == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
           }
-          upto = (n * G + 2 * p.rows - 1) / (2 * p.rows) * p.kv_heads;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-          }
+          blocks = (n * G + 2 * p.rows - 1) / (2 * p.rows);
+          level = __reduce_max_sync(0xffffffffu, blocks);
         }
         const bool end = b0 >= p.B;
         Item it{};
         if (!end) {
-          const int at = next - before;
-          const int who = __popc(__ballot_sync(0xffffffffu, upto <= at));
-          it.start = __shfl_sync(0xffffffffu, start, who);
-          it.n = __shfl_sync(0xffffffffu, n, who);
-          const int prior = __shfl_sync(0xffffffffu, upto, who > 0 ? who - 1 : 0);
-          const int idx = at - (who > 0 ? prior : 0);
-          const int blocks = (it.n * G + 2 * p.rows - 1) / (2 * p.rows);
-          it.row0 = (blocks - 1 - idx / p.kv_heads) * 2 * p.rows;
-          it.head = idx % p.kv_heads;
+          const int idx = (next - before) / p.kv_heads;
+          const uint32_t mine = __ballot_sync(0xffffffffu, (who >> lane & 1) && __popc(who & ((1u << lane) - 1)) == idx);
+          const int from = __ffs(mine) - 1;
+          it.start = __shfl_sync(0xffffffffu, start, from);
+          it.n = __shfl_sync(0xffffffffu, n, from);
+          it.row0 = (level - 1) * 2 * p.rows;
+          it.head = (next - before) % p.kv_heads;
           it.t[0] = range_of(it.n, it.row0, p.rows, G, window);
           it.t[1] = range_of(it.n, it.row0 + p.rows, p.rows, G, window);
         }
@@ -637,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!alive)  // nothing may still be on its way when the CTA leaves
             for (uint32_t r = ring > C::kStages ? ring - C::kStages : 0; r < ring; ++r)
-              wait(b.kv_full + r % C::kStages, r / C::kStages & 1, status);
+              mbar_wait_landed(b.kv_full + r % C::kStages, r / C::kStages & 1, status);
         }
         if (end) break;
         ring = __shfl_sync(0xffffffffu, __reduce_max_sync(0xffffffffu, ring), 0);
@@ -734,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (alive) item_done(k);
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (fills > 0) wait(b.q_full + t, (fills - 1) & 1, status);  // (nothing on its way when the CTA leaves)
+      if (fills > 0) mbar_wait_landed(b.q_full + t, (fills - 1) & 1, status);  // (nothing on its way when the CTA leaves)
     }
   }
   __syncwarp();
