@@ -80,7 +80,7 @@ int kv_pages_extend(int32_t* page_table, int width, const int32_t* lens, const i
   a.page_table = page_table; a.lens = lens; a.fresh = new_tokens; a.free_pages = const_cast<int32_t*>(free_pages);
   a.free_state = free_state; a.q_start = q_start; a.lens_out = lens_out; a.free_out = free_out; a.positions = positions;
   a.slots = slots; a.width = width; a.shift = shift_of(page_size); a.num_pages = num_pages; a.capacity = capacity; a.B = B;
-  a.rows = rows; a.status = Ws(ws).status;
+  a.rows = rows; a.status = Ws(ws).status; a.ticket = Ws(ws).tickets;
   return launch_kv_pages_extend(a, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -95,6 +95,7 @@ int kv_pages_release(const int32_t* page_table, int width, const int32_t* lens, 
   a.page_table = const_cast<int32_t*>(page_table); a.lens = lens; a.done = done; a.free_pages = free_pages;
   a.free_state = free_state; a.lens_out = lens_out; a.free_out = free_out; a.width = width; a.shift = shift_of(page_size);
   a.num_pages = num_pages; a.capacity = capacity; a.B = B; a.status = Ws(ws).status;
+  a.ticket = Ws(ws).tickets;
   return launch_kv_pages_release(a, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

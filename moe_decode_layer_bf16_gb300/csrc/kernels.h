@@ -319,6 +319,7 @@ struct PagesArgs {
   int64_t* slots;            // extend: [rows]
   int width, shift, num_pages, capacity, B, rows;  // shift: log2 of the page's tokens
   int* status;
+  int* ticket;  // zero between calls
 };
 cudaError_t launch_kv_pages_extend(const PagesArgs& a, cudaStream_t s);
 cudaError_t launch_kv_pages_release(const PagesArgs& a, cudaStream_t s);

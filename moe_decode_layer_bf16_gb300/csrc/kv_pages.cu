@@ -7,24 +7,22 @@
 // holds, no later sequence that needs pages fits either, so nothing has to be decided
 // in turn.  Running sums of the rows that are given make q_start.
 //
-// One cluster of CTAs, each with a run of the sequences; they exchange their sums through
-// shared memory.  Rows and pages of a run are then written by one thread each, which
-// finds its sequence among the run's running sums by bisection: coalesced, and even
-// whatever the lengths are.  Bound by latency: a launch and three dependent reads.
-#include <cooperative_groups.h>
+// Every CTA forms the running sums for itself (a thread each for up to 1024 sequences at a
+// time) and writes its share of the rows and pages, a thread each, which finds its sequence
+// among the sums by bisection: coalesced, and even whatever the lengths are.  What a step
+// in place overwrites (lengths, the stack's count) is written by the last CTA to have read
+// it.  Bound by latency: a launch and three dependent reads.
+#include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "../../include/moe_decode.h"
 
-namespace cg = cooperative_groups;
-
 namespace moe {
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxThreads = 1024;
 
 struct Sums {
   long long pages, rows;
@@ -32,44 +30,29 @@ struct Sums {
 
 MOE_DEV Sums operator+(const Sums& a, const Sums& b) { return {a.pages + b.pages, a.rows + b.rows}; }
 
-// The sum over the threads before this one; *all gets the sum over the CTA.
-MOE_DEV Sums scan_before(Sums v, Sums* s_warp, Sums* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sums up = v;
+MOE_DEV Sums scan_warp(Sums v) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Sums w{__shfl_up_sync(0xffffffffu, up.pages, o), __shfl_up_sync(0xffffffffu, up.rows, o)};
-    if (lane >= o) up = up + w;
+    const Sums w{__shfl_up_sync(0xffffffffu, v.pages, o), __shfl_up_sync(0xffffffffu, v.rows, o)};
+    if (lane >= o) v = v + w;
   }
+  return v;
+}
+
+// The sum over the threads before this one; *all gets the sum over the CTA.
+MOE_DEV Sums scan_before(Sums v, Sums* s_warp, Sums* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  Sums up = scan_warp(v);
   __syncthreads();  // (s_warp may still be read)
   if (lane == 31) s_warp[warp] = up;
   __syncthreads();
-  Sums w = s_warp[lane];
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Sums x{__shfl_up_sync(0xffffffffu, w.pages, o), __shfl_up_sync(0xffffffffu, w.rows, o)};
-    if (lane >= o) w = w + x;
-  }
+  const Sums w = scan_warp(lane < warps ? s_warp[lane] : Sums{0, 0});
   *all = {__shfl_sync(0xffffffffu, w.pages, 31), __shfl_sync(0xffffffffu, w.rows, 31)};
-  const Sums before{__shfl_sync(0xffffffffu, w.pages, warp > 0 ? warp - 1 : 0),
-                    __shfl_sync(0xffffffffu, w.rows, warp > 0 ? warp - 1 : 0)};
+  const int from = warp > 0 ? warp - 1 : 0;
+  const Sums before{__shfl_sync(0xffffffffu, w.pages, from), __shfl_sync(0xffffffffu, w.rows, from)};
   up = {up.pages - v.pages, up.rows - v.rows};
   return warp > 0 ? up + before : up;
-}
-
-// The sums of the CTAs before this one, and of all.
-MOE_DEV Sums cluster_before(cg::cluster_group& cluster, Sums mine, Sums* s_part, Sums* all) {
-  if (threadIdx.x == 0) *s_part = mine;
-  cluster.sync();
-  Sums before{0, 0}, total{0, 0};
-  const int rank = (int)cluster.block_rank(), n = (int)cluster.num_blocks();
-  for (int r = 0; r < n; ++r) {
-    const Sums v = *cluster.map_shared_rank(s_part, r);
-    if (r < rank) before = before + v;
-    total = total + v;
-  }
-  *all = total;
-  return before;
 }
 
 // The last of the n entries of `first` (ascending, first[0] <= i) that is at most i.
@@ -82,108 +65,87 @@ MOE_DEV int find(const int* first, int n, int i) {
   return lo;
 }
 
+// Whether this CTA is the last of the grid to come here.
+MOE_DEV bool last_to_come(int* ticket) {
+  __shared__ bool s_last;
+  if (gridDim.x == 1) {
+    __syncthreads();
+    return true;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s_last = atom_add_acq_rel(ticket, 1) == (int)gridDim.x - 1;
+    if (s_last) *ticket = 0;  // ready for the next call
+  }
+  __syncthreads();
+  return s_last;
+}
+
 // A sequence's tokens held and asked for, pages held and needed.
 struct Need {
   int len, fresh, held, pages;
 };
-MOE_DEV Need need_of(const PagesArgs& a, int b, bool* bad) {
-  Need n{a.lens[b], a.fresh[b], 0, 0};
-  const long long cap = (long long)a.width << a.shift;
-  if (n.len < 0 || n.fresh < 0 || (long long)n.len + n.fresh > cap) {
-    *bad = true;
-    n.fresh = 0;
-    return n;
-  }
-  const int up = (1 << a.shift) - 1;
-  n.held = (n.len + up) >> a.shift;
-  n.pages = ((n.len + n.fresh + up) >> a.shift) - n.held;
-  return n;
-}
 
-__global__ void __launch_bounds__(kThreads) extend_kernel(PagesArgs a) {
-  __shared__ Sums s_warp[kThreads / 32], s_part[2];
-  __shared__ int s_row[kThreads], s_page[kThreads];      // the run's rows and pages before each sequence, from its own first
-  __shared__ int s_len[kThreads], s_old[kThreads], s_held[kThreads];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+__global__ void __launch_bounds__(kMaxThreads) extend_kernel(PagesArgs a) {
+  __shared__ Sums s_warp[kMaxThreads / 32];
+  __shared__ int s_row[kMaxThreads], s_page[kMaxThreads];  // rows and pages before each sequence, from the first one's
+  __shared__ int s_len[kMaxThreads], s_old[kMaxThreads], s_held[kMaxThreads];
+  const int tid = threadIdx.x, threads = blockDim.x, page_tokens = 1 << a.shift;
   grid_dep_launch();
   grid_dep_wait();
-  const int run = (a.B + ranks - 1) / ranks;
-  const int b0 = min(rank * run, a.B), b1 = min(b0 + run, a.B);
   bool bad = false;
   const int stack = a.free_state[0];
   const int count = stack < 0 || stack > a.capacity ? 0 : stack;
   if (count != stack) bad = true;
-  if (tid < kThreads / 32) s_warp[tid] = {0, 0};
-  // what the run's sequences ask for
-  Sums mine{0, 0}, all, part;
-  for (int c = b0; c < b1; c += kThreads) {
-    const int b = c + tid;
-    Sums v{0, 0};
-    if (b < b1) {
-      const Need n = need_of(a, b, &bad);
-      v = {n.pages, n.fresh};
+  // the sequences from b0 on, a thread each: what this thread's asks for and gets
+  Sums asked{0, 0}, got{0, 0};  // before these sequences
+  auto sequences = [&](int b0, Sums* at, Sums* part) {
+    Need n{0, 0, 0, 0};
+    if (b0 + tid < a.B) {
+      n.len = a.lens[b0 + tid];
+      n.fresh = a.fresh[b0 + tid];
+      if (n.len < 0 || n.fresh < 0 || (long long)n.len + n.fresh > (long long)a.width << a.shift) {
+        bad = true;
+        n.fresh = 0;
+      } else {
+        n.held = (n.len + page_tokens - 1) >> a.shift;
+        n.pages = ((n.len + n.fresh + page_tokens - 1) >> a.shift) - n.held;
+      }
     }
-    scan_before(v, s_warp, &part);
-    mine = mine + part;
-  }
-  const Sums asked0 = cluster_before(cluster, mine, &s_part[0], &all);
-  const long long asked_pages = all.pages;
-  // what they get
-  auto given = [&](int c, const Sums& asked, Need* n, Sums* before) {
-    const int b = c + tid;
-    *n = Need{0, 0, 0, 0};
-    if (b < b1) *n = need_of(a, b, &bad);
-    Sums sum;
-    *before = asked + scan_before({n->pages, n->fresh}, s_warp, &sum);
-    const bool room = n->fresh == 0 || before->rows + n->fresh <= a.rows;
+    *at = scan_before({n.pages, n.fresh}, s_warp, part);
+    const bool room = n.fresh == 0 || asked.rows + at->rows + n.fresh <= a.rows;
+    const bool fits = n.pages == 0 || asked.pages + at->pages + n.pages <= count;
     if (!room) bad = true;
-    if (!room || (n->pages > 0 && before->pages + n->pages > count)) n->fresh = n->pages = 0;
-    return sum;
+    asked = asked + *part;
+    if (__syncthreads_or(!room || !fits)) {  // not all of them are served
+      if (!room || !fits) n.fresh = n.pages = 0;
+      *at = scan_before({n.pages, n.fresh}, s_warp, part);
+    }
+    return n;
   };
-  mine = {0, 0};
-  Sums asked = asked0;
-  for (int c = b0; c < b1; c += kThreads) {
-    Need n;
-    Sums before;
-    const Sums sum = given(c, asked, &n, &before);
-    scan_before({n.pages, n.fresh}, s_warp, &part);
-    asked = asked + sum;
-    mine = mine + part;
-  }
-  Sums got = cluster_before(cluster, mine, &s_part[1], &all);
-  if (rank == 0 && tid == 0) {
-    a.free_out[0] = stack - (int)all.pages;
-    a.free_out[1] = (int)min(asked_pages - all.pages, (long long)INT32_MAX);
-    a.q_start[a.B] = (int)all.rows;
-  }
-  asked = asked0;
-  for (int c = b0; c < b1; c += kThreads) {
-    const int m = min(kThreads, b1 - c), b = c + tid;
-    Need n;
-    Sums before;
-    const Sums sum = given(c, asked, &n, &before);
-    asked = asked + sum;
-    const Sums at = scan_before({n.pages, n.fresh}, s_warp, &part);
-    if (b < b1) {
-      a.q_start[b] = (int)(got.rows + at.rows);
-      a.lens_out[b] = n.len + n.fresh;
+  Need n;
+  Sums at, part;
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
+    const int m = min(threads, a.B - b0);
+    n = sequences(b0, &at, &part);
+    if (tid < m) {
       s_row[tid] = (int)at.rows;
       s_page[tid] = (int)at.pages;
       s_len[tid] = n.len;
       s_held[tid] = n.held;
       // the page that is filled further
-      s_old[tid] = n.fresh > 0 && (n.len & ((1 << a.shift) - 1)) ? a.page_table[(size_t)b * a.width + (n.len >> a.shift)] : -1;
+      s_old[tid] = n.fresh > 0 && (n.len & (page_tokens - 1)) ? a.page_table[(size_t)(b0 + tid) * a.width + (n.len >> a.shift)] : -1;
     }
     __syncthreads();
-    const int top = count - 1 - (int)got.pages;  // the run's first page on the stack
-    for (int i = tid; i < (int)part.pages; i += kThreads) {
+    const int top = count - 1 - (int)got.pages;  // these sequences' first page on the stack
+    const int first = blockIdx.x * threads + tid, step = gridDim.x * threads;
+    for (int i = first; i < (int)part.pages; i += step) {
       const int s = find(s_page, m, i);
       const int page = a.free_pages[top - i];
       if (page < 0 || page >= a.num_pages) bad = true;
-      a.page_table[(size_t)(c + s) * a.width + s_held[s] + (i - s_page[s])] = page;
+      a.page_table[(size_t)(b0 + s) * a.width + s_held[s] + (i - s_page[s])] = page;
     }
-    for (int i = tid; i < (int)part.rows; i += kThreads) {
+    for (int i = first; i < (int)part.rows; i += step) {
       const int s = find(s_row, m, i);
       const int pos = s_len[s] + (i - s_row[s]);
       const int j = (pos >> a.shift) - s_held[s];
@@ -191,33 +153,44 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(PagesArgs a) {
       const bool ok = page >= 0 && page < a.num_pages;
       if (!ok) bad = true;
       a.positions[got.rows + i] = pos;
-      a.slots[got.rows + i] = ok ? ((int64_t)page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
+      a.slots[got.rows + i] = ok ? ((int64_t)page << a.shift) + (pos & (page_tokens - 1)) : -1;
     }
     got = got + part;
-    __syncthreads();
+    if (b0 + threads < a.B) __syncthreads();
   }
-  for (long long i = all.rows + rank * kThreads + tid; i < a.rows; i += ranks * kThreads) {
+  for (long long i = got.rows + blockIdx.x * threads + tid; i < a.rows; i += gridDim.x * threads) {
     a.positions[i] = -1;
     a.slots[i] = -1;
   }
   if (bad) atomicExch(a.status, MOE_ERR_INVALID_ARG);
-  cluster.sync();  // no CTA leaves while another still reads its sums
+  if (!last_to_come(a.ticket)) return;
+  if (tid == 0) {
+    a.free_out[0] = stack - (int)got.pages;
+    a.free_out[1] = (int)min(asked.pages - got.pages, (long long)INT32_MAX);
+    a.q_start[a.B] = (int)got.rows;
+  }
+  const bool once = a.B <= threads;  // this thread's sequence is still in hand
+  asked = got = {0, 0};
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
+    if (!once) n = sequences(b0, &at, &part);
+    if (b0 + tid < a.B) {
+      a.q_start[b0 + tid] = (int)(got.rows + at.rows);
+      a.lens_out[b0 + tid] = n.len + n.fresh;
+    }
+    got = got + part;
+  }
 }
 
-__global__ void __launch_bounds__(kThreads) release_kernel(PagesArgs a) {
-  __shared__ Sums s_warp[kThreads / 32], s_part;
-  __shared__ int s_page[kThreads];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+__global__ void __launch_bounds__(kMaxThreads) release_kernel(PagesArgs a) {
+  __shared__ Sums s_warp[kMaxThreads / 32];
+  __shared__ int s_page[kMaxThreads];
+  const int tid = threadIdx.x, threads = blockDim.x;
   grid_dep_launch();
   grid_dep_wait();
-  const int run = (a.B + ranks - 1) / ranks;
-  const int b0 = min(rank * run, a.B), b1 = min(b0 + run, a.B);
   bool bad = false;
   const int stack = a.free_state[0];
-  if (tid < kThreads / 32) s_warp[tid] = {0, 0};
   auto pages_of = [&](int b) {
-    if (b >= b1 || !a.done[b]) return 0;
+    if (b >= a.B || !a.done[b]) return 0;
     const int len = a.lens[b];
     if (len < 0 || len > ((long long)a.width << a.shift)) {
       bad = true;
@@ -225,63 +198,64 @@ __global__ void __launch_bounds__(kThreads) release_kernel(PagesArgs a) {
     }
     return (len + (1 << a.shift) - 1) >> a.shift;
   };
-  Sums mine{0, 0}, all, part;
-  for (int c = b0; c < b1; c += kThreads) {
-    scan_before({pages_of(c + tid), 0}, s_warp, &part);
-    mine = mine + part;
+  const bool once = a.B <= threads;
+  Sums all{0, 0}, to{0, 0}, at, part;
+  int n = 0;
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
+    n = pages_of(b0 + tid);
+    at = scan_before({n, 0}, s_warp, &part);
+    all = all + part;
   }
-  Sums to = cluster_before(cluster, mine, &s_part, &all);
-  // a stack that cannot hold them all takes none: all conversations stay as they are
+  // a stack that cannot hold them all takes none: all sequences stay as they are
   const bool fits = stack >= 0 && stack <= a.capacity && all.pages <= a.capacity - stack;
   if (!fits) bad = true;
-  for (int c = b0; c < b1; c += kThreads) {
-    const int m = min(kThreads, b1 - c), b = c + tid;
-    const int n = pages_of(b);
-    const Sums at = scan_before({n, 0}, s_warp, &part);
-    if (b < b1) {
-      const int len = a.lens[b];
-      s_page[tid] = (int)at.pages;
-      a.lens_out[b] = fits && n > 0 ? 0 : len;  // (one of no tokens stays one)
+  for (int b0 = 0; fits && b0 < a.B; b0 += threads) {
+    const int m = min(threads, a.B - b0);
+    if (!once) {
+      n = pages_of(b0 + tid);
+      at = scan_before({n, 0}, s_warp, &part);
     }
+    if (tid < m) s_page[tid] = (int)at.pages;
     __syncthreads();
-    for (int i = tid; fits && i < (int)part.pages; i += kThreads) {
+    for (int i = blockIdx.x * threads + tid; i < (int)part.pages; i += gridDim.x * threads) {
       const int s = find(s_page, m, i);
-      const int page = a.page_table[(size_t)(c + s) * a.width + (i - s_page[s])];
+      const int page = a.page_table[(size_t)(b0 + s) * a.width + (i - s_page[s])];
       if (page < 0 || page >= a.num_pages) bad = true;
       a.free_pages[stack + to.pages + i] = page;
     }
     to = to + part;
-    __syncthreads();
+    if (!once) __syncthreads();
   }
-  if (rank == 0 && tid == 0) {
+  if (bad) atomicExch(a.status, MOE_ERR_INVALID_ARG);
+  if (!last_to_come(a.ticket)) return;
+  if (tid == 0) {
     a.free_out[0] = stack + (fits ? (int)all.pages : 0);
     a.free_out[1] = 0;
   }
-  if (bad) atomicExch(a.status, MOE_ERR_INVALID_ARG);
-  cluster.sync();
+  for (int b = tid; b < a.B; b += threads) {
+    const int len = a.lens[b], pages = once ? n : pages_of(b);
+    a.lens_out[b] = fits && pages > 0 ? 0 : len;  // (one of no tokens stays one)
+  }
 }
 
+// Few threads' sums are formed sooner (64 sequences, a token each: 256 threads ..., 1024 ...).
+int threads_for(int B, long long each) { return B <= 256 && each <= 1024 ? 256 : kMaxThreads; }
+
 template <class K>
-cudaError_t launch(K kernel, const PagesArgs& a, int ranks, cudaStream_t s) {
-  PdlLaunch L(dim3(ranks), dim3(kThreads), 0, s);
-  cudaLaunchAttribute attr[2];
-  attr[0] = L.attr[0];
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ranks;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  L.cfg.attrs = attr;
-  L.cfg.numAttrs = 2;
+cudaError_t launch(K kernel, const PagesArgs& a, long long each, cudaStream_t s) {
+  const int threads = threads_for(a.B, each);
+  const int ctas = (int)std::min<long long>(64, std::max<long long>(1, (each + threads - 1) / threads));
+  PdlLaunch L(dim3(ctas), dim3(threads), 0, s);
   return cudaLaunchKernelEx(&L.cfg, kernel, a);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_pages_extend(const PagesArgs& a, cudaStream_t s) {
-  return launch(extend_kernel, a, a.B <= kThreads && a.rows <= kThreads ? 1 : kMaxCluster, s);
-}
+cudaError_t launch_kv_pages_extend(const PagesArgs& a, cudaStream_t s) { return launch(extend_kernel, a, a.rows, s); }
 
+// (how many pages there are is not known here: a quarter of the table's entries, say)
 cudaError_t launch_kv_pages_release(const PagesArgs& a, cudaStream_t s) {
-  return launch(release_kernel, a, a.B <= 128 ? 1 : kMaxCluster, s);
+  return launch(release_kernel, a, (long long)a.B * a.width / 4, s);
 }
 
 }  // namespace moe
