@@ -421,9 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 12; i + 1 < kKeys / 2; i += 2) top[i / 2 & 3] = max3(top[i / 2 & 3], s[i], s[i + 1]);
         const float mt = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        // Where a row's maximum grows by much, the maximum in use follows.  (Past this barrier
-        // both warps have read their scores, and weights may take the scores' place.)
-        if (either((mt - m) * c > kGrow)) {
+        // Where a row's maximum grows by much, the maximum in use follows; what lies in rows past
+        // the tile's has no part in it.  (Past this barrier both warps have read their scores, and
+        // weights may take the scores' place.)
+        if (either(live && (mt - m) * c > kGrow)) {
           *mine = mt;
           either(false);
           const float mn = max3(m, mt, *theirs), mcn = mn == -INFINITY ? 0.f : mn * c;

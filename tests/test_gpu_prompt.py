@@ -505,6 +505,20 @@ def test_prompt_is_the_same_each_time():
         assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("G", [3, 7, 100])
+def test_what_was_there_before_does_not_matter(G):
+    """Tiles of whole tokens leave rows over, which hold what an earlier call left there."""
+    rng = np.random.default_rng(22)
+    t, v, start = packed(rng, [700, 50], G, 1, 128)
+    full, _, all_rows = packed(rng, [2048], 16, 16, 128)
+    got = []
+    for scale in (0.0, 1e4, float("nan")):
+        run_prompt([full[0] * scale, full[1], full[2]], all_rows)
+        got.append(run_prompt(t, start))
+    for out, lse, _ in got[1:]:
+        assert np.array_equal(out, got[0][0]) and np.array_equal(lse, got[0][1])
+
+
 def test_prompts_alone_are_the_prompts_together():
     """A prompt's rows do not depend on what it is packed with."""
     rng = np.random.default_rng(19)
