@@ -198,6 +198,12 @@ MOE_DEV void fma2(float& x, float& y, float u, float v, float d) {
       : "+f"(x), "+f"(y)
       : "f"(u), "f"(v), "f"(d));
 }
+MOE_DEV void fma2(float& x, float& y, float u, float v, float d, float e) {
+  asm("{\n .reg .b64 a, b, e;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 e, {%4, %5};\n"
+      " fma.rn.f32x2 a, a, b, e;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v), "f"(d), "f"(e));
+}
 MOE_DEV void mul2(float& x, float& y, float u, float v) {
   asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
       : "+f"(x), "+f"(y)
@@ -209,20 +215,11 @@ MOE_DEV void add2(float& x, float& y, float c, float d) {
       : "f"(c), "f"(d));
 }
 
-// tanh z for |z| < kNear: z times a polynomial in z^2, the interpolation of tanh(z) / z at
-// Chebyshev's nodes of z^2 < kNear^2, off by 4e-9 of it; two at a time.
-constexpr float kNear = 0.625f;
-MOE_DEV void tanh_near2(float& x, float& y) {
-  float u = x, v = y, f = -0.005657135f, g = -0.005657135f;
-  mul2(u, v, x, y);
-  fma2(f, g, u, v, 0.020588191f);
-  fma2(f, g, u, v, -0.05372011f);
-  fma2(f, g, u, v, 0.13331114f);
-  fma2(f, g, u, v, -0.33333260f);
-  fma2(f, g, u, v, 1.f);
-  mul2(x, y, f, g);
-}
-// tanh z = 1 - 2 / (1 + e^(2 z)): off by 2^-21 of it from kNear on
+// tanh z: for |z| < kClose z times a polynomial in z^2, the interpolation of tanh(z) / z at
+// Chebyshev's nodes of z^2 < kClose^2, off by 6e-8 of it; else 1 - 2 / (1 + e^(2 z)), off by
+// 2^-20.4 of it at most.  (The choice is each score's own: a row does not depend on what
+// others hold.)
+constexpr float kClose = 0.375f;
 MOE_DEV float tanh_far(float z) {
   const float y = z * (2.f * kLog2e);
   return 1.f - __fdividef(2.f, 1.f + ex2(y > 80.f ? 80.f : y));  // (2^y stays finite, a NaN stays one)
@@ -234,28 +231,32 @@ MOE_DEV void modified(const PromptArgs& p, float* s, float slope, float gap) {
   const float cap = p.softcap;
   if (cap > 0.f) {
     const float in = p.sm_scale / cap, out = cap * kLog2e;
-    float far = 0.f;
+    const float c0 = 0.99999994f * out, c1 = -0.33331971f * out, c2 = 0.13284431f * out, c3 = -0.048268908f * out;
+    auto close = [&](float& x, float& y) {  // out * tanh
+      float u = x, v = y, f = c3, g = c3;
+      mul2(u, v, x, y);
+      fma2(f, g, u, v, c2);
+      fma2(f, g, u, v, c1);
+      fma2(f, g, u, v, c0);
+      mul2(x, y, f, g);
+    };
+    float most = 0.f;
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
       mul2(s[i], s[i + 1], in, in);
-      far = fmaxf(far, fmaxf(fabsf(s[i]), fabsf(s[i + 1])));
+      most = max3(most, fabsf(s[i]), fabsf(s[i + 1]));
     }
-    if (__any_sync(0xffffffffu, far >= kNear)) {
+    if (__any_sync(0xffffffffu, most >= kClose)) {
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
-        const float x = tanh_far(s[i]), y = tanh_far(s[i + 1]);
-        const bool fx = !(fabsf(s[i]) < kNear), fy = !(fabsf(s[i + 1]) < kNear);
-        tanh_near2(s[i], s[i + 1]);
-        s[i] = fx ? x : s[i];
-        s[i + 1] = fy ? y : s[i + 1];
-        mul2(s[i], s[i + 1], out, out);
+        const float x = s[i], y = s[i + 1];
+        close(s[i], s[i + 1]);
+        if (!(fabsf(x) < kClose)) s[i] = out * tanh_far(x);
+        if (!(fabsf(y) < kClose)) s[i + 1] = out * tanh_far(y);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        tanh_near2(s[i], s[i + 1]);
-        mul2(s[i], s[i + 1], out, out);
-      }
+      for (int i = 0; i < N; i += 2) close(s[i], s[i + 1]);
     }
   } else {
     const float scale = p.sm_scale * kLog2e;
@@ -267,8 +268,9 @@ MOE_DEV void modified(const PromptArgs& p, float* s, float slope, float gap) {
     for (int i = 0; i < N; i += 2) {
       float x = (float)i, y = (float)(i + 1);
       add2(x, y, gap, gap);  // (exact)
-      mul2(x, y, slope, slope);
-      add2(s[i], s[i + 1], x, y);
+      fma2(x, y, slope, slope, s[i], s[i + 1]);
+      s[i] = x;
+      s[i + 1] = y;
     }
   }
 }
