@@ -537,9 +537,10 @@ int kv_pages_release(const int32_t *page_table, int width, const int32_t *lens, 
  * head_dim 64 or 128; heads % kv_heads == 0, heads <= 4096, kv_heads <= 1024;
  * B <= 2^20, total <= 2^24, total * heads < 2^31 - 1024.  B == 0 or total == 0 is a no-op.
  * Rows that no prompt holds are left as they are.  A prompt whose rows do not lie
- * in [0, total) is left out and sets the status word to MOE_ERR_INVALID_ARG.
- * Scores, statistics and sums are fp32 (caps as decode_attention's); the weights
- * are rounded to bf16 for their product with V.  An infinity or a NaN in a row of
+ * in [0, total), or that starts before an earlier one ends, is left out and sets
+ * the status word to MOE_ERR_INVALID_ARG.
+ * Scores, statistics and sums are fp32 (a capped score is within 2^-20 of itself);
+ * the weights are rounded to bf16 for their product with V.  An infinity or a NaN in a row of
  * q makes the row NaN; a NaN in a row's k or v reaches the rows that see it,
  * and no other; what rows outside the prompts hold does not matter.
  * One kernel; results do not depend on the order in which CTAs finish.

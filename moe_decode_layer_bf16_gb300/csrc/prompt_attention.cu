@@ -4,29 +4,37 @@
 //   out = sum_j exp(s_j) v_j / sum_j exp(s_j);  lse = log sum_j exp(s_j).
 //
 // What bounds it: the two products, 4 D flops for each visible pair of a row and a key,
-// on the tensor cores; beside them an exponential for each pair.
+// on the tensor cores; beside them an exponential for each pair.  Measured: one prompt of
+// 8192 tokens, 56 heads of 128 on 8, 962 GFLOP, 617 to 671 us by the power cap's clock
+// (1.43 to 1.56 PFLOP/s, 0.72 to 0.78 of the library product's burst rate; tensor pipe 65%
+// busy); 16 prompts of 20 to 2048 tokens 154 us (1.0 PFLOP/s); 33 tokens 8.9 us.
 //
 // Rows.  The query heads of a key/value head see the same keys, so their rows are packed
 // token by token: row r of a prompt and kv head is token r / G, head r % G.  An item is
-// 256 packed rows of one prompt and kv head, as two tiles of 128, each with its own
-// range of key tiles (128 keys).  Packing wastes nothing whatever the group is and keeps
-// the masked part of a tile small: 128 rows are 128 / G tokens.
+// two tiles of 128 packed rows (or as many as whole tokens fill) of one prompt and kv head,
+// each with its own range of key tiles (128 keys).  Packing wastes next to nothing whatever
+// the group is and keeps the masked part of a tile small: 128 rows are 128 / G tokens.
 //
-// One CTA an SM takes items from a counter, the longest first (of 32 prompts at a time).  Twelve
-// warps: two softmax warpgroups, a tile each; one warp issues the MMAs, one copies keys
-// and values (TMA, a ring of tiles) and hands out the items, two load the queries and
-// look through the values of tiles that not every row sees.  For each key tile
-//   S = Q K^T into tensor memory (tcgen05, fp32), a thread reads its row of S,
+// One CTA an SM takes items from a counter, the longest first (of 32 prompts at a time).
+// Twenty warps: sixteen for the softmax, of which two share a row, half of its columns each;
+// one issues the MMAs, one copies keys and values (TMA, a ring of tiles) and hands out the
+// items, two fetch the queries and look through the values of tiles that not every row sees.
+// For each key tile
+//   S = Q K^T into tensor memory (tcgen05, fp32), a thread reads its half row of S,
 //   p = 2^(s c - m c) in bf16 over S's first columns,
 //   O += P V (P from tensor memory).
 // While one tile's softmax runs, the tensor cores work on the other tile.  The running
 // maximum m is moved, and O and the sum rescaled, only when a row's grows by more than
-// 2^8: until then the weights are up to 2^8, with the same relative precision.
+// 2^8: until then the weights are up to 2^8, with the same relative precision, and a row's
+// two warps need no word of each other but a vote.  (A row a thread, 12 warps: the serving
+// mix 180 us, the same prompt of 8192 tokens; with four more warps that write the results
+// while the next item begins: 180 us, because they take registers and issue slots from the
+// softmax; the results held back until the next item's first weights: 216 us.)
 //
 // What a masked position holds must not matter, but 0 x NaN is NaN: values of tiles
 // that some row does not see in full (the diagonal, a window's edge, a prompt's end) are
 // looked through before their product, infinities and NaN replaced by zeros, and put
-// back at the end into the rows that see them.
+// back at the end into the rows that see them (3 of the serving mix's 154 us).
 #include <cuda.h>
 
 #include <algorithm>
@@ -46,7 +54,8 @@ namespace {
 // mbar_wait_landed for waits that are often long: the thread sleeps up to a millisecond at a
 // time, where one that asks again and again takes its scheduler's slots from the softmax (a
 // serving mix 189 -> 177 us).
-MOE_DEV bool wait(uint64_t* bar, uint32_t parity, int* status) {
+constexpr unsigned long long kItemNs = 5000ull * 1000ull * 1000ull;  // an item of 2^24 keys takes 0.2 s
+MOE_DEV bool wait(uint64_t* bar, uint32_t parity, int* status, unsigned long long limit = kWaitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer_ns();
   do {
@@ -56,7 +65,7 @@ MOE_DEV bool wait(uint64_t* bar, uint32_t parity, int* status) {
         : "=r"(ok) : "r"(su32(bar)), "r"(parity), "r"(1000000u) : "memory");
     if (ok) return true;
     if (*(volatile int*)status == MOE_ERR_DEVICE_TIMEOUT) return false;
-  } while (globaltimer_ns() - t0 < kWaitNs);
+  } while (globaltimer_ns() - t0 < limit);
   atomicExch(status, MOE_ERR_DEVICE_TIMEOUT);
   return false;
 }
@@ -67,7 +76,7 @@ constexpr int kBox = 128 * kKeys;  // bytes of 64 columns of 128 rows
 constexpr int kSlots = 4;     // items handed out ahead
 constexpr int kLooks = 4;     // tiles of values in the ring at most
 constexpr int kThreads = 640;
-constexpr int kMma = 16, kCopy = 17, kHelp = 18;  // warps (the softmax's are the first eight)
+constexpr int kMma = 16, kCopy = 17, kHelp = 18;  // warps (the softmax's are the first sixteen)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.f;  // log2 of the growth of a row's maximum that is let pass
 
@@ -125,7 +134,7 @@ enum Command : uint32_t {
 struct Bars {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
-  uint64_t item_full[kSlots], item_empty[kSlots], v_done[kSlots], v_ok[kLooks];
+  uint64_t item_full[kSlots], item_empty[kSlots], v_done[kSlots], v_ok[kLooks], drained;
   Item item[kSlots];
   uint32_t cmd[8];
   int bad[kSlots];  // the item met infinities or NaN among values that it looked through
@@ -335,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(b.v_done + i, 2);
     }
     for (int i = 0; i < kLooks; ++i) mbar_init(b.v_ok + i, 2);
+    mbar_init(&b.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMma) {
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The k-th item of this CTA: every role but the copying warp, which makes them.
   auto item = [&](int k, Item* it) {
-    if (!wait(b.item_full + k % kSlots, (k / kSlots) & 1, status)) return false;
+    if (!wait(b.item_full + k % kSlots, (k / kSlots) & 1, status, kItemNs)) return false;
     *it = b.item[k % kSlots];
     return it->n > 0;
   };
@@ -553,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A step is a key tile of an item: its scores, with the products of the step before
         // (whose item may be another one).
         uint32_t cmd = 0, old = 0;
+        bool ended = false;
         Place key, val;
         while (true) {
           bool early = false;
@@ -574,7 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!landed(key)) break;
           cmd = b.cmd[key.st];
-          if (cmd & kEnd) break;
+          if (cmd & kEnd) {
+            ended = true;
+            break;
+          }
           if ((cmd & kHas) && !early && !scores(T0(), key, cmd)) break;
           if ((cmd & (kHas << 1)) && !scores(T1(), key, cmd)) break;
           tc_commit(b.kv_empty + key.st);
@@ -583,6 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           val.next();
           key = val;
           key.next();
+        }
+        if (!ended) {  // a wait failed: no MMA may still be under way when the CTA leaves
+          tc_commit(&b.drained);
+          mbar_wait_landed(&b.drained, 0, status);
         }
       }
       __syncwarp();
@@ -593,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool alive = true;
       // A run of 32 prompts at a time, a lane each.  Their items come by level, the longest first:
       // at level L the L-th block of rows of each prompt that has one.
-      int b0 = -32, before = 0, level = 0, start = 0, n = 0, blocks = 0;  // before: items before this level
+      int b0 = -32, before = 0, level = 0, start = 0, n = 0, blocks = 0, ended = 0;  // before: items before this level; ended: the last row so far
       int next = blockIdx.x;
       for (int k = 0; alive; ++k) {
         int ahead = 0;
@@ -613,12 +631,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           b0 += 32;
           start = n = 0;
+          bool bad = false;
           if (b0 + lane < p.B) {
             start = p.q_start[b0 + lane];
             const int stop = p.q_start[b0 + lane + 1];
-            if (step_rows_ok(start, stop, p.total)) n = stop - start;
-            else if (blockIdx.x == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
+            bad = !step_rows_ok(start, stop, p.total);
+            if (!bad) n = stop - start;
           }
+          // a prompt that starts before an earlier one ends is none either
+          int end = n > 0 ? start + n : 0;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int before_it = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end = max(end, before_it);
+          }
+          int prior = __shfl_up_sync(0xffffffffu, end, 1);
+          prior = lane > 0 ? max(prior, ended) : ended;
+          ended = max(ended, __shfl_sync(0xffffffffu, end, 31));
+          if (n > 0 && start < prior) {
+            n = 0;
+            bad = true;
+          }
+          if (bad && blockIdx.x == 0) atomicExch(status, MOE_ERR_INVALID_ARG);
           blocks = (n * G + 2 * p.rows - 1) / (2 * p.rows);
           level = __reduce_max_sync(0xffffffffu, blocks);
         }
@@ -635,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.t[0] = range_of(it.n, it.row0, p.rows, G, window);
           it.t[1] = range_of(it.n, it.row0 + p.rows, p.rows, G, window);
         }
-        if (!wait(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status)) break;
+        if (!wait(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status, kItemNs)) break;
         if (lane == 0) {
           b.item[k % kSlots] = it;
           b.bad[k % kSlots] = 0;
@@ -690,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item it;
       for (int k = 0; alive && item(k, &it); ++k) {
         if (it.t[t].lo <= it.t[t].hi) {
-          if (!wait(b.q_empty + t, (fills & 1) ^ 1, status)) break;
+          if (!wait(b.q_empty + t, (fills & 1) ^ 1, status, kItemNs)) break;
           ++fills;
           if (p.rows % G == 0) {
             // whole tokens: one copy for 64 columns
