@@ -455,7 +455,8 @@ int decode_attention(const moe_kv_cache *cache, const void *q, long long q_strid
  * rmsnorm_residual whose output is what fp8_block_gemm reads:
  *   r' = x + residual (fp32; x NULL: the residual);  residual_out = bf16(r');
  *   y = residual_out * rsqrt(mean(residual_out^2) + eps) * gain   (fp32);
- *   codes, scales = the quantisation of fp8_quant_rows, of y unrounded;
+ *   codes, scales = the quantisation of fp8_quant_rows, of y unrounded (y / s to an
+ *   fp32 step);
  *   out = bf16(y), where out is not NULL.
  *   x, residual   bf16 [M, H], rows x_stride / residual_stride elements apart
  *                 (>= H, % 8 == 0)

@@ -351,10 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&b.tmem)), "r"(512) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  grid_dep_launch();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_launch();  // (not before the tensor memory is this CTA's: the next kernel may want some and wait for this one)
   // All of tensor memory is this CTA's, so it starts at 0: S (and P) of tile t at 128 t, O at 256 + 128 t.
   constexpr uint32_t tmem = 0;
   grid_dep_wait();

@@ -11,10 +11,10 @@ from __future__ import annotations
 
 import torch
 
-from . import moe_workspace_init
+from . import moe_device_status, moe_workspace_init
 from .attention import (AttentionDecode, _bf16, _calls, _f32, _fail, _handle, _i32, _size, _torch_stream, _u8, _want,
-                        _want_device, _want_rows, _want_workspace, fp8_block_gemm, fp8_linear, kv_cache_append,
-                        kv_cache_workspace_size)
+                        _want_device, _want_rows, _want_workspace, fp8_block_gemm, fp8_linear, fp8_linear_workspace_size,
+                        kv_cache_append, kv_cache_workspace_size)
 
 _i64 = torch.int64
 
@@ -179,7 +179,6 @@ class AttentionPrompt:
     projection."""
 
     def __init__(self, decode: AttentionDecode, max_tokens: int):
-        from .attention import fp8_linear_workspace_size
         self.decode, self.max_tokens = decode, max_tokens
         d = decode
         h, hk, dim, device = d.heads, d.kv_heads, d.head_dim, d.cache.k.device
@@ -193,10 +192,11 @@ class AttentionPrompt:
 
     def __call__(self, x, page_table, q_start, lens, max_new: int, out=None, stream=None):
         """x: bf16 [tokens, hidden], or the (codes, scales) of rmsnorm_residual_fp8;
-        page_table, q_start and lens as kv_cache_append's, every sequence of the step
-        with all its tokens (lens[b] = q_start[b + 1] - q_start[b]); max_new a bound of
-        them.  Rows of no sequence come out as the projection of what their row of
-        the mixed heads holds.  Returns bf16 [tokens, hidden]."""
+        page_table, q_start and lens as kv_cache_append's; max_new a bound of a
+        sequence's rows.  A sequence with rows is new: all its tokens are in the step
+        (lens[b] = q_start[b + 1] - q_start[b]; one that goes on is decode_attention's);
+        sequences without rows are left alone.  Rows of no sequence come out as
+        something.  Returns bf16 [tokens, hidden]."""
         quantised = isinstance(x, (tuple, list))
         rows = x[0] if quantised else x
         if stream is not None:  # (rotate and a new output's memory belong to it as well)
@@ -222,5 +222,4 @@ class AttentionPrompt:
         return out
 
     def status(self) -> int:
-        from . import moe_device_status
         return moe_device_status(self.workspace)

@@ -493,6 +493,27 @@ def test_prompt_strides_and_no_lse():
     assert np.array_equal(f, g)
 
 
+@pytest.mark.parametrize("D,n,window", [(128, 70001, 0), (64, 150000, 40000)])
+def test_prompt_of_a_long_document(D, n, window):
+    """Some rows of it, among them the first and the last, in float64."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(23)
+    qkv = torch.randn((n, 4, D), generator=g, device=DEV).to(torch.bfloat16)
+    q, k, v = qkv[:, :2], qkv[:, 2:3], qkv[:, 3:]
+    out, lse, ws = torch.empty_like(q, memory_format=torch.contiguous_format), torch.empty((n, 2), device=DEV), workspace()
+    m.prompt_attention(q, k, v, dev(np.array([0, n], np.int32)), out, ws, lse=lse, window=window)
+    assert m.moe_device_status(ws) == m.MOE_OK
+    for row in (0, 1, 127, 128, 40000, 40001, n // 2 + 77, n - 129, n - 1):
+        first = max(0, row - window + 1) if window else 0
+        K, V, Q = (x.double() for x in (k[first:row + 1, 0], v[first:row + 1, 0], q[row]))
+        s = Q @ K.t() / math.sqrt(D)
+        p = torch.softmax(s, dim=1)
+        ref = [x.cpu().numpy() for x in (p @ V, torch.logsumexp(s, dim=1), p @ V.abs(), ((Q.abs() @ K.abs().t()) / math.sqrt(D)).amax(dim=1),
+                                         s.abs().amax(dim=1))]
+        t_out, t_lse = tolerance(ref, D, row + 1 - first)
+        assert (np.abs(host(out[row]) - ref[0]) <= t_out).all() and (np.abs(host(lse[row]) - ref[1]) <= t_lse).all(), row
+
+
 def test_prompt_is_the_same_each_time():
     rng = np.random.default_rng(18)
     t, v, start = packed(rng, rng.integers(1, 400, 20).tolist(), 14, 2, 128)
