@@ -213,6 +213,13 @@ MOE_DEV void fma2(float& x, float& y, float u, float v, float d, float e) {
       : "+f"(x), "+f"(y)
       : "f"(u), "f"(v), "f"(d), "f"(e));
 }
+// (x, y) += (u, v) * c
+MOE_DEV void bias2(float& x, float& y, float u, float v, float c) {
+  asm("{\n .reg .b64 a, b, e;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 e, {%4, %4};\n"
+      " fma.rn.f32x2 a, b, e, a;\n mov.b64 {%0, %1}, a;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(u), "f"(v), "f"(c));
+}
 MOE_DEV void mul2(float& x, float& y, float u, float v) {
   asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
       : "+f"(x), "+f"(y)
@@ -273,13 +280,11 @@ MOE_DEV void modified(const PromptArgs& p, float* s, float slope, float gap) {
     for (int i = 0; i < N; i += 2) mul2(s[i], s[i + 1], scale, scale);
   }
   if (p.slopes) {
+    float x = gap, y = gap + 1.f;  // (whole numbers below 2^24: exact)
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      float x = (float)i, y = (float)(i + 1);
-      add2(x, y, gap, gap);  // (exact)
-      fma2(x, y, slope, slope, s[i], s[i + 1]);
-      s[i] = x;
-      s[i + 1] = y;
+      bias2(s[i], s[i + 1], x, y, slope);
+      add2(x, y, 2.f, 2.f);
     }
   }
 }
