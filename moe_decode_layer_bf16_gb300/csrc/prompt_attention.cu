@@ -459,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
               tc_st16(to + i, w);
             }
+            // both halves of O are rescaled before either warp's weights let products at them
+            tc_wait_st();
+            tc_fence_before();
+            either(false);
           }
           m = mn;
           mc = mcn;

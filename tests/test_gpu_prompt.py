@@ -472,6 +472,23 @@ def test_prompt_far_scores():
         assert status == m.MOE_OK and (np.abs(out - ref[0]) <= t_out).all() and (np.abs(lse - ref[1]) <= t_lse).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,hk", [(7, 2), (1, 4), (16, 1)])
+def test_prompt_rows_that_see_themselves(D, G, hk):
+    """With a window of one token a row's result is its value, bit for bit; in most key tiles
+    of an item some rows see nothing, so that the maximum in use is moved in the midst of it.
+    Many times over: what one warp rescales while products run shows now and then only."""
+    rng = np.random.default_rng(24)
+    t, v, start = packed(rng, [1748, 1, 633, 300], G * hk, hk, D)
+    want = t[2].repeat_interleave(G, 1)
+    out, ws, s = torch.empty_like(want), workspace(), dev(start)
+    for _ in range(400):
+        out.zero_()
+        m.prompt_attention(*t, s, out, ws, window=1)
+        assert torch.equal(out, want)
+    assert m.moe_device_status(ws) == m.MOE_OK
+
+
 def test_prompt_strides_and_no_lse():
     """Queries, keys and values of matrices of their own, with gaps of their own; far rows."""
     rng = np.random.default_rng(17)
