@@ -26,10 +26,10 @@
 // While one tile's softmax runs, the tensor cores work on the other tile.  The running
 // maximum m is moved, and O and the sum rescaled, only when a row's grows by more than
 // 2^8: until then the weights are up to 2^8, with the same relative precision, and a row's
-// two warps need no word of each other but a vote.  (A row a thread, 12 warps: the serving
-// mix 180 us, the same prompt of 8192 tokens; with four more warps that write the results
-// while the next item begins: 180 us, because they take registers and issue slots from the
-// softmax; the results held back until the next item's first weights: 216 us.)
+// two warps need no word of each other but a vote.  (With a row a thread, 12 warps in all,
+// the serving mix takes 180 us and the long prompt as long as now; with four more warps that
+// write the results while the next item begins 180, because they take registers and issue
+// slots from the softmax.)
 //
 // What a masked position holds must not matter, but 0 x NaN is NaN: values of tiles
 // that some row does not see in full (the diagonal, a window's edge, a prompt's end) are
