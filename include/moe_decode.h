@@ -533,7 +533,7 @@ int kv_pages_release(const int32_t *page_table, int width, const int32_t *lens, 
  *   q     bf16 [total, heads, head_dim], k, v bf16 [total, kv_heads, head_dim],
  *         rows q_stride / k_stride / v_stride elements apart (% 8 == 0; slices of
  *         a fused projection do), 16-byte aligned
- *   out   bf16 [total, heads, head_dim];  lse fp32 [total, heads] or NULL
+ *   out   bf16 [total, heads, head_dim], 16-byte aligned;  lse fp32 [total, heads] or NULL
  *   slopes fp32 [heads] or NULL
  * head_dim 64 or 128; heads % kv_heads == 0, heads <= 4096, kv_heads <= 1024;
  * B <= 2^20, total <= 2^24, total * heads < 2^31 - 1024.  B == 0 or total == 0 is a no-op.

@@ -339,7 +339,9 @@ struct PromptArgs {
   float sm_scale, softcap;
   int* status;
   int* tickets;
-  int rows;  // packed rows of a tile (the launch's)
+  // the launch's
+  int rows;    // packed rows of a tile
+  bool out32;  // out lies on a multiple of 32 bytes
 };
 cudaError_t launch_prompt_attention(const PromptArgs& a, int sms, cudaStream_t s);
 

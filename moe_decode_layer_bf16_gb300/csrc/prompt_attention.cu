@@ -174,12 +174,21 @@ MOE_DEV void tc_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// 16 bf16 values, rounded, to 32 bytes of memory
-MOE_DEV void store16(void* to, const float* f) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(pack_bf16(f[0], f[1])),
-               "r"(pack_bf16(f[2], f[3])), "r"(pack_bf16(f[4], f[5])), "r"(pack_bf16(f[6], f[7])), "r"(pack_bf16(f[8], f[9])),
-               "r"(pack_bf16(f[10], f[11])), "r"(pack_bf16(f[12], f[13])), "r"(pack_bf16(f[14], f[15]))
-               : "memory");
+// 16 bf16 values, rounded, to 32 bytes of memory: one store, where the place is a multiple of
+// 32 bytes (a store's address is one of its size), else two.
+MOE_DEV void store16(void* to, const float* f, bool whole) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};\n st.global.v4.b32 [%0 + 16], {%5,%6,%7,%8};" ::"l"(to), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  }
 }
 MOE_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[e] *= inv;
-        if (live) store16(out + i, o);
+        if (live) store16(out + i, o, p.out32);
       }
       tc_fence_before();
       if (p.lse && live && h == 0) p.lse[at] = (mc + log2f(l)) * kLn2;
@@ -867,6 +876,7 @@ cudaError_t launch_prompt_attention(const PromptArgs& args, int sms, cudaStream_
   // A tile's rows: whole tokens, which one copy brings, where that fills it to 7 / 8; else 128.
   const int whole = kRows / a.G * a.G;
   a.rows = 8 * whole >= 7 * kRows ? whole : kRows;
+  a.out32 = ((uintptr_t)a.out & 31) == 0;  // (a row's 16 values lie a multiple of 32 bytes behind)
   // (a cap's inverse, and the cap times log2 e, stay finite; no score comes near either end)
   if (a.softcap > 0.f) a.softcap = std::min(std::max(a.softcap, 0x1p-100f), 0x1p100f);
   const float c = a.sm_scale * kLog2e;
