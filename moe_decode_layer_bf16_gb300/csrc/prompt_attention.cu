@@ -69,6 +69,12 @@ MOE_DEV bool wait(uint64_t* bar, uint32_t parity, int* status, unsigned long lon
   atomicExch(status, MOE_ERR_DEVICE_TIMEOUT);
   return false;
 }
+// The same for a whole warp: its lanes go on or give up together.  (Each reads the clock and
+// the status for itself, and one that went on alone would wait for the others at the next
+// warp-wide instruction.)
+MOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, int* status, unsigned long long limit = kWaitNs) {
+  return __all_sync(0xffffffffu, wait(bar, parity, status, limit));
+}
 
 constexpr int kKeys = 128;    // keys of a tile
 constexpr int kRows = 128;    // packed rows of a tile
@@ -406,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int heads = G * p.kv_heads;
     uint32_t steps = 0, items = 0;
     Item it;
-    // (A wait that fails leaves the status set, and every later wait gives up at once: a pair's
+    // (A wait that fails leaves the status set, and every later one gives up in a millisecond: a pair's
     // warps go through the same barriers to the item's end either way.)
     for (int k = 0;; ++k) {
       const bool more = item(k, &it);
@@ -626,10 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ================================================================ items, keys and values
       asm volatile("fence.proxy.async.global;" ::: "memory");
       uint32_t ring = 0;
-      bool alive = true;
+      bool alive = true, ended = false;
       // A run of 32 prompts at a time, a lane each.  Their items come by level, the longest first:
       // at level L the L-th block of rows of each prompt that has one.
-      int b0 = -32, before = 0, level = 0, start = 0, n = 0, blocks = 0, ended = 0;  // before: items before this level; ended: the last row so far
+      int b0 = -32, before = 0, level = 0, start = 0, n = 0, blocks = 0, last = 0;  // before: items before this level; last: the last row so far
       int next = blockIdx.x;
       for (int k = 0; alive; ++k) {
         int ahead = 0;
@@ -664,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane >= o) end = max(end, before_it);
           }
           int prior = __shfl_up_sync(0xffffffffu, end, 1);
-          prior = lane > 0 ? max(prior, ended) : ended;
-          ended = max(ended, __shfl_sync(0xffffffffu, end, 31));
+          prior = lane > 0 ? max(prior, last) : last;
+          last = max(last, __shfl_sync(0xffffffffu, end, 31));
           if (n > 0 && start < prior) {
             n = 0;
             bad = true;
@@ -687,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it.t[0] = range_of(it.n, it.row0, p.rows, G, window);
           it.t[1] = range_of(it.n, it.row0 + p.rows, p.rows, G, window);
         }
-        if (!wait(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status, kItemNs)) break;
+        if (!warp_wait(b.item_empty + k % kSlots, ((k / kSlots) & 1) ^ 1, status, kItemNs)) break;
         if (lane == 0) {
           b.item[k % kSlots] = it;
           b.bad[k % kSlots] = 0;
@@ -707,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (wait(b.kv_empty + st, (ring / C::kStages & 1) ^ 1, status)) {
               b.cmd[st] = kEnd;
               mbar_arrive(b.kv_full + st);
+              ended = true;
             }
           }
           for (int j = it.lo(); !end && j <= it.hi(); ++j) {
@@ -721,15 +728,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!alive) break;
           }
-          if (!alive)  // nothing may still be on its way when the CTA leaves
-            for (uint32_t r = ring > C::kStages ? ring - C::kStages : 0; r < ring; ++r)
-              mbar_wait_landed(b.kv_full + r % C::kStages, r / C::kStages & 1, status);
         }
+        ended = __any_sync(0xffffffffu, ended);
         if (end) break;
         ring = __shfl_sync(0xffffffffu, __reduce_max_sync(0xffffffffu, ring), 0);
         alive = __all_sync(0xffffffffu, alive);
         next = (int)gridDim.x + __shfl_sync(0xffffffffu, ahead, 0);
       }
+      // nothing may still be on its way when the CTA leaves (at the regular end all has been used)
+      for (uint32_t r = ring > C::kStages ? ring - C::kStages : 0; !ended && r < ring; ++r)
+        mbar_wait_landed(b.kv_full + r % C::kStages, r / C::kStages & 1, status);
       // the last CTA leaves the counters as it found them
       if (lane == 0 && atom_add_acq_rel(p.tickets + 1, 1) == (int)gridDim.x - 1) p.tickets[0] = p.tickets[1] = 0;
     } else {
@@ -740,9 +748,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ring = 0, fills = 0, edges = 0;
       bool alive = true;
       Item it;
-      for (int k = 0; alive && item(k, &it); ++k) {
+      for (int k = 0; alive && __all_sync(0xffffffffu, item(k, &it)); ++k) {
         if (it.t[t].lo <= it.t[t].hi) {
-          if (!wait(b.q_empty + t, (fills & 1) ^ 1, status, kItemNs)) break;
+          if (!warp_wait(b.q_empty + t, (fills & 1) ^ 1, status, kItemNs)) break;
           ++fills;
           if (p.rows % G == 0) {
             // whole tokens: one copy for 64 columns
@@ -786,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // could not tell its phase from the last but one
         for (int i = 0; alive && i < 2 * (it.hi() - it.lo() + 1); ++i, ++ring) {
           const uint32_t st = ring % C::kStages;
-          if (!wait(b.kv_full + st, ring / C::kStages & 1, status)) { alive = false; break; }
+          if (!warp_wait(b.kv_full + st, ring / C::kStages & 1, status)) { alive = false; break; }
           if (!(i & 1) || !it.edge(it.lo() + i / 2, window)) {
             __syncwarp();
             if (lane == 0) mbar_arrive(b.kv_empty + st);

@@ -26,3 +26,25 @@ def test_prompt_results_at_any_16_bytes(D, at):
     m.prompt_attention(*t, dev(start), out, ws)
     assert m.moe_device_status(ws) == m.MOE_OK and np.array_equal(host(out), want)
     assert bool((room[:at] == 7).all()) and bool((room[at + n:] == 7).all())
+
+
+# ---------------------------------------------------------------- waits that give up
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 5)])
+def test_prompt_gives_up_as_a_whole(D, G):
+    """With an earlier call's time-out still in the status word no wait lasts longer than some
+    milliseconds, which an item of this document does: whatever has been reached by then, the
+    call ends, says so, leaves the rows of no prompt and the workspace as they were, and the
+    next call is right."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(41)
+    n = 200000
+    qkv = torch.randn((n + 2, G + 2, D), generator=g, device=DEV).to(torch.bfloat16)
+    out, ws = torch.full((n + 2, G, D), 7.0, dtype=torch.bfloat16, device=DEV), workspace()
+    ws.view(torch.int32)[0] = m.MOE_ERR_DEVICE_TIMEOUT
+    start = dev(np.array([1, n + 1], np.int32))
+    m.prompt_attention(qkv[:, :G], qkv[:, G:G + 1], qkv[:, G + 1:], start, out, ws)
+    assert m.moe_device_status(ws) == m.MOE_ERR_DEVICE_TIMEOUT and not ws.any()
+    assert bool((out[0] == 7).all()) and bool((out[n + 1] == 7).all())
+    t, v, start = packed(np.random.default_rng(42), [300, 40], 6, 2, D)
+    got, want = run_prompt(t, start, ws=ws), run_prompt(t, start)
+    assert got[2] == m.MOE_OK and np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
