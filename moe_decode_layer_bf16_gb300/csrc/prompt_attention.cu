@@ -587,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A step is a key tile of an item: its scores, with the products of the step before
         // (whose item may be another one).
         uint32_t cmd = 0, old = 0;
-        bool ended = false;
         Place key, val;
         while (true) {
           bool early = false;
@@ -609,10 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!landed(key)) break;
           cmd = b.cmd[key.st];
-          if (cmd & kEnd) {
-            ended = true;
-            break;
-          }
+          if (cmd & kEnd) break;
           if ((cmd & kHas) && !early && !scores(T0(), key, cmd)) break;
           if ((cmd & (kHas << 1)) && !scores(T1(), key, cmd)) break;
           tc_commit(b.kv_empty + key.st);
@@ -622,10 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           key = val;
           key.next();
         }
-        if (!ended) {  // a wait failed: no MMA may still be under way when the CTA leaves
-          tc_commit(&b.drained);
-          mbar_wait_landed(&b.drained, 0, status);
-        }
+        // No MMA, and no arrival at a barrier that one is to make, may still be under way when the
+        // CTA leaves (the last tiles' ring places and queries are given back, and nobody waits for them).
+        tc_commit(&b.drained);
+        mbar_wait_landed(&b.drained, 0, status);
       }
       __syncwarp();
     } else if (warp == kCopy) {
