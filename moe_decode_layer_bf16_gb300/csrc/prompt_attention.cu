@@ -456,7 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Where a row's maximum grows by much, the maximum in use follows; what lies in rows past
         // the tile's has no part in it.  (Past this barrier both warps have read their scores, and
         // weights may take the scores' place.)
-        if (either(live && (mt - m) * c > kGrow)) {
+        tc_fence_before();
+        const bool grown = either(live && (mt - m) * c > kGrow);
+        tc_fence_after();
+        if (grown) {
           *mine = mt;
           either(false);
           const float mn = max3(m, mt, *theirs), mcn = mn == -INFINITY ? 0.f : mn * c;
@@ -478,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_wait_st();
             tc_fence_before();
             either(false);
+            tc_fence_after();
           }
           m = mn;
           mc = mcn;
