@@ -544,7 +544,8 @@ int kv_pages_release(const int32_t *page_table, int width, const int32_t *lens, 
  * the weights are rounded to bf16 for their product with V.  An infinity or a NaN in a row of
  * q makes the row NaN; a NaN in a row's k or v reaches the rows that see it,
  * and no other; what rows outside the prompts hold does not matter.
- * One kernel; results do not depend on the order in which CTAs finish.
+ * One kernel; results do not depend on the order in which CTAs finish, and a
+ * row's, to the last bit, on no other head or row than those that it sees.
  */
 int prompt_attention_workspace_size(size_t *bytes);
 int prompt_attention(const void *q, long long q_stride, const void *k, long long k_stride, const void *v,

@@ -24,9 +24,9 @@
 //   p = 2^(s c - m c) in bf16 over S's first columns,
 //   O += P V (P from tensor memory).
 // While one tile's softmax runs, the tensor cores work on the other tile.  The running
-// maximum m is moved, and O and the sum rescaled, only when a row's grows by more than
-// 2^8: until then the weights are up to 2^8, with the same relative precision, and a row's
-// two warps need no word of each other but a vote.  (With a row a thread, 12 warps in all,
+// maximum m of a row is moved, and its O and sum rescaled, only when it grows by more than
+// 2^8 (a known refinement of the softmax in one pass): until then the weights are up to 2^8,
+// with the same relative precision, and a row's two warps need no word of each other but a vote.  (With a row a thread, 12 warps in all,
 // the serving mix takes 180 us and the long prompt as long as now; with four more warps that
 // write the results while the next item begins 180, because they take registers and issue
 // slots from the softmax.)
@@ -462,8 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (grown) {
           *mine = mt;
           either(false);
-          const float mn = max3(m, mt, *theirs), mcn = mn == -INFINITY ? 0.f : mn * c;
-          const float f = m == -INFINITY ? 0.f : ex2(mc - mcn);
+          // each row's by its own scores alone: what the warps' other rows hold, other heads and later
+          // tokens, must not move its last bits
+          const float both = fmaxf(mt, *theirs);
+          const bool up = live && (both - m) * c > kGrow;
+          const float mn = up ? both : m, mcn = up ? both * c : mc;
+          const float f = !up ? 1.f : m == -INFINITY ? 0.f : ex2(mc - mcn);
           l0 *= f;
           l1 *= f;
           if (j > rg.lo) {  // (this tile's products so far were complete before S was)

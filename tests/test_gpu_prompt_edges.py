@@ -48,3 +48,29 @@ def test_prompt_gives_up_as_a_whole(D, G):
     t, v, start = packed(np.random.default_rng(42), [300, 40], 6, 2, D)
     got, want = run_prompt(t, start, ws=ws), run_prompt(t, start)
     assert got[2] == m.MOE_OK and np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+# ---------------------------------------------------------------- what a row depends on
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,hk", [(7, 1), (1, 3), (40, 1)])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=25.0), dict(window=90)])
+def test_prompt_with_another_end(D, G, hk, kw):
+    """The rows of a prompt's start are the same bit for bit whatever follows them, and a head's
+    whatever the other heads hold: the running maximum of loud rows moves while that of the
+    quiet ones, a warp's other rows, stays."""
+    rng = np.random.default_rng(43)
+    n, same = 500, 311
+    t, v, start = packed(rng, [n], G * hk, hk, D)
+    q, k, val = (x.clone() for x in t)
+    k[:] *= torch.linspace(0.2, 3.0, n, device=DEV).to(torch.bfloat16)[:, None, None]  # (scores grow along the rows)
+    first = run_prompt((q, k, val), start, **kw)
+    q[same:] *= 30.0
+    k[same:] *= -2.0
+    if G > 1:
+        q[:, 1::2] *= 16.0
+    after = run_prompt((q, k, val), start, **kw)
+    heads = slice(0, None, 2) if G > 1 else slice(None)
+    assert first[2] == after[2] == m.MOE_OK
+    assert np.array_equal(first[0][:same, heads], after[0][:same, heads]) and np.array_equal(first[1][:same, heads], after[1][:same, heads])
+    alone = run_prompt([x[:same] for x in (q, k, val)], np.array([0, same], np.int32), **kw)
+    assert np.array_equal(alone[0], after[0][:same]) and np.array_equal(alone[1], after[1][:same])
