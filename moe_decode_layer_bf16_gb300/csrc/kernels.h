@@ -340,8 +340,9 @@ struct PromptArgs {
   int* status;
   int* tickets;
   // the launch's
-  int rows;    // packed rows of a tile
-  bool out32;  // out lies on a multiple of 32 bytes
+  int rows;      // packed rows of a tile
+  bool out32;    // out lies on a multiple of 32 bytes
+  float cap_in;  // sm_scale / softcap
 };
 cudaError_t launch_prompt_attention(const PromptArgs& a, int sms, cudaStream_t s);
 

@@ -38,6 +38,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "async.cuh"
@@ -261,7 +262,7 @@ template <int N>
 MOE_DEV void modified(const PromptArgs& p, float* s, float slope, float gap) {
   const float cap = p.softcap;
   if (cap > 0.f) {
-    const float in = p.sm_scale / cap, out = cap * kLog2e;
+    const float in = p.cap_in, out = cap * kLog2e;
     const float c0 = 0.99999994f * out, c1 = -0.33331971f * out, c2 = 0.13284431f * out, c3 = -0.048268908f * out;
     auto close = [&](float& x, float& y) {  // out * tanh
       float u = x, v = y, f = c3, g = c3;
@@ -889,8 +890,10 @@ cudaError_t launch_prompt_attention(const PromptArgs& args, int sms, cudaStream_
   const int whole = kRows / a.G * a.G;
   a.rows = 8 * whole >= 7 * kRows ? whole : kRows;
   a.out32 = ((uintptr_t)a.out & 31) == 0;  // (a row's 16 values lie a multiple of 32 bytes behind)
-  // (a cap's inverse, and the cap times log2 e, stay finite; no score comes near either end)
+  // The cap times log2 e and the factor under the tanh stay finite: no score comes near the caps'
+  // ends, and with the factor at its own every score but zero has the cap for its size.
   if (a.softcap > 0.f) a.softcap = std::min(std::max(a.softcap, 0x1p-100f), 0x1p100f);
+  a.cap_in = a.softcap > 0.f ? std::min(std::max(a.sm_scale / a.softcap, -FLT_MAX), FLT_MAX) : 0.f;
   const float c = a.sm_scale * kLog2e;
   const bool mods = a.softcap > 0.f || a.slopes || !(c > 1e-30f && c < 1e30f);
   if (a.D == 64) return mods ? launch_as<64, true>(a, sms, s) : launch_as<64, false>(a, sms, s);

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import moe_decode_layer_bf16_gb300 as m
-from tests.test_gpu_prompt import DEV, dev, host, packed, run_prompt, workspace
+from oracle import prompt_oracle as orc
+from tests.test_gpu_prompt import DEV, dev, host, packed, run_prompt, tolerance, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -74,3 +75,21 @@ def test_prompt_with_another_end(D, G, hk, kw):
     assert np.array_equal(first[0][:same, heads], after[0][:same, heads]) and np.array_equal(first[1][:same, heads], after[1][:same, heads])
     alone = run_prompt([x[:same] for x in (q, k, val)], np.array([0, same], np.int32), **kw)
     assert np.array_equal(alone[0], after[0][:same]) and np.array_equal(alone[1], after[1][:same])
+
+
+# ---------------------------------------------------------------- caps
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sm_scale", [1e9, -1e9, 3e38])
+@pytest.mark.parametrize("softcap", [1e-30, 1e-38])
+def test_prompt_caps_far_below_the_scale(D, sm_scale, softcap):
+    """Scores within 1e-30 of zero, some of them zero itself: every row is the mean of what it
+    sees, as with queries of zeros."""
+    rng = np.random.default_rng(44)
+    t, v, start = packed(rng, [200, 9], 4, 2, D)
+    q = t[0].clone()
+    q[50:90] = 0.0
+    q[120, 1] = 0.0
+    out, lse, status = run_prompt((q, t[1], t[2]), start, sm_scale, softcap=softcap)
+    ref = orc.attention(np.zeros_like(v[0]), v[1], v[2], start, 1.0)
+    t_out, t_lse = tolerance(ref, D, 200)
+    assert status == m.MOE_OK and (np.abs(out - ref[0]) <= t_out).all() and (np.abs(lse - ref[1]) <= t_lse).all()
