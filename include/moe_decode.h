@@ -546,12 +546,22 @@ int kv_pages_release(const int32_t *page_table, int width, const int32_t *lens, 
  * and no other; what rows outside the prompts hold does not matter.
  * One kernel; results do not depend on the order in which CTAs finish, and a
  * row's, to the last bit, on no other head or row than those that it sees.
+ *
+ * prompt_attention_checked is the same, told how many tokens the sequences hold:
+ * lens int32 [B], as kv_cache_append takes it (NULL: nothing is checked).  A
+ * prompt with rows that are not all of its tokens (lens[b] is not q_start[b + 1]
+ * - q_start[b]: one that goes on from what the cache holds, which only
+ * decode_attention attends) is left out and sets the status word as well.
  */
 int prompt_attention_workspace_size(size_t *bytes);
 int prompt_attention(const void *q, long long q_stride, const void *k, long long k_stride, const void *v,
                      long long v_stride, int heads, int kv_heads, int head_dim, const int32_t *q_start, int B, int total,
                      float sm_scale, float softcap, int window, const float *slopes, void *out, float *lse, void *ws,
                      size_t ws_bytes, void *stream);
+int prompt_attention_checked(const void *q, long long q_stride, const void *k, long long k_stride, const void *v,
+                             long long v_stride, int heads, int kv_heads, int head_dim, const int32_t *q_start,
+                             const int32_t *lens, int B, int total, float sm_scale, float softcap, int window,
+                             const float *slopes, void *out, float *lse, void *ws, size_t ws_bytes, void *stream);
 
 /* Expert kernels (moe_decode_layer_plan, moe_set_expert_path). */
 enum moe_expert_path {

@@ -31,8 +31,10 @@ def bind(L):
     L.prompt_attention_workspace_size.argtypes = [psz]
     L.prompt_attention.argtypes = [_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _i, _vp, _i, _i, _f, _f, _i, _vp, _vp, _vp, _vp,
                                    _sz, _vp]
+    L.prompt_attention_checked.argtypes = [_vp, _ll, _vp, _ll, _vp, _ll, _i, _i, _i, _vp, _vp, _i, _i, _f, _f, _i, _vp, _vp,
+                                           _vp, _vp, _sz, _vp]
     for n in ("rmsnorm_residual_fp8", "kv_pages_extend", "kv_pages_release", "prompt_attention_workspace_size",
-              "prompt_attention", "fp8_quant_rows", "fp8_block_gemm_workspace_size", "fp8_block_gemm", "fp8_linear_workspace_size",
+              "prompt_attention", "prompt_attention_checked", "fp8_quant_rows", "fp8_block_gemm_workspace_size", "fp8_block_gemm", "fp8_linear_workspace_size",
               "fp8_linear", "kv_cache_workspace_size", "kv_cache_append", "decode_attention_workspace_size",
               "decode_attention"):
         getattr(L, n).restype = ctypes.c_int

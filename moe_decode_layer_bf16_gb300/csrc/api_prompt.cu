@@ -105,10 +105,10 @@ int prompt_attention_workspace_size(size_t* bytes) {
   return MOE_OK;
 }
 
-int prompt_attention(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
-                     long long v_stride, int heads, int kv_heads, int head_dim, const int32_t* q_start, int B, int total,
-                     float sm_scale, float softcap, int window, const float* slopes, void* out, float* lse, void* ws,
-                     size_t ws_bytes, void* stream) {
+int prompt_attention_checked(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                             long long v_stride, int heads, int kv_heads, int head_dim, const int32_t* q_start,
+                             const int32_t* lens, int B, int total, float sm_scale, float softcap, int window,
+                             const float* slopes, void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   if (B < 0 || total < 0 || heads < 1 || kv_heads < 1 || head_dim < 1) return MOE_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return MOE_ERR_UNSUPPORTED;
   if (heads % kv_heads || heads > 4096 || kv_heads > 1024) return MOE_ERR_UNSUPPORTED;
@@ -127,11 +127,19 @@ int prompt_attention(const void* q, long long q_stride, const void* k, long long
   const Ws l(ws);
   PromptArgs a;
   a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
-  a.q_start = q_start; a.slopes = slopes; a.out = out; a.lse = lse;
+  a.q_start = q_start; a.lens = lens; a.slopes = slopes; a.out = out; a.lse = lse;
   a.kv_heads = kv_heads; a.G = heads / kv_heads; a.D = head_dim; a.B = B; a.total = total;
   a.window = std::min(window, kMaxLen); a.sm_scale = sm_scale; a.softcap = softcap;
   a.status = l.status; a.tickets = l.tickets;
   return launch_prompt_attention(a, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int prompt_attention(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                     long long v_stride, int heads, int kv_heads, int head_dim, const int32_t* q_start, int B, int total,
+                     float sm_scale, float softcap, int window, const float* slopes, void* out, float* lse, void* ws,
+                     size_t ws_bytes, void* stream) {
+  return prompt_attention_checked(q, q_stride, k, k_stride, v, v_stride, heads, kv_heads, head_dim, q_start, nullptr, B,
+                                  total, sm_scale, softcap, window, slopes, out, lse, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -308,9 +308,9 @@ PyObject* release(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// q, k, v, q_start, out, workspace, lse, sm_scale, softcap, window, slopes, stream
+// q, k, v, q_start, out, workspace, lse, sm_scale, softcap, window, slopes, stream, lens
 PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return call(n, 12, [&]() -> int {
+  return call(n, 13, [&]() -> int {
     const at::Tensor &q = tensor(a[0]), &k = tensor(a[1]), &v = tensor(a[2]), &start = tensor(a[3]), &out = tensor(a[4]),
                      &work = tensor(a[5]);
     const int dev = q.get_device();
@@ -336,9 +336,10 @@ PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int window = (int)integer(a[9]);
     const size_t bytes = room(work, dev);
     void* s = stream_of(a[11], dev);
-    return prompt_attention(q.data_ptr(), row_stride(q, heads * d), k.data_ptr(), row_stride(k, hk * d), v.data_ptr(),
-                            row_stride(v, hk * d), (int)heads, (int)hk, (int)d, starts, (int)B, (int)total, (float)scale,
-                            (float)cap, window, slopes, out.data_ptr(), lse, work.data_ptr(), bytes, s);
+    const int32_t* lens = a[12] == Py_None ? nullptr : ints(tensor(a[12]), {B}, dev);
+    return prompt_attention_checked(q.data_ptr(), row_stride(q, heads * d), k.data_ptr(), row_stride(k, hk * d), v.data_ptr(),
+                                    row_stride(v, hk * d), (int)heads, (int)hk, (int)d, starts, lens, (int)B, (int)total,
+                                    (float)scale, (float)cap, window, slopes, out.data_ptr(), lse, work.data_ptr(), bytes, s);
   });
 }
 

@@ -331,6 +331,7 @@ struct PromptArgs {
   const void* v;
   long long q_stride, k_stride, v_stride;
   const int32_t* q_start;  // [B + 1]
+  const int32_t* lens;     // [B]: tokens of the sequences, all of them rows here; or null
   const float* slopes;     // [G * kv_heads] or null
   void* out;
   float* lse;

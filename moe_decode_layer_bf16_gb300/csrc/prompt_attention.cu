@@ -677,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           int prior = __shfl_up_sync(0xffffffffu, end, 1);
           prior = lane > 0 ? max(prior, last) : last;
           last = max(last, __shfl_sync(0xffffffffu, end, 31));
-          if (n > 0 && start < prior) {
+          const bool on = n > 0 && p.lens && p.lens[b0 + lane] != n;  // (it goes on from tokens that are no rows here)
+          if (n > 0 && (start < prior || on)) {
             n = 0;
             bad = true;
           }

@@ -105,20 +105,23 @@ def _release_refused(page_table, lens, done, free_pages, free_state, lens_out, f
 
 
 def prompt_attention(q, k, v, q_start, out, workspace, lse=None, sm_scale: float | None = None, softcap: float = 0.0,
-                     window: int = 0, slopes=None, stream=None):
+                     window: int = 0, slopes=None, stream=None, lens=None):
     """Causal attention of packed prompts over themselves: q bf16 [total, heads,
     head dim], k and v bf16 [total, kv heads, head dim], any row stride; rows
     [q_start[b], q_start[b + 1]) are a prompt.  out bf16 like q; lse float32
     [total, heads] or None; sm_scale 1 / sqrt(head dim) by default; slopes
-    float32 [heads]."""
-    rc = _calls().prompt_attention(q, k, v, q_start, out, workspace, lse, sm_scale, softcap, window, slopes, _handle(stream))
+    float32 [heads].  With lens (int32, a value for each prompt: the tokens that its
+    sequence holds) a prompt whose rows are not all of them is left out, and the
+    workspace's status says so."""
+    rc = _calls().prompt_attention(q, k, v, q_start, out, workspace, lse, sm_scale, softcap, window, slopes, _handle(stream),
+                                   lens)
     if rc < 0:
-        _prompt_refused(q, k, v, q_start, out, workspace, lse, slopes)
+        _prompt_refused(q, k, v, q_start, out, workspace, lse, slopes, lens)
     elif rc:
         _fail(rc, "prompt_attention")
 
 
-def _prompt_refused(q, k, v, q_start, out, workspace, lse, slopes):
+def _prompt_refused(q, k, v, q_start, out, workspace, lse, slopes, lens):
     _want_rows(q, "q", (None, None, None))
     total, h, d = q.shape
     _want_rows(k, "k", (total, None, d))
@@ -131,8 +134,10 @@ def _prompt_refused(q, k, v, q_start, out, workspace, lse, slopes):
         _want(lse, "lse", _f32, (total, h))
     if slopes is not None:
         _want(slopes, "slopes", _f32, (h,))
+    if lens is not None:
+        _want(lens, "lens", _i32, (q_start.shape[0] - 1,))
     _want_workspace(workspace)
-    _want_device(q, k, v, q_start, out, lse, slopes, workspace)
+    _want_device(q, k, v, q_start, out, lse, slopes, lens, workspace)
     raise ValueError("prompt_attention: arguments refused")
 
 
@@ -194,9 +199,11 @@ class AttentionPrompt:
         """x: bf16 [tokens, hidden], or the (codes, scales) of rmsnorm_residual_fp8;
         page_table, q_start and lens as kv_cache_append's; max_new a bound of a
         sequence's rows.  A sequence with rows is new: all its tokens are in the step
-        (lens[b] = q_start[b + 1] - q_start[b]; one that goes on is decode_attention's);
-        sequences without rows are left alone.  Rows of no sequence come out as
-        something.  Returns bf16 [tokens, hidden]."""
+        (lens[b] = q_start[b + 1] - q_start[b]).  One that goes on is decode_attention's:
+        its keys and values go into the cache, but its rows are not attended, and
+        status() says MOE_ERR_INVALID_ARG.  Sequences without rows are left alone.
+        Rows of no sequence, or of one that goes on, come out as something.  Returns
+        bf16 [tokens, hidden]."""
         quantised = isinstance(x, (tuple, list))
         rows = x[0] if quantised else x
         if stream is not None:  # (rotate and a new output's memory belong to it as well)
@@ -217,7 +224,7 @@ class AttentionPrompt:
         if d.rotate is not None:
             d.rotate(q, k)
         kv_cache_append(k, v, c.k, c.v, c.k_scale, c.v_scale, page_table, q_start, lens, max_new, self.workspace)
-        prompt_attention(q, k, v, q_start, mixed, self.workspace, **d.options)
+        prompt_attention(q, k, v, q_start, mixed, self.workspace, lens=lens, **d.options)
         fp8_linear(mixed.flatten(1), w["o"], w["o_s"], out, self.workspace, e8m0=d.e8m0)
         return out
 

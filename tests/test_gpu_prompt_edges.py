@@ -8,7 +8,8 @@ import torch
 
 import moe_decode_layer_bf16_gb300 as m
 from oracle import prompt_oracle as orc
-from tests.test_gpu_prompt import DEV, dev, host, packed, run_prompt, tolerance, workspace
+from tests.fixtures_attention import bf16, bf16_values
+from tests.test_gpu_prompt import DEV, dev, host, layers, packed, run_prompt, tolerance, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,45 @@ def test_prompt_caps_far_below_the_scale(D, sm_scale, softcap):
     ref = orc.attention(np.zeros_like(v[0]), v[1], v[2], start, 1.0)
     t_out, t_lse = tolerance(ref, D, 200)
     assert status == m.MOE_OK and (np.abs(out - ref[0]) <= t_out).all() and (np.abs(lse - ref[1]) <= t_lse).all()
+
+
+# ---------------------------------------------------------------- sequences that go on
+@pytest.mark.parametrize("n", [5, 45])  # (prompts are looked at 32 at a time)
+def test_prompts_that_go_on_are_left_out(n):
+    rng = np.random.default_rng(45)
+    rows = rng.integers(0, 60, n)
+    t, v, start = packed(rng, rows.tolist(), 4, 2, 64)
+    want = run_prompt(t, start)
+    exact = np.where(rows > 0, rows, rng.integers(0, 9, n)).astype(np.int32)  # (what has no rows may hold anything)
+    same = run_prompt(t, start, lens=dev(exact))
+    assert same[2] == m.MOE_OK and np.array_equal(same[0], want[0]) and np.array_equal(same[1], want[1])
+    on = (rng.random(n) < 0.4) & (rows > 0)
+    on[rows.argmax()] = True
+    for lens in (exact + 7 * on, np.where(on, exact - 1, exact), np.where(on, -2 ** 31, exact)):
+        out, lse, status = run_prompt(t, start, lens=dev(lens.astype(np.int32)))
+        gone = np.repeat(on, rows)
+        assert status == m.MOE_ERR_INVALID_ARG
+        assert (out[gone] == 7).all() and (lse[gone] == 7).all()
+        assert np.array_equal(out[~gone], want[0][~gone]) and np.array_equal(lse[~gone], want[1][~gone])
+
+
+def test_attention_prompt_reports_a_sequence_that_goes_on():
+    """A step of new prompts and of one sequence that holds more than the step's rows."""
+    rng = np.random.default_rng(46)
+    hidden = 128
+    cache, att, prompt, pages = layers(rng, hidden, 2, 1, 64, 16, 3, 6, 60)
+    new = [np.array(x, np.int32) for x in ([0, 20, 0], [30, 1, 9])]
+    x = bf16(bf16_values(rng, (40, hidden))).to(DEV)
+    pages.extend(dev(new[0]))
+    prompt(x[:20], pages.page_table, pages.q_start, pages.lens, 20)
+    assert prompt.status() == m.MOE_OK  # (sequences without rows are left alone)
+    pages.extend(dev(new[1]))
+    out = prompt(x, pages.page_table, pages.q_start, pages.lens, 30)
+    assert prompt.status() == m.MOE_ERR_INVALID_ARG
+    alone = m.KvPages(cache, 2, 6, 60)
+    alone.extend(dev(np.array([30, 9], np.int32)))
+    rows = list(range(30)) + list(range(31, 40))
+    want = prompt(x[rows].contiguous(), alone.page_table, alone.q_start, alone.lens, 30)
+    assert prompt.status() == m.MOE_OK
+    # (the projections' cells are the same for 39 and 40 rows)
+    assert torch.equal(out[rows], want)
