@@ -79,7 +79,7 @@ def main(argv=None):
         graph.replay()
     lens = pages.lens.tolist()
     pages.release(pages.lens > 0)
-    status = (decode.status(), prompt.status(), moe.moe_device_status(pages.workspace))
+    status = (decode.status(), prompt.status(), pages.status())
     assert status == (moe.MOE_OK,) * 3, status
     assert lens == [n + a.steps + 1 for n in a.prompts], lens
     print(f"prompts of {a.prompts} tokens and {a.steps + 1} steps: {lens} tokens; {int(pages.free[0])} pages free again; "

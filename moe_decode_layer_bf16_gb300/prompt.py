@@ -148,7 +148,8 @@ class KvPages:
     After extend: page_table, q_start and lens are what kv_cache_append and
     decode_attention take, positions and slots [max_rows] describe the step's rows
     (-1 behind the last), free[0] counts the pages left and free[1] those that were
-    asked for and not given."""
+    asked for and not given.  A sequence can also stay as it was because it outgrew its
+    table or the step max_rows: status() says so."""
 
     def __init__(self, cache, batch: int, width: int, max_rows: int):
         n, _, self.page_size, _ = cache.k.shape
@@ -175,6 +176,9 @@ class KvPages:
         """The pages of the sequences with done (bool [batch]) are free again."""
         kv_pages_release(self.page_table, self.lens, done, self.free_pages, self.free, self.page_size, self.num_pages,
                          self.lens, self.free, self.workspace, stream=stream)
+
+    def status(self) -> int:
+        return moe_device_status(self.workspace)
 
 
 class AttentionPrompt:

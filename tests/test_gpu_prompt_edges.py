@@ -136,3 +136,18 @@ def test_attention_prompt_reports_a_sequence_that_goes_on():
     assert prompt.status() == m.MOE_OK
     # (the projections' cells are the same for 39 and 40 rows)
     assert torch.equal(out[rows], want)
+
+
+# ---------------------------------------------------------------- pages
+def test_pages_report_who_was_not_served():
+    """More rows than the step has room for, and a sequence that outgrows its table."""
+    cache = m.Fp8KvCache(40, 1, 64, 16)
+    p = m.KvPages(cache, 3, 4, max_rows=50)
+    assert p.status() == m.MOE_OK
+    for new, lens, status in (([20, 10, 20], [20, 10, 20], m.MOE_OK), ([30, 21, 0], [50, 10, 20], m.MOE_ERR_INVALID_ARG),
+                              ([1, 1, 45], [51, 11, 20], m.MOE_ERR_INVALID_ARG), ([0, 1, 1], [51, 12, 21], m.MOE_OK)):
+        p.extend(dev(np.array(new, np.int32)))
+        assert host(p.lens).tolist() == lens and int(p.q_start[-1]) <= 50
+        assert p.status() == status and p.status() == m.MOE_OK
+    p.release(torch.ones(3, dtype=torch.bool, device=DEV))
+    assert p.status() == m.MOE_OK and host(p.free).tolist() == [40, 0]
