@@ -71,32 +71,36 @@ int kv_pages_extend(int32_t* page_table, int width, const int32_t* lens, const i
                     const int32_t* free_pages, int capacity, const int32_t* free_state, int page_size, int num_pages,
                     int32_t* q_start, int32_t* lens_out, int32_t* free_out, int32_t* positions, int64_t* slots, int rows,
                     void* ws, size_t ws_bytes, void* stream) {
-  const int rc = check_pages(page_table, width, lens, B, free_pages, capacity, free_state, page_size, num_pages, lens_out,
-                             free_out, ws, ws_bytes);
+  int rc = check_pages(page_table, width, lens, B, free_pages, capacity, free_state, page_size, num_pages, lens_out,
+                       free_out, ws, ws_bytes);
   if (rc != MOE_OK) return rc;
   if (rows < 0 || (B > 0 && !new_tokens) || !q_start || (rows > 0 && (!positions || !slots))) return MOE_ERR_INVALID_ARG;
   if (rows > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  int sms = 0;
+  if ((rc = current_device_sms(&sms)) != MOE_OK) return rc;
   PagesArgs a{};
   a.page_table = page_table; a.lens = lens; a.fresh = new_tokens; a.free_pages = const_cast<int32_t*>(free_pages);
   a.free_state = free_state; a.q_start = q_start; a.lens_out = lens_out; a.free_out = free_out; a.positions = positions;
   a.slots = slots; a.width = width; a.shift = shift_of(page_size); a.num_pages = num_pages; a.capacity = capacity; a.B = B;
   a.rows = rows; a.status = Ws(ws).status; a.ticket = Ws(ws).tickets;
-  return launch_kv_pages_extend(a, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_kv_pages_extend(a, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int kv_pages_release(const int32_t* page_table, int width, const int32_t* lens, const uint8_t* done, int B,
                      int32_t* free_pages, int capacity, const int32_t* free_state, int page_size, int num_pages,
                      int32_t* lens_out, int32_t* free_out, void* ws, size_t ws_bytes, void* stream) {
-  const int rc = check_pages(page_table, width, lens, B, free_pages, capacity, free_state, page_size, num_pages, lens_out,
-                             free_out, ws, ws_bytes);
+  int rc = check_pages(page_table, width, lens, B, free_pages, capacity, free_state, page_size, num_pages, lens_out,
+                       free_out, ws, ws_bytes);
   if (rc != MOE_OK) return rc;
   if (B > 0 && !done) return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  if ((rc = current_device_sms(&sms)) != MOE_OK) return rc;
   PagesArgs a{};
   a.page_table = const_cast<int32_t*>(page_table); a.lens = lens; a.done = done; a.free_pages = free_pages;
   a.free_state = free_state; a.lens_out = lens_out; a.free_out = free_out; a.width = width; a.shift = shift_of(page_size);
   a.num_pages = num_pages; a.capacity = capacity; a.B = B; a.status = Ws(ws).status;
   a.ticket = Ws(ws).tickets;
-  return launch_kv_pages_release(a, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  return launch_kv_pages_release(a, sms, (cudaStream_t)stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int prompt_attention_workspace_size(size_t* bytes) {

@@ -321,8 +321,8 @@ struct PagesArgs {
   int* status;
   int* ticket;  // zero between calls
 };
-cudaError_t launch_kv_pages_extend(const PagesArgs& a, cudaStream_t s);
-cudaError_t launch_kv_pages_release(const PagesArgs& a, cudaStream_t s);
+cudaError_t launch_kv_pages_extend(const PagesArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_pages_release(const PagesArgs& a, int sms, cudaStream_t s);
 
 // Causal attention over packed prompts (prompt_attention.cu).
 struct PromptArgs {
