@@ -2,14 +2,18 @@
 allocation, one kernel or one kind of batch: against the oracle, or bit for bit against
 the ordinary call."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
 
 import moe_decode_layer_bf16_gb300 as m
 from oracle import prompt_oracle as orc
+from oracle.moe_oracle import e4m3_decode
 from tests.fixtures_attention import bf16, bf16_values
-from tests.test_gpu_prompt import DEV, dev, host, layers, packed, run_prompt, tolerance, workspace
+from tests.test_gpu_prompt import (DEV, check_norm, check_prompt, dev, host, layers, packed, run_prompt, tolerance,
+                                   workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +155,169 @@ def test_pages_report_who_was_not_served():
         assert p.status() == status and p.status() == m.MOE_OK
     p.release(torch.ones(3, dtype=torch.bool, device=DEV))
     assert p.status() == m.MOE_OK and host(p.free).tolist() == [40, 0]
+
+
+# ---------------------------------------------------------------- infinities and NaN under caps and biases
+MODS = [dict(softcap=20.0), dict(slopes=True), dict(softcap=5.0, slopes=True, window=60)]
+
+
+def options(kw, heads):
+    kw = dict(kw)
+    if kw.pop("slopes", False):
+        kw["slopes"] = np.exp2(-8.0 * np.arange(1, heads + 1) / heads).astype(np.float32)
+    return kw
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kw", MODS)
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_prompt_bad_values_under_caps_and_biases(D, kw, bad):
+    rng = np.random.default_rng(47)
+    H, hk = 4, 2
+    kw = options(kw, H)
+    t, v, start = packed(rng, [300, 200], H, hk, D)
+    ref = orc.attention(*v, start, 1 / math.sqrt(D), **kw)
+    t_out, t_lse = tolerance(ref, D, 300, kw.get("softcap"))
+    at, window = [(0, 0, 5), (140, 1, 63), (299, 0, 7), (300, 1, 9), (431, 0, 40)], kw.get("window", 0)
+    for r, h, c in at:
+        t[2][r, h, c] = bad
+    out, lse, status = run_prompt(t, start, **kw)
+    assert status == m.MOE_OK and (np.abs(lse - ref[1]) <= t_lse).all()
+    hit = np.zeros(out.shape, bool)
+    for r, h, c in at:
+        end = 300 if r < 300 else 500
+        hit[r:min(end, r + window) if window else end, 2 * h:2 * h + 2, c] = True
+    assert not np.isfinite(out[hit]).any() and (np.abs(out - ref[0]) <= t_out)[~hit].all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kw", MODS)
+def test_prompt_bad_keys_and_queries_under_caps_and_biases(D, kw):
+    """A NaN in a key or a query as without caps.  An infinity in a query's row: scores of plus or
+    minus the cap, as the formula says; without a cap NaN."""
+    rng = np.random.default_rng(48)
+    H, hk = 4, 2
+    kw = options(kw, H)
+    cap, window = kw.get("softcap"), kw.get("window", 0)
+    t, v, start = packed(rng, [300, 200], H, hk, D)
+    v[0][17, 0, 0] = v[0][333, 2, 1] = np.inf
+    t[0][17, 0, 0] = t[0][333, 2, 1] = float("inf")
+    with np.errstate(invalid="ignore"):
+        ref = orc.attention(*v, start, 1 / math.sqrt(D), **kw)
+    scores = [x.copy() for x in ref]
+    for a in scores[3:]:  # (such rows' scores are the cap's size, and nothing is lost on the way to it)
+        a[17, 0], a[333, 2] = (0.0 if a is scores[3] else cap or 0.0), (0.0 if a is scores[3] else cap or 0.0)
+    if "slopes" in kw and cap:
+        for r, h, i in ((17, 0, 17), (333, 2, 33)):
+            scores[4][r, h] = cap + kw["slopes"][h] * min(i, (window or 1000) - 1)
+    t_out, t_lse = tolerance(scores, D, 300, cap)
+    t[1][140, 1, 3] = float("nan")
+    t[1][420, 0, 90 % D] = float("nan")
+    t[0][499, 3, D - 1] = float("nan")
+    out, lse, status = run_prompt(t, start, **kw)
+    hit = np.zeros(lse.shape, bool)
+    hit[140:min(300, 140 + window) if window else 300, 2:] = True
+    hit[420:min(500, 420 + window) if window else 500, :2] = True
+    hit[499, 3] = True
+    if not cap:
+        hit[17, 0] = hit[333, 2] = True
+    assert status == m.MOE_OK and np.isnan(out[hit]).all() and np.isnan(lse[hit]).all()
+    assert (np.abs(out - ref[0]) <= t_out)[~hit].all() and (np.abs(lse - ref[1]) <= t_lse)[~hit].all()
+
+
+# ---------------------------------------------------------------- batches
+def test_prompt_of_many_heads_and_many_empty_prompts():
+    rng = np.random.default_rng(49)
+    check_prompt(rng, [3, 130], 2048, 1024, 64)
+    check_prompt(rng, [2, 1], 4096, 1, 128)
+    lens = np.zeros(3000, int)
+    lens[[0, 31, 32, 700, 1999, 2999]] = [5, 140, 1, 300, 64, 9]
+    check_prompt(rng, lens.tolist(), 6, 2, 64, before=3, after=1)
+
+
+# ---------------------------------------------------------------- norm
+@pytest.mark.parametrize("M,H", [(305, 1024), (999, 656), (304, 1024), (400, 512), (311, 256), (5000, 16), (700, 2048)])
+@pytest.mark.parametrize("kw", [dict(x=True, out=True), dict(e8m0=True, extra=8)])
+def test_norm_widths_of_many_rows(M, H, kw):
+    rng = np.random.default_rng(M * H)
+    kw = dict(kw)
+    x = bf16_values(rng, (M, H)) if kw.pop("x", False) else None
+    check_norm(bf16_values(rng, (M, H), 2.0), bf16(1 + 0.1 * rng.standard_normal(H)).float().numpy(), x, **kw)
+
+
+@pytest.mark.parametrize("M", [3, 400])
+@pytest.mark.parametrize("e8m0", [False, True])
+def test_norm_gains_of_any_size(M, e8m0):
+    """Groups of columns whose scales lie from 2^-112 to 2^104: the quotient by way of a reciprocal
+    has factors of its own at both ends."""
+    rng = np.random.default_rng(50)
+    H = 1280
+    gain = np.repeat(np.exp2([-100.0, -95.0, -90.0, -60.0, 0.0, 60.0, 92.0, 101.0, 110.0, 0.0]), 128)
+    gain = bf16(gain * (1 + 0.1 * rng.standard_normal(H))).float().numpy()
+    check_norm(bf16_values(rng, (M, H), 2.0), gain, e8m0=e8m0, out=True)
+
+
+# ---------------------------------------------------------------- the sublayer
+def test_attention_prompt_rotates_by_positions():
+    """Position encodings by the positions that extend gives, in the prompts and in the steps after them."""
+    rng = np.random.default_rng(51)
+    hidden, heads, hk, D, lens = 256, 4, 2, 64, [33, 1, 20]
+    state = {}
+
+    def rotate(q, k):
+        at = state["pages"].positions[:q.shape[0]].float()
+        angle = at[:, None] * torch.exp2(-torch.arange(D // 2, device=DEV).float() / 4)[None]
+        cos, sin = angle.cos()[:, None], angle.sin()[:, None]
+        for x in (q, k):
+            a, b = x[..., :D // 2].float(), x[..., D // 2:].float()
+            x.copy_(torch.cat([a * cos - b * sin, a * sin + b * cos], -1))
+
+    total = sum(lens)
+    cache, att, prompt, pages = layers(rng, hidden, heads, hk, D, 16, 3, 4, total, rotate=rotate)
+    state["pages"] = pages
+    x = bf16(bf16_values(rng, (total, hidden))).to(DEV)
+    pages.extend(dev(np.array(lens, np.int32)))
+    assert host(pages.positions).tolist() == [i for n in lens for i in range(n)]
+    y = prompt(x, pages.page_table, pages.q_start, pages.lens, max(lens))
+    w, ws = att.weights, workspace(att.workspace.numel())
+    qkv, mixed, want = (torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((total, heads + 2 * hk, D), (total, heads, D), (total, hidden)))
+    m.fp8_linear(x, w["qkv"], w["qkv_s"], qkv.flatten(1), ws)
+    q, k, v = qkv[:, :heads], qkv[:, heads:heads + hk], qkv[:, heads + hk:]
+    plain = k.clone()
+    rotate(q, k)
+    assert not torch.equal(plain, k)
+    m.prompt_attention(q, k, v, pages.q_start, mixed, ws)
+    m.fp8_linear(mixed.flatten(1), w["o"], w["o_s"], want, ws)
+    assert torch.equal(y, want)
+    # the cache holds the rotated keys: half a step of E4M3, 2^-4 of a normal value, 2^-10 scales below 2^-6
+    table, codes, scales = host(pages.page_table), e4m3_decode(host(cache.k)), host(cache.k_scale).astype(np.float64)
+    for b, n in enumerate(lens):
+        lo = int(sum(lens[:b]))
+        for i in range(n):
+            page, at = int(table[b, i // 16]), i % 16
+            held, sc, want_k = codes[page, :, at], scales[page][:, None], host(k[lo + i])
+            assert (np.abs(held * sc - want_k) <= np.maximum(np.abs(want_k) * 2.0 ** -4, sc * 2.0 ** -10)).all()
+    # a step of a token each: the same by single calls, whose queries and keys are rotated by the new positions
+    pages.extend(torch.ones(3, dtype=torch.int32, device=DEV))
+    assert host(pages.positions)[:4].tolist() == [*lens, -1]
+    last = x[:3].contiguous()
+    out = att(last, pages.page_table, pages.q_start, pages.lens)
+    step, attended, got = (torch.empty(s, dtype=torch.bfloat16, device=DEV) for s in ((3, heads + 2 * hk, D), (3, heads, D), (3, hidden)))
+    m.fp8_linear(last, w["qkv"], w["qkv_s"], step.flatten(1), ws)
+    rotate(step[:, :heads], step[:, heads:heads + hk])
+    m.decode_attention(step[:, :heads], cache.k, cache.v, cache.k_scale, cache.v_scale, pages.page_table, pages.q_start, pages.lens, 1,
+                       attended, ws)
+    m.fp8_linear(attended.flatten(1), w["o"], w["o_s"], got, ws)
+    assert torch.equal(out, got)
+    assert (att.status(), prompt.status(), pages.status()) == (m.MOE_OK,) * 3
+
+
+def test_attention_prompt_of_no_tokens():
+    rng = np.random.default_rng(52)
+    cache, att, prompt, pages = layers(rng, 128, 2, 1, 64, 16, 2, 4, 8)
+    pages.extend(torch.zeros(2, dtype=torch.int32, device=DEV))
+    x = torch.zeros((0, 128), dtype=torch.bfloat16, device=DEV)
+    quantised = torch.zeros((0, 128), dtype=torch.uint8, device=DEV), torch.zeros((1, 0), device=DEV)
+    for rows in (x, quantised):
+        assert prompt(rows, pages.page_table, pages.q_start, pages.lens, 1).shape == (0, 128)
+    assert prompt.status() == pages.status() == m.MOE_OK
