@@ -541,9 +541,12 @@ int kv_pages_release(const int32_t *page_table, int width, const int32_t *lens, 
  * in [0, total), or that starts before an earlier one ends, is left out and sets
  * the status word to MOE_ERR_INVALID_ARG.
  * Scores, statistics and sums are fp32 (a capped score is within 2^-20 of itself);
- * the weights are rounded to bf16 for their product with V.  An infinity or a NaN in a row of
- * q makes the row NaN; a NaN in a row's k or v reaches the rows that see it,
- * and no other; what rows outside the prompts hold does not matter.
+ * the weights are rounded to bf16 for their product with V, and are up to 2^8 before
+ * the division by their sum: finite values of v above about 2^120 / n (n tokens seen)
+ * may overflow.  A NaN in a row of q makes the row NaN, and so does an infinity
+ * where softcap is 0 (with a cap its scores are plus or minus the cap, as the
+ * formula says); a NaN in a row's k or v reaches the rows that see it, and no
+ * other; what rows outside the prompts hold does not matter.
  * One kernel; results do not depend on the order in which CTAs finish, and a
  * row's, to the last bit, on no other head or row than those that it sees.
  *
