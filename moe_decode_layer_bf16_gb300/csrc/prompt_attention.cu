@@ -5,9 +5,9 @@
 //
 // What bounds it: the two products, 4 D flops for each visible pair of a row and a key,
 // on the tensor cores; beside them an exponential for each pair.  Measured: one prompt of
-// 8192 tokens, 56 heads of 128 on 8, 962 GFLOP, 617 to 671 us by the power cap's clock
-// (1.43 to 1.56 PFLOP/s, 0.72 to 0.78 of the library product's burst rate; tensor pipe 65%
-// busy); 16 prompts of 20 to 2048 tokens 154 us (1.0 PFLOP/s); 33 tokens 8.9 us.
+// 8192 tokens, 56 heads of 128 on 8, 962 GFLOP, 617 to 672 us by the power cap's clock
+// (1.43 to 1.56 PFLOP/s, 0.72 to 0.78 of the library product's burst rate; tensor pipe 63%
+// busy); 16 prompts of 20 to 2048 tokens 154 us (1.0 PFLOP/s); 33 tokens 9.1 us.
 //
 // Rows.  The query heads of a key/value head see the same keys, so their rows are packed
 // token by token: row r of a prompt and kv head is token r / G, head r % G.  An item is
@@ -26,10 +26,10 @@
 // While one tile's softmax runs, the tensor cores work on the other tile.  The running
 // maximum m of a row is moved, and its O and sum rescaled, only when it grows by more than
 // 2^8 (a known refinement of the softmax in one pass): until then the weights are up to 2^8,
-// with the same relative precision, and a row's two warps need no word of each other but a vote.  (With a row a thread, 12 warps in all,
-// the serving mix takes 180 us and the long prompt as long as now; with four more warps that
-// write the results while the next item begins 180, because they take registers and issue
-// slots from the softmax.)
+// with the same relative precision, and a row's two warps need no word of each other but a
+// vote.  (With a row a thread, 12 warps in all, the serving mix took 180 us and the long prompt
+// as long as now; with four more warps that write the results while the next item begins 180,
+// because they take registers and issue slots from the softmax.)
 //
 // What a masked position holds must not matter, but 0 x NaN is NaN: values of tiles
 // that some row does not see in full (the diagonal, a window's edge, a prompt's end) are
@@ -222,12 +222,6 @@ MOE_DEV void fma2(float& x, float& y, float u, float v, float d) {
       " fma.rn.f32x2 a, a, b, e;\n mov.b64 {%0, %1}, a;\n}"
       : "+f"(x), "+f"(y)
       : "f"(u), "f"(v), "f"(d));
-}
-MOE_DEV void fma2(float& x, float& y, float u, float v, float d, float e) {
-  asm("{\n .reg .b64 a, b, e;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n mov.b64 e, {%4, %5};\n"
-      " fma.rn.f32x2 a, a, b, e;\n mov.b64 {%0, %1}, a;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(u), "f"(v), "f"(d), "f"(e));
 }
 // (x, y) += (u, v) * c
 MOE_DEV void bias2(float& x, float& y, float u, float v, float c) {
